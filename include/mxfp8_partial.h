@@ -450,6 +450,136 @@ MXFP8_API int nvfp4_partial_cast(const mxfp8_tensor* input, const mxfp8_tensor* 
                        mxfp8_tensor* output_rowwise, mxfp8_tensor* output_colwise, int64_t rows,
                        int64_t cols, int64_t start_offset, int64_t out_offset, void* stream);
 
+/*
+ * Training operators around the MXFP8 weights: 8-bit activation checkpoints, the
+ * block-scaled matrix product that reads them and the cast's outputs, and layer norm.
+ * (No counterpart in the source pages, which end at the weights.)
+ *
+ * Conventions of these entry points, besides the ones at the top of this file:
+ * - A matrix argument is 2-D [>= rows][>= cols] with row stride shape[1] (a padded or a
+ *   larger buffer's rows), or 1-D and dense.  A vector argument has numel >= its length.
+ * - Scales in the GEMM layout: the 128x4-tile layout of mxfp8_swizzle_scales, at least
+ *   mxfp8_swizzled_scales_size bytes, 16-byte aligned.
+ * - Outputs must not overlap inputs, unless an argument says so.
+ * - A call with no elements to write returns 0 and launches nothing.
+ */
+
+/*
+ * 8-bit activation checkpoint: E4M3 codes of an activation (or of a gradient) with one E8M0
+ * scale per 128 values, along its rows and/or along its columns, from one read of the input.
+ * The scale convention is the one at the top of this file with blocks of 128 (the last block
+ * of a row or column may be shorter) and without the rounding through BF16:
+ * code = E4M3(x * 2^-e), one rounding.  A block that holds a NaN or an infinity has the scale
+ * byte 0xFF and NaN codes.
+ *
+ * input          [in]  F32 or BF16 matrix rows x cols.
+ * codes_rowwise  [out] OPTIONAL U8 matrix rows x cols, in blocks of 1x128.
+ * scale_rowwise  [out] required iff codes_rowwise: its scale grid [rows][ceil(cols/128)] in the
+ *                      GEMM layout (transpose 0), padding entries written as zeros.
+ * codes_colwise  [out] OPTIONAL U8 matrix rows x cols (not transposed), in blocks of 128x1.
+ * scale_colwise  [out] required iff codes_colwise: its scale grid [ceil(rows/128)][cols] in the
+ *                      GEMM layout with transpose 1, padding entries written as zeros.
+ * Errors: 1 bad sizes or a scale buffer that is not 16-byte aligned; 2 a buffer too small;
+ * 3 dtype; 4 a missing input or scale buffer, or neither direction present.
+ */
+MXFP8_API int mxfp8_checkpoint_save(const mxfp8_tensor* input, mxfp8_tensor* codes_rowwise,
+                          mxfp8_tensor* scale_rowwise, mxfp8_tensor* codes_colwise,
+                          mxfp8_tensor* scale_colwise, int64_t rows, int64_t cols, void* stream);
+
+/*
+ * The values that one copy of a checkpoint stands for: output = decode(code) * 2^(s - 127).
+ *
+ * codes   [in]  U8 matrix rows x cols;  scale [in] its scales as mxfp8_checkpoint_save wrote
+ *               them;  colwise 1 for the columnwise copy, 0 for the rowwise one.
+ * output  [out] F32 or BF16 matrix rows x cols (exact in both, BF16 subnormals rounded to
+ *               nearest-even).  Errors as above; 1 also for another colwise.
+ */
+MXFP8_API int mxfp8_checkpoint_restore(const mxfp8_tensor* codes, const mxfp8_tensor* scale,
+                             mxfp8_tensor* output, int64_t rows, int64_t cols, int32_t colwise,
+                             void* stream);
+
+/*
+ * Matrix product of two block-scaled 8-bit operands,
+ *   out[i][j] = sum_p A(i, p) * B(j, p) (+ addend[i][j]),   i < m, j < n, p < k,
+ * A(i, p) = decode(code) * 2^(s - 127), s the scale of the block of p; likewise B.  Products
+ * are exact and summed in F32; the addend joins in F32 and the result is rounded once.
+ *
+ * a, b               [in] U8 E4M3 codes.  Rowwise (colwise flag 0): the matrix m x k (n x k), the
+ *                         contraction along its rows.  Columnwise (flag 1): the matrix k x m
+ *                         (k x n), the contraction along its columns -- the columnwise copy of
+ *                         a checkpoint or of a weight, read as it lies.
+ * a_scale, b_scale   [in] the operand's scales in the GEMM layout, logical grid
+ *                         [m][ceil(k/block)] ([n][...]): transpose 0 of a rowwise grid,
+ *                         transpose 1 of a columnwise one.  Padding entries must not be 0xFF.
+ * a_block, b_block        values per scale along the contraction: 128 (checkpoints) or 32
+ *                         (weights of mxfp8_partial_cast).
+ * addend             [in] OPTIONAL F32 matrix m x n; may be the same matrix as an F32 out (the
+ *                         product is then added to it).
+ * out               [out] F32 or BF16 matrix m x n.
+ * With y = x W^T, W [outs][ins]: output y: a = x rowwise, b = W rowwise; input gradient
+ * dx = dy W: a = dy rowwise, b = W columnwise; weight gradient dW = dy^T x: a = dy columnwise,
+ * b = x columnwise.  k may be 0 (operands and scales may then be empty): out = addend or 0.
+ * Operands whose base and row stride are multiples of 16 bytes are fetched by TMA; others
+ * run a slower kernel.
+ * Results do not depend on the run: no atomics, one fixed order of sums per shape.
+ * Errors: 1 bad sizes (m, n, k <= 2^31 - 1024), flags or blocks, unaligned scales, or an addend
+ * that overlaps out without being the same matrix; 2 a buffer too small; 3 dtype; 4 missing.
+ */
+MXFP8_API int mxfp8_gemm(const mxfp8_tensor* a, const mxfp8_tensor* a_scale, const mxfp8_tensor* b,
+               const mxfp8_tensor* b_scale, const mxfp8_tensor* addend, mxfp8_tensor* out, int64_t m,
+               int64_t n, int64_t k, int32_t a_colwise, int32_t b_colwise, int32_t a_block,
+               int32_t b_block, void* stream);
+
+/*
+ * Health of the products: waits for `stream`, then returns 0, or MXFP8_ERR_CUDA when a product
+ * on the current device gave up a wait on its own copies or tensor-core work since the last
+ * call (each wait inside the kernels ends after about two seconds; the outputs of such a
+ * product are invalid).  Not for use during stream capture.
+ */
+MXFP8_API int mxfp8_gemm_status(void* stream);
+
+/*
+ * Layer norm of each row: output = (x - mean) * rstd * weight + bias, mean and rstd =
+ * 1 / sqrt(var + eps) over the row's cols values (var: the mean squared deviation), in F32,
+ * rounded once.
+ *
+ * input   [in]  F32 or BF16 matrix rows x cols;  output [out] same dtype; may be the input.
+ * weight  [in]  F32 or BF16 vector of cols;  bias [in] OPTIONAL, weight's dtype.
+ * mean, rstd [out] F32 vectors of rows.
+ * Errors: 1 bad sizes (cols <= 2^31 - 1024) or eps < 0 or NaN; 2 too small; 3 dtype; 4 missing.
+ */
+MXFP8_API int mxfp8_layer_norm_forward(const mxfp8_tensor* input, const mxfp8_tensor* weight,
+                             const mxfp8_tensor* bias, mxfp8_tensor* output, mxfp8_tensor* mean,
+                             mxfp8_tensor* rstd, int64_t rows, int64_t cols, float eps, void* stream);
+
+/*
+ * Gradients of layer norm.  With xh = (x - mean) * rstd and g = grad_output * weight:
+ *   grad_input  = rstd * (g - mean_cols(g) - xh * mean_cols(g * xh))
+ *   grad_weight = sum_rows grad_output * xh,   grad_bias = sum_rows grad_output.
+ *
+ * grad_output [in]  F32 or BF16 matrix rows x cols.
+ * input       [in]  the forward pass's input: the dtype of grad_output, or U8: the rowwise copy of
+ *                   its checkpoint, with input_scale its scales (input_scale is empty otherwise).
+ * weight      [in]  F32 or BF16 vector;  mean, rstd [in] F32, as the forward pass left them.
+ * grad_input  [out] dtype of grad_output; may be grad_output itself.
+ * grad_weight [out] F32 vector of cols;  grad_bias [out] OPTIONAL F32 vector of cols.
+ * workspace   [out] at least mxfp8_layer_norm_workspace_size(rows, cols) bytes (U8), 16-byte
+ *                   aligned; its contents before the call do not matter and after it mean
+ *                   nothing.  Calls that overlap on the GPU need workspaces of their own.
+ * The sums over rows have one fixed order for a shape: results do not depend on the run.
+ * rows == 0: the gradients of weight and bias are set to zero.
+ * Errors: 1 bad sizes, unaligned scales or workspace; 2 too small; 3 dtype; 4 missing.
+ */
+MXFP8_API int mxfp8_layer_norm_backward(const mxfp8_tensor* grad_output, const mxfp8_tensor* input,
+                              const mxfp8_tensor* input_scale, const mxfp8_tensor* weight,
+                              const mxfp8_tensor* mean, const mxfp8_tensor* rstd,
+                              mxfp8_tensor* grad_input, mxfp8_tensor* grad_weight,
+                              mxfp8_tensor* grad_bias, mxfp8_tensor* workspace, int64_t rows,
+                              int64_t cols, void* stream);
+
+/* Bytes of workspace of mxfp8_layer_norm_backward on any device (-1 for bad sizes). */
+MXFP8_API int64_t mxfp8_layer_norm_workspace_size(int64_t rows, int64_t cols);
+
 /* Message describing the calling thread's most recent non-zero status ("" if none). */
 MXFP8_API const char* mxfp8_last_error(void);
 

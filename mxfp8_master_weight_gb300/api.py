@@ -404,7 +404,8 @@ class Prepared:
         if job_array is not None:  # batched entry: (job array, count)
             self.args = (job_array, int(scalars[0]))
         else:
-            self.args = tuple(ctypes.byref(h) for h in handles) + tuple(int(v) for v in scalars)
+            self.args = tuple(ctypes.byref(h) for h in handles) + tuple(
+                v if isinstance(v, float) else int(v) for v in scalars)
         self.tensors = tensors
         self.device = _device_of(*tensors)
 
@@ -487,6 +488,151 @@ def prepare_partial_cast_batched(jobs) -> Prepared:
 def prepare_quantize_whole_blocks_batched(jobs) -> Prepared:
     arr, keep = _quantize_jobs(jobs)
     return Prepared("mxfp8_quantize_whole_blocks_batched", [arr], (len(jobs),), keep, job_array=arr)
+
+
+# ---------------------------------------------------------------- training operators
+def matrix_handle(t: torch.Tensor | None, name: str) -> Tensor:
+    """mxfp8_tensor of a matrix argument: 2-D with unit stride along its rows (a slice of a
+    wider buffer keeps that buffer's row stride), or 1-D and dense."""
+    if t is None or t.numel() == 0:
+        return _capi.empty_tensor()
+    if t.dim() != 2 or t.is_contiguous():
+        return handle(t, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor, got device {t.device}")
+    if t.dtype not in _DTYPES:
+        raise MXFP8Error(3, f"{name}: unsupported dtype {t.dtype}")
+    rows, cols = t.shape
+    stride = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or stride < cols:
+        raise MXFP8Error(5, f"{name}: rows must be contiguous and must not overlap")
+    h = Tensor(ctypes.c_void_p(t.data_ptr()), _DTYPES[t.dtype], 2, (ctypes.c_int64 * 2)(rows, stride))
+    h.cols = cols  # the row stride may be wider than the view
+    return h
+
+
+def _matrix(t, name, rows, cols):
+    h = matrix_handle(t, name)
+    width = getattr(h, "cols", None)
+    if width is not None and width < cols:
+        raise MXFP8Error(2, f"{name}: shape [{t.shape[0]}, {width}] smaller than [{rows}, {cols}]")
+    return h
+
+
+def _checkpoint_save_args(input, codes_rowwise, scale_rowwise, codes_colwise, scale_colwise, rows, cols):
+    return [_matrix(input, "input", rows, cols), _matrix(codes_rowwise, "codes_rowwise", rows, cols),
+            handle(scale_rowwise, "scale_rowwise"), _matrix(codes_colwise, "codes_colwise", rows, cols),
+            handle(scale_colwise, "scale_colwise")]
+
+
+def mxfp8_checkpoint_save(input, codes_rowwise, scale_rowwise, codes_colwise, scale_colwise, rows: int,
+                          cols: int, stream=None) -> None:
+    """8-bit checkpoint of an activation: E4M3 codes and one E8M0 scale per 128 values, along
+    the rows and/or along the columns (None omits a direction); scales in the GEMM layout."""
+    hs = _checkpoint_save_args(input, codes_rowwise, scale_rowwise, codes_colwise, scale_colwise, rows, cols)
+    _call("mxfp8_checkpoint_save", _device_of(input, codes_rowwise, codes_colwise),
+          *[ctypes.byref(h) for h in hs], int(rows), int(cols), _stream(stream, input))
+
+
+def prepare_checkpoint_save(input, codes_rowwise, scale_rowwise, codes_colwise, scale_colwise, rows, cols) -> Prepared:
+    ts = (input, codes_rowwise, scale_rowwise, codes_colwise, scale_colwise)
+    return Prepared("mxfp8_checkpoint_save", _checkpoint_save_args(*ts, rows, cols), (rows, cols),
+                    [t for t in ts if t is not None])
+
+
+def _checkpoint_restore_args(codes, scale, output, rows, cols):
+    return [_matrix(codes, "codes", rows, cols), handle(scale, "scale"), _matrix(output, "output", rows, cols)]
+
+
+def mxfp8_checkpoint_restore(codes, scale, output, rows: int, cols: int, colwise: bool = False,
+                             stream=None) -> None:
+    """The values one copy of a checkpoint stands for, in F32 or BF16 (exact in both)."""
+    hs = _checkpoint_restore_args(codes, scale, output, rows, cols)
+    _call("mxfp8_checkpoint_restore", _device_of(codes, output), *[ctypes.byref(h) for h in hs], int(rows),
+          int(cols), int(bool(colwise)), _stream(stream, output))
+
+
+def prepare_checkpoint_restore(codes, scale, output, rows, cols, colwise=False) -> Prepared:
+    return Prepared("mxfp8_checkpoint_restore", _checkpoint_restore_args(codes, scale, output, rows, cols),
+                    (rows, cols, bool(colwise)), [codes, scale, output])
+
+
+def _gemm_args(a, a_scale, b, b_scale, addend, out, m, n, k, a_colwise, b_colwise):
+    return [_matrix(a, "a", *((k, m) if a_colwise else (m, k))), handle(a_scale, "a_scale"),
+            _matrix(b, "b", *((k, n) if b_colwise else (n, k))), handle(b_scale, "b_scale"),
+            _matrix(addend, "addend", m, n), _matrix(out, "out", m, n)]
+
+
+def mxfp8_gemm(a, a_scale, b, b_scale, addend, out, m: int, n: int, k: int, a_colwise: bool = False,
+               b_colwise: bool = False, a_block: int = 128, b_block: int = 128, stream=None) -> None:
+    """out = A B^T (+ addend) of block-scaled 8-bit operands: A m x k and B n x k, each stored
+    with k along its rows, or (``*_colwise``) along its columns.  ``*_block``: values per scale along k (128
+    for checkpoints, 32 for the weights of mxfp8_partial_cast); scales in the GEMM layout."""
+    hs = _gemm_args(a, a_scale, b, b_scale, addend, out, m, n, k, a_colwise, b_colwise)
+    _call("mxfp8_gemm", _device_of(out, a, b), *[ctypes.byref(h) for h in hs], int(m), int(n), int(k),
+          int(bool(a_colwise)), int(bool(b_colwise)), int(a_block), int(b_block), _stream(stream, out))
+
+
+def prepare_gemm(a, a_scale, b, b_scale, addend, out, m, n, k, a_colwise=False, b_colwise=False, a_block=128,
+                 b_block=128) -> Prepared:
+    hs = _gemm_args(a, a_scale, b, b_scale, addend, out, m, n, k, a_colwise, b_colwise)
+    return Prepared("mxfp8_gemm", hs, (m, n, k, bool(a_colwise), bool(b_colwise), a_block, b_block),
+                    [t for t in (out, a, a_scale, b, b_scale, addend) if t is not None])
+
+
+def mxfp8_gemm_status(device=None, stream=None) -> None:
+    """Waits for the stream; raises when a product gave up a wait since the last call."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    _call("mxfp8_gemm_status", dev, _stream(torch.cuda.current_stream(dev) if stream is None else stream, None))
+
+
+def _layer_norm_forward_args(input, weight, bias, output, mean, rstd, rows, cols):
+    return [_matrix(input, "input", rows, cols), handle(weight, "weight"), handle(bias, "bias"),
+            _matrix(output, "output", rows, cols), handle(mean, "mean"), handle(rstd, "rstd")]
+
+
+def mxfp8_layer_norm_forward(input, weight, bias, output, mean, rstd, rows: int, cols: int, eps: float = 1e-5,
+                             stream=None) -> None:
+    """Layer norm of each row; ``bias`` may be None.  Leaves the F32 statistics for the backward pass."""
+    hs = _layer_norm_forward_args(input, weight, bias, output, mean, rstd, rows, cols)
+    _call("mxfp8_layer_norm_forward", _device_of(input, output), *[ctypes.byref(h) for h in hs], int(rows),
+          int(cols), float(eps), _stream(stream, input))
+
+
+def prepare_layer_norm_forward(input, weight, bias, output, mean, rstd, rows, cols, eps=1e-5) -> Prepared:
+    ts = (input, weight, bias, output, mean, rstd)
+    return Prepared("mxfp8_layer_norm_forward", _layer_norm_forward_args(*ts, rows, cols), (rows, cols, float(eps)),
+                    [t for t in ts if t is not None])
+
+
+def mxfp8_layer_norm_workspace_size(rows: int, cols: int) -> int:
+    """Bytes of workspace of mxfp8_layer_norm_backward."""
+    return int(_capi.load().mxfp8_layer_norm_workspace_size(int(rows), int(cols)))
+
+
+def _layer_norm_backward_args(grad_output, input, input_scale, weight, mean, rstd, grad_input, grad_weight,
+                              grad_bias, workspace, rows, cols):
+    return [_matrix(grad_output, "grad_output", rows, cols), _matrix(input, "input", rows, cols),
+            handle(input_scale, "input_scale"), handle(weight, "weight"), handle(mean, "mean"),
+            handle(rstd, "rstd"), _matrix(grad_input, "grad_input", rows, cols),
+            handle(grad_weight, "grad_weight"), handle(grad_bias, "grad_bias"), handle(workspace, "workspace")]
+
+
+def mxfp8_layer_norm_backward(grad_output, input, input_scale, weight, mean, rstd, grad_input, grad_weight,
+                              grad_bias, workspace, rows: int, cols: int, stream=None) -> None:
+    """Layer norm's gradients.  ``input``: the forward pass's input, or the codes of its rowwise
+    checkpoint with ``input_scale`` their scales (else None).  ``grad_bias`` may be None."""
+    ts = (grad_output, input, input_scale, weight, mean, rstd, grad_input, grad_weight, grad_bias, workspace)
+    hs = _layer_norm_backward_args(*ts, rows, cols)
+    _call("mxfp8_layer_norm_backward", _device_of(grad_output, grad_weight), *[ctypes.byref(h) for h in hs],
+          int(rows), int(cols), _stream(stream, grad_weight))
+
+
+def prepare_layer_norm_backward(grad_output, input, input_scale, weight, mean, rstd, grad_input, grad_weight,
+                                grad_bias, workspace, rows, cols) -> Prepared:
+    ts = (grad_output, input, input_scale, weight, mean, rstd, grad_input, grad_weight, grad_bias, workspace)
+    return Prepared("mxfp8_layer_norm_backward", _layer_norm_backward_args(*ts, rows, cols), (rows, cols),
+                    [t for t in ts if t is not None])
 
 
 def block_shapes(rows: int, cols: int):

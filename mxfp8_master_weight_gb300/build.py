@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 UNITS = ["capi.cu", "amax.cu", "cast_f32.cu", "cast_bf16.cu", "cast_f32_unaligned.cu",
          "cast_bf16_unaligned.cu", "cast_bf16_unaligned_f16.cu", "fused_f32.cu", "fused_bf16.cu",
-         "misc.cu", "noalloc.cu", "nvfp4.cu"]
+         "misc.cu", "noalloc.cu", "nvfp4.cu", "linear_capi.cu", "checkpoint.cu", "gemm.cu", "norm.cu"]
 
 
 def _nvcc() -> str:
@@ -64,17 +64,20 @@ def source_digest() -> str:
 
 # Translation units that hold host code only (argument validation, dispatch, the
 # allocation-free entry point's set-up): edits there leave every kernel unchanged.
-HOST_ONLY_UNITS = ("capi.cu", "noalloc.cu")
+HOST_ONLY_UNITS = ("capi.cu", "noalloc.cu", "checks.h", "linear_capi.cu")
+
+# Sources of the training operators: none of the cast's kernels is made from them.
+OPERATOR_UNITS = ("linear.h", "checkpoint.cu", "gemm.cu", "gemm_impl.cuh", "norm.cu", "tensor_core.cuh")
 
 
 def kernel_digest() -> str:
-    """SHA-256 over the code of the device-side sources only (every csrc file except the
-    host-only units, comments excluded): the key of recorded per-kernel counters, which
-    a host-side edit does not invalidate."""
+    """SHA-256 over the code of the cast's device-side sources only (every csrc file except
+    the host-only units and the training operators', comments excluded): the key of
+    recorded per-kernel counters, which a host-side edit does not invalidate."""
     h = hashlib.sha256()
     for f in _sources():
         name = os.path.basename(f)
-        if name in HOST_ONLY_UNITS or not f.startswith(CSRC):
+        if name in HOST_ONLY_UNITS + OPERATOR_UNITS or not f.startswith(CSRC):
             continue
         h.update(name.encode())
         with open(f, encoding="utf-8") as fh:

@@ -10,21 +10,13 @@
 
 #include <cuda_runtime.h>
 
+#include "checks.h"
 #include "kernels.h"
 #include "mxfp8_partial.h"
 
-namespace {
+namespace mxfp8 {
 
-using mxfp8::AmaxParams;
-using mxfp8::CastParams;
-using mxfp8::DeviceInfo;
-using mxfp8::FragGeom;
-using mxfp8::FusedParams;
-using mxfp8::ReduceScaleSegment;
-using mxfp8::ScaleSegment;
-using mxfp8::SwizzleParams;
-
-thread_local char g_err[512] = {0};
+static thread_local char g_err[512] = {0};
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -39,53 +31,50 @@ int ok() {
   return MXFP8_OK;
 }
 
-int64_t elem_bytes(int32_t dtype) {
-  switch (dtype) {
-    case MXFP8_DTYPE_F32: return 4;
-    case MXFP8_DTYPE_BF16: return 2;
-    case MXFP8_DTYPE_U8: return 1;
-    default: return 0;
+constexpr int kMaxDevices = 64;
+static std::atomic<int> g_sms[kMaxDevices];
+
+int device_info(DeviceInfo* d) {
+  cudaError_t e = cudaGetDevice(&d->device);
+  if (e != cudaSuccess) return fail(MXFP8_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  int sms = d->device < kMaxDevices ? g_sms[d->device].load() : 0;
+  if (sms == 0) {
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d->device);
+    if (e != cudaSuccess) return fail(MXFP8_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(e));
+    if (d->device < kMaxDevices) g_sms[d->device].store(sms);
   }
-}
-
-int64_t numel(const mxfp8_tensor* t) {
-  if (t->ndim == 1) return t->shape[0];
-  return t->shape[0] * t->shape[1];
-}
-
-// Empty handle: absent pointer, NULL data, or a zero extent (section "Changes":
-// omission is expressed by an empty tensor handle).
-bool is_empty(const mxfp8_tensor* t) {
-  if (t == nullptr || t->data == nullptr) return true;
-  if (t->ndim == 1) return t->shape[0] == 0;
-  return t->shape[0] == 0 || t->shape[1] == 0;
-}
-
-// Structural checks of a present tensor: ndim, non-negative shape, known dtype,
-// element alignment.
-int check_tensor(const mxfp8_tensor* t, const char* name) {
-  if (t->ndim != 1 && t->ndim != 2) return fail(MXFP8_ERR_INVALID, "%s: ndim must be 1 or 2", name);
-  if (t->shape[0] < 0 || (t->ndim == 2 && t->shape[1] < 0))
-    return fail(MXFP8_ERR_INVALID, "%s: negative shape", name);
-  if (t->ndim == 2 && t->shape[1] > 0 && t->shape[0] > INT64_MAX / t->shape[1])
-    return fail(MXFP8_ERR_INVALID, "%s: shape overflows int64", name);
-  const int64_t eb = elem_bytes(t->dtype);
-  if (eb == 0) return fail(MXFP8_ERR_DTYPE, "%s: unknown dtype %d", name, int(t->dtype));
-  if (reinterpret_cast<uintptr_t>(t->data) % uintptr_t(eb) != 0)
-    return fail(MXFP8_ERR_INVALID, "%s: data pointer not aligned to its element size", name);
+  d->sms = sms;
   return MXFP8_OK;
 }
 
-// A 2-D block grid tensor of at least [r][c] (padding allowed, row stride = shape[1]).
-int check_grid(const mxfp8_tensor* t, const char* name, int64_t r, int64_t c, int32_t dtype) {
-  if (int rc = check_tensor(t, name)) return rc;
-  if (t->dtype != dtype) return fail(MXFP8_ERR_DTYPE, "%s: wrong dtype %d (want %d)", name, int(t->dtype), int(dtype));
-  if (t->ndim != 2) return fail(MXFP8_ERR_SHAPE, "%s: must be 2-D", name);
-  if (t->shape[0] < r || t->shape[1] < c)
-    return fail(MXFP8_ERR_SHAPE, "%s: shape [%lld, %lld] smaller than block grid [%lld, %lld]", name,
-                (long long)t->shape[0], (long long)t->shape[1], (long long)r, (long long)c);
-  return MXFP8_OK;
+int cuda_status(cudaError_t e, const char* what) {
+  if (e != cudaSuccess) return fail(MXFP8_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return ok();
 }
+
+}  // namespace mxfp8
+
+namespace {
+
+using mxfp8::check_grid;
+using mxfp8::check_tensor;
+using mxfp8::cuda_status;
+using mxfp8::device_info;
+using mxfp8::elem_bytes;
+using mxfp8::fail;
+using mxfp8::g_err;
+using mxfp8::is_empty;
+using mxfp8::numel;
+using mxfp8::ok;
+
+using mxfp8::AmaxParams;
+using mxfp8::CastParams;
+using mxfp8::DeviceInfo;
+using mxfp8::FragGeom;
+using mxfp8::FusedParams;
+using mxfp8::ReduceScaleSegment;
+using mxfp8::ScaleSegment;
+using mxfp8::SwizzleParams;
 
 // Weight size limits: byte offsets of every element stay far inside int64 and a band's
 // warp-tile count, ceil(cols / tile width), fits the 32-bit count the kernels keep.
@@ -107,27 +96,6 @@ int check_dims(int64_t rows, int64_t cols, int64_t start, int64_t len) {
     return fail(MXFP8_ERR_INVALID, "fragment [%lld, %lld) exceeds rows*cols = %lld", (long long)start,
                 (long long)(start + len), (long long)(rows * cols));
   return MXFP8_OK;
-}
-
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_sms[kMaxDevices];
-
-int device_info(DeviceInfo* d) {
-  cudaError_t e = cudaGetDevice(&d->device);
-  if (e != cudaSuccess) return fail(MXFP8_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
-  int sms = d->device < kMaxDevices ? g_sms[d->device].load() : 0;
-  if (sms == 0) {
-    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d->device);
-    if (e != cudaSuccess) return fail(MXFP8_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(e));
-    if (d->device < kMaxDevices) g_sms[d->device].store(sms);
-  }
-  d->sms = sms;
-  return MXFP8_OK;
-}
-
-int cuda_status(cudaError_t e, const char* what) {
-  if (e != cudaSuccess) return fail(MXFP8_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-  return ok();
 }
 
 // Fragment geometry and the warp tiles (32 rows x tw columns) that cover it.

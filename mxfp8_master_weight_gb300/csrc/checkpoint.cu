@@ -1,0 +1,273 @@
+// 8-bit activation checkpoints: E4M3 codes with one E8M0 scale per 128 values, along the rows
+// and along the columns of an activation, from one read; and the values a copy stands for.
+//
+//   e = floor(log2(max |x| of the block)) - 8 (clamped at -127),  code = E4M3(x * 2^-e),
+//   restored = decode(code) * 2^e
+//
+// The multiplication by a power of two is exact, so a code carries one rounding (nearest-even,
+// saturating at 448: a block maximum in [448, 512) * 2^e becomes 448 * 2^e).
+//
+// Both kernels are streaming passes bound by HBM: save moves 4 (BF16) or 6 (F32) bytes per
+// element and two directions, restore 3 or 5.  A block of 256 threads owns one 128x128 tile --
+// the smallest piece that holds whole blocks of both directions -- in registers: thread t has
+// columns 8 (t % 16) .. + 7 of rows t / 16 + 16 p, p < 8, so a row's maximum is a butterfly over
+// 16 lanes, a column's one shuffle and a pass through shared memory, and every code row leaves
+// as 128 contiguous bytes.
+#include "common.cuh"
+#include "linear.h"
+
+namespace mxfp8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = kCkptBlock;
+constexpr int kPasses = 8;   // rows per thread
+constexpr int kRowStep = 16; // rows between a thread's passes
+
+// Byte of entry (r, b) of a logical scale grid with `tcols` 128x4 tiles per 128 rows.
+__device__ __forceinline__ int64_t scale_byte(int64_t r, int64_t b, int64_t tcols) {
+  return ((r >> 7) * tcols + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
+}
+
+// Stores the scale of row r of the tile's block b; the row's last block also zeroes the
+// padding entries up to a whole group of four.
+__device__ __forceinline__ void store_scale(uint8_t* s, int64_t r, int64_t b, int64_t nblocks, uint32_t byte) {
+  uint8_t* p = s + scale_byte(r, b, scale_tile_cols(nblocks));
+  *p = static_cast<uint8_t>(byte);
+  if (b == nblocks - 1) {
+    for (int64_t i = (b & 3) + 1; i < 4; ++i) *++p = 0;
+  }
+}
+
+// Eight consecutive elements as 32-bit words: BF16 pairs or F32 values.
+template <class T>
+struct Eight {
+  static constexpr int W = T::kBytes * 2;
+  uint32_t w[W];
+  __device__ __forceinline__ float get(int k) const {
+    if constexpr (T::kBytes == 4) {
+      return __uint_as_float(w[k]);
+    } else {
+      return (k & 1) ? bf16_hi(w[k >> 1]) : bf16_lo(w[k >> 1]);
+    }
+  }
+};
+
+// Elements [0, n) of p, zeros past them.
+template <class T>
+__device__ __forceinline__ Eight<T> load_eight(const char* p, int n, bool vec) {
+  Eight<T> v;
+  if (vec && n >= 8) {
+#pragma unroll
+    for (int i = 0; i < Eight<T>::W; i += 4) {
+      const uint4 c = ld_stream16(p + 4 * i);
+      v.w[i] = c.x; v.w[i + 1] = c.y; v.w[i + 2] = c.z; v.w[i + 3] = c.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < Eight<T>::W; ++i) v.w[i] = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k < n) {
+        const uint32_t b = load_bits<T>(p, k);
+        if constexpr (T::kBytes == 4) v.w[k] = b; else v.w[k >> 1] |= b << (16 * (k & 1));
+      }
+    }
+  }
+  return v;
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* p, uint2 q, int n, bool vec) {
+  if (vec && n >= 8) {
+    *reinterpret_cast<uint2*>(p) = q;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) p[k] = static_cast<uint8_t>((k < 4 ? q.x : q.y) >> (8 * (k & 3)));
+  }
+}
+
+template <class T>
+__device__ __forceinline__ uint2 encode(const Eight<T>& v, const float (&mult)[8]) {
+  float p[8];
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) mul2_rn(v.get(k), v.get(k + 1), mult[k], mult[k + 1], p[k], p[k + 1]);
+  return make_uint2(e4m3x2_rn_sat(p[0], p[1]) | (e4m3x2_rn_sat(p[2], p[3]) << 16),
+                    e4m3x2_rn_sat(p[4], p[5]) | (e4m3x2_rn_sat(p[6], p[7]) << 16));
+}
+
+template <class T, bool kRow, bool kCol>
+__global__ void __launch_bounds__(kThreads) k_checkpoint_save(const __grid_constant__ CheckpointSaveParams p) {
+  __shared__ uint32_t s_max[kThreads / 32][kTile];  // per warp: column maxima of |x| (F32 bits)
+  __shared__ float s_mult[kTile];
+  grid_dependency_sync();
+  const int64_t tcols = (p.cols + kTile - 1) / kTile;
+  const int64_t rb = blockIdx.x / tcols, cb = blockIdx.x % tcols;
+  const int t = threadIdx.x, c8 = t % 16 * 8, r0 = t / 16;
+  const int64_t col = cb * kTile + c8;
+  const int n = int(p.cols - col < 8 ? (p.cols > col ? p.cols - col : 0) : 8);
+  Eight<T> v[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int64_t r = rb * kTile + r0 + kRowStep * i;
+    v[i] = load_eight<T>(static_cast<const char*>(p.in) + (r * p.ld + col) * T::kBytes, r < p.rows ? n : 0, p.vec_in);
+  }
+  uint32_t cm[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // column maxima over this thread's rows
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t a = __float_as_uint(v[i].get(k)) & 0x7fffffffu;
+      m = max(m, a);
+      if constexpr (kCol) cm[k] = max(cm[k], a);
+    }
+    if constexpr (kRow) {
+#pragma unroll
+      for (int off = 1; off < 16; off <<= 1) m = max(m, __shfl_xor_sync(kFullMask, m, off));
+      const uint32_t s = e8m0_from_bits<F32T>(m);
+      const int64_t r = rb * kTile + r0 + kRowStep * i;
+      if (c8 == 0) store_scale(p.s_r, r, cb, tcols, s);  // rows past the last: padding, s = 0
+      const float f = scale_multiplier(s);
+      const float mult[8] = {f, f, f, f, f, f, f, f};
+      if (r < p.rows) store_codes(p.q_r + r * p.ld_r + col, encode<T>(v[i], mult), n, p.vec_r);
+    }
+  }
+  if constexpr (kCol) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) cm[k] = max(cm[k], __shfl_xor_sync(kFullMask, cm[k], 16));
+    if (t % 32 < 16) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s_max[t / 32][c8 + k] = cm[k];
+    }
+    __syncthreads();
+    if (t < kTile) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) m = max(m, s_max[w][t]);
+      const uint32_t s = e8m0_from_bits<F32T>(m);
+      s_mult[t] = scale_multiplier(s);
+      store_scale(p.s_c, cb * kTile + t, rb, (p.rows + kTile - 1) / kTile, s);
+    }
+    __syncthreads();
+    float mult[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mult[k] = s_mult[c8 + k];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int64_t r = rb * kTile + r0 + kRowStep * i;
+      if (r < p.rows) store_codes(p.q_c + r * p.ld_c + col, encode<T>(v[i], mult), n, p.vec_c);
+    }
+  }
+}
+
+// 2^(s - 127); NaN for the NaN scale 255.
+__device__ __forceinline__ float scale_value(uint32_t s) {
+  return __uint_as_float(s == 255u ? 0x7fc00000u : (s == 0u ? 0x00400000u : s << 23));
+}
+
+// Two E4M3 codes (low 16 bits) as floats, exactly.
+__device__ __forceinline__ void decode2(uint32_t q, float& lo, float& hi) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(q)));
+  lo = f16_lo(h);
+  hi = f16_hi(h);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_checkpoint_restore(const __grid_constant__ CheckpointRestoreParams p) {
+  grid_dependency_sync();
+  const int64_t tcols = (p.cols + kTile - 1) / kTile, trows = (p.rows + kTile - 1) / kTile;
+  const int64_t rb = blockIdx.x / tcols, cb = blockIdx.x % tcols;
+  const int t = threadIdx.x, c8 = t % 16 * 8, r0 = t / 16;
+  const int64_t col = cb * kTile + c8;
+  if (col >= p.cols) return;
+  const int n = int(p.cols - col < 8 ? p.cols - col : 8);
+  uint2 q[kPasses];
+  uint32_t s[kPasses];  // rowwise: the scale of each row
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int64_t r = rb * kTile + r0 + kRowStep * i;
+    q[i] = make_uint2(0, 0);
+    s[i] = 0;
+    if (r >= p.rows) continue;
+    const uint8_t* src = p.q + r * p.ld_q + col;
+    if (p.vec_q && n == 8) {
+      q[i] = *reinterpret_cast<const uint2*>(src);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t b = k < n ? src[k] : 0u;
+        if (k < 4) q[i].x |= b << (8 * k); else q[i].y |= b << (8 * (k - 4));
+      }
+    }
+    if (!p.colwise) s[i] = p.s[scale_byte(r, cb, scale_tile_cols(tcols))];
+  }
+  float f[8];
+  if (p.colwise) {  // the scales of the thread's columns
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = k < n ? scale_value(p.s[scale_byte(col + k, rb, scale_tile_cols(trows))]) : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int64_t r = rb * kTile + r0 + kRowStep * i;
+    if (r >= p.rows) continue;
+    if (!p.colwise) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = scale_value(s[i]);
+    }
+    float y[8];
+    decode2(q[i].x & 0xffffu, y[0], y[1]);
+    decode2(q[i].x >> 16, y[2], y[3]);
+    decode2(q[i].y & 0xffffu, y[4], y[5]);
+    decode2(q[i].y >> 16, y[6], y[7]);
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) mul2_rn(y[k], y[k + 1], f[k], f[k + 1], y[k], y[k + 1]);
+    char* dst = static_cast<char*>(p.out) + (r * p.ld_o + col) * T::kBytes;
+    uint32_t w[Eight<T>::W];
+    if constexpr (T::kBytes == 4) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(y[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = bf16x2_rn(y[2 * k], y[2 * k + 1]);
+    }
+    if (p.vec_out && n == 8) {
+#pragma unroll
+      for (int k = 0; k < Eight<T>::W; k += 4)
+        *reinterpret_cast<uint4*>(dst + 4 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < n) store_bits<T>(dst, k, T::kBytes == 4 ? w[k % Eight<T>::W] : w[k >> 1] >> (16 * (k & 1)));
+    }
+  }
+}
+
+int64_t tiles(int64_t rows, int64_t cols) {
+  return ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
+}
+
+template <class T>
+cudaError_t save(const CheckpointSaveParams& p, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(tiles(p.rows, p.cols)));
+  if (p.q_r != nullptr && p.q_c != nullptr)
+    return launch_kernel(k_checkpoint_save<T, true, true>, grid, dim3(kThreads), 0, stream, p);
+  if (p.q_r != nullptr)
+    return launch_kernel(k_checkpoint_save<T, true, false>, grid, dim3(kThreads), 0, stream, p);
+  return launch_kernel(k_checkpoint_save<T, false, true>, grid, dim3(kThreads), 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_checkpoint_save(const CheckpointSaveParams& p, int dtype, cudaStream_t stream) {
+  return dtype == 0 ? save<F32T>(p, stream) : save<BF16T>(p, stream);
+}
+
+cudaError_t launch_checkpoint_restore(const CheckpointRestoreParams& p, int dtype, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(tiles(p.rows, p.cols)));
+  return dtype == 0 ? launch_kernel(k_checkpoint_restore<F32T>, grid, dim3(kThreads), 0, stream, p)
+                    : launch_kernel(k_checkpoint_restore<BF16T>, grid, dim3(kThreads), 0, stream, p);
+}
+
+}  // namespace mxfp8
