@@ -18,7 +18,10 @@
 // k_gemm_any: operands whose base or row stride is not a multiple of 16 bytes, which no TMA map
 // can describe.  256 threads fetch the boxes with whatever loads the addresses allow and store
 // them swizzled; one thread issues the matrix instructions.
+#include <atomic>
+
 #include "gemm_impl.cuh"
+#include "gemm_maps.h"
 
 namespace mxfp8 {
 namespace {
@@ -171,7 +174,26 @@ __global__ void __launch_bounds__(kAnyLoaders + 32) k_gemm_any(const __grid_cons
 
 }  // namespace
 
-cudaError_t launch_gemm(const GemmParams& p, const DeviceInfo&, cudaStream_t stream, const char** what) {
+// Device address of g_given_up for the current device, looked up once per device.
+static cudaError_t given_up_address(int device, unsigned** out) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<unsigned*> known[kMaxDevices];
+  unsigned* p = device < kMaxDevices ? known[device].load() : nullptr;
+  if (p == nullptr) {
+    const cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_given_up);
+    if (e != cudaSuccess) return e;
+    if (device < kMaxDevices) known[device].store(p);
+  }
+  *out = p;
+  return cudaSuccess;
+}
+
+cudaError_t launch_gemm(const GemmParams& p, const DeviceInfo& dev, cudaStream_t stream, const char** what) {
+  if (p.a.aligned && p.b.aligned) {
+    unsigned* given_up = nullptr;
+    const cudaError_t e = given_up_address(dev.device, &given_up);
+    return e == cudaSuccess ? launch_gemm_pair(p, given_up, dev, stream, what) : e;
+  }
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_gemm_any),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kAnySmem);
   if (e != cudaSuccess) return e;

@@ -1,0 +1,21 @@
+// TMA descriptors of a product's operands and scales (host code).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "linear.h"
+
+namespace mxfp8 {
+
+// Boxes of `rows` stored rows by 128 bytes under the 128-byte swizzle; zeros past the matrix.
+cudaError_t operand_map(const GemmOperand& o, int64_t k, int rows, CUtensorMap* map, const char** what);
+// Boxes of `row_tiles` 512-byte scale tiles, one above the other: coordinates (0, tile along k,
+// 128-row block).
+cudaError_t scale_map(const GemmOperand& o, int64_t k, int row_tiles, CUtensorMap* map, const char** what);
+
+// The kernels for aligned operands.
+cudaError_t launch_gemm_pair(const GemmParams& g, unsigned* given_up, const DeviceInfo& dev, cudaStream_t stream,
+                             const char** what);
+
+}  // namespace mxfp8

@@ -1,0 +1,212 @@
+// Block-scaled product for large outputs: tiles of 256 x 256 by pairs of CTAs.
+//
+// The two SMs of a pair work on one tile with one stream of matrix instructions (cta_group::2,
+// 256 x 256 x 32): each holds 128 rows of A, 128 rows of B and 128 rows of the sums, so a
+// stage of 128 values of k costs an SM 33.5 KB of copies for 512 cycles of matrix work.  A
+// single-SM tile of 128 x 256 would fetch 50 KB for the same 512 cycles.
+//
+// Roles in a CTA: warp 0 fetches (one thread, TMA, six stages), warp 1 of the leading CTA issues scale
+// copies and matrix instructions for both, eight warps write the sums out.
+//
+// Tensor memory has 512 columns; two buffers of 256 sums and the scales do not fit.  The buffers
+// therefore share 32 columns: buffer 0 is columns 0..255, buffer 1 columns 224..479, two sets of
+// scales 480..511.  The writers drain the shared columns of a tile first; then the next
+// tile's instructions start in the other buffer while they write the rest.
+#include <cuda.h>
+
+#include "gemm_impl.cuh"
+#include "gemm_maps.h"
+
+namespace mxfp8 {
+namespace {
+
+constexpr int kStages = 6;
+constexpr int kStageBytes = 2 * kBoxBytes + 3 * kScaleTile;  // A, B, scales of A, scales of both B halves
+constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
+constexpr int kWriters = 8;
+constexpr int kThreads = 64 + 32 * kWriters;
+constexpr int kSecondBuffer = 224;  // first column of the second buffer of sums
+constexpr int kScaleCol = 480;
+
+struct PairParams {
+  GemmParams g;
+  CUtensorMap a, b, sa, sb;
+  unsigned* given_up;
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_gemm_pair(const __grid_constant__ PairParams q) {
+  extern __shared__ char raw[];
+  const GemmParams& p = q.g;
+  // the same offset in both CTAs: their dynamic shared memory starts alike
+  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 3);
+  volatile uint32_t* gave_up = tmem_slot + 1;
+  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages, sums_full = empty + 8 * kStages,
+                 sums_free = sums_full + 16;
+  const int warp = threadIdx.x >> 5;
+  const uint32_t rank = tc::cluster_rank();
+  grid_dependency_sync();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(full + 8 * s, 1);
+      tc::mbar_init(empty + 8 * s, 1);
+    }
+    tc::mbar_init(sums_full, 1);
+    tc::mbar_init(sums_full + 8, 1);
+    tc::mbar_init(sums_free, 2 * kWriters);
+    *gave_up = 0;
+    tc::mbar_init_fence();
+    tc::prefetch_map(&q.a);
+    tc::prefetch_map(&q.b);
+    tc::prefetch_map(&q.sa);
+    tc::prefetch_map(&q.sb);
+  }
+  if (warp == 1) tc::tmem_alloc<2>(tc::smem_addr(tmem_slot), 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t tiles_m = (p.m + 255) / 256, tiles_n = (p.n + 255) / 256, ntiles = tiles_m * tiles_n;
+  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int64_t nk = (p.k + kBlockK - 1) / kBlockK;
+
+  if (warp == 0) {
+    if (tc::elect_one()) {
+      const uint32_t lead_full = tc::in_cta(full, 0);
+      int s = 0;
+      uint32_t phase = 1;
+      int64_t issued = 0;
+      for (int64_t tile = first; tile < ntiles && *gave_up == 0; tile += step) {
+        int64_t tm, tn;
+        tile_at(tile, tiles_m, tiles_n, tm, tn);
+        const int am = int(tm * 256 + rank * 128), bn = int(tn * 256 + rank * 128);
+        for (int64_t kb = 0; kb < nk; ++kb) {
+          if (!tc::mbar_wait(empty + 8 * s, phase, gave_up)) break;
+          const uint32_t st = tc::smem_addr(smem + s * kStageBytes), bar = lead_full + 8 * s;
+          const int k0 = int(kb * kBlockK);
+          if (rank == 0) tc::mbar_expect(full + 8 * s, 2 * kStageBytes);
+          tc::tma_load_2d_pair(st, &q.a, p.a.colwise ? am : k0, p.a.colwise ? k0 : am, bar);
+          tc::tma_load_2d_pair(st + kBoxBytes, &q.b, p.b.colwise ? bn : k0, p.b.colwise ? k0 : bn, bar);
+          tc::tma_load_3d_pair(st + 2 * kBoxBytes, &q.sa, 0, int(scale_tile_of(kb, p.a.block)), int(2 * tm + rank), bar);
+          tc::tma_load_3d_pair(st + 2 * kBoxBytes + kScaleTile, &q.sb, 0, int(scale_tile_of(kb, p.b.block)), int(2 * tn), bar);
+          ++issued;
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // a wait was given up: let the copies in flight land (or a bounded time pass) before leaving
+      if (*gave_up != 0 && rank == 0) {
+        const long long t0 = clock64();
+        for (int i = 0; i < kStages && i < issued; ++i) {
+          const int64_t c = issued - 1 - i;
+          while (!tc::mbar_try(full + 8 * int(c % kStages), uint32_t(c / kStages) & 1) && clock64() - t0 < tc::kWaitCycles) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && tc::elect_one()) {
+      const uint32_t idesc = tc::instr_desc(256, 256, p.a.colwise, p.b.colwise);
+      const uint32_t astep = p.a.colwise ? 4096 : 32, bstep = p.b.colwise ? 4096 : 32;
+      int s = 0;
+      uint32_t phase = 0, nth = 0, set = 0;
+      bool good = true;
+      for (int64_t tile = first; tile < ntiles && good; tile += step, ++nth) {
+        if (nth > 0) good = tc::mbar_wait(sums_free, (nth - 1) & 1, gave_up);
+        tc::fence_after_sync();
+        const uint32_t d = tmem + (nth & 1 ? kSecondBuffer : 0);
+        for (int64_t kb = 0; kb < nk && good; ++kb) {
+          good = tc::mbar_wait(full + 8 * s, phase, gave_up);
+          if (!good) break;
+          tc::fence_after_sync();
+          const uint32_t st = tc::smem_addr(smem + s * kStageBytes);
+          const uint32_t sa = tmem + kScaleCol + 16 * set, sb = sa + 4;
+          set ^= 1;
+          tc::copy_scales<2>(sa, tc::scale_desc(st + 2 * kBoxBytes));
+          tc::copy_scales<2>(sb, tc::scale_desc(st + 2 * kBoxBytes + kScaleTile));
+          tc::copy_scales<2>(sb + 4, tc::scale_desc(st + 2 * kBoxBytes + 2 * kScaleTile));
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            tc::mma_scaled<2>(d, tc::operand_desc(st + j * astep), tc::operand_desc(st + kBoxBytes + j * bstep),
+                              tc::with_scale_ids(idesc, scale_id_of(kb, j, p.a.block), scale_id_of(kb, j, p.b.block)),
+                              sa, sb, kb > 0 || j > 0);
+          tc::commit_pair(empty + 8 * s, 3);
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+        tc::commit_pair(sums_full + 8 * (nth & 1), 3);
+      }
+    }
+  } else {
+    const int half = (warp - 2) >> 2;  // columns 128 half .. + 127
+    const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
+    uint32_t nth = 0;
+    for (int64_t tile = first; tile < ntiles; tile += step, ++nth) {
+      int64_t tm, tn;
+      tile_at(tile, tiles_m, tiles_n, tm, tn);
+      const uint32_t buffer = nth & 1;
+      // no two tiles' sums are ready at once that this warp has not drained: the next tile's
+      // instructions wait for sums_free
+      if (!tc::mbar_wait(sums_full + 8 * buffer, (nth >> 1) & 1, gave_up)) break;
+      tc::fence_after_sync();
+      const int64_t row = tm * 256 + 128 * rank + 32 * (warp & 3) + (threadIdx.x & 31);
+      const int64_t col0 = tn * 256 + 128 * half;
+      const uint32_t d = tmem + lanes + (buffer ? kSecondBuffer : 0) + 128 * half;
+      // the shared columns, the last of buffer 0 and the first of buffer 1, come first; the arrival
+      // after the first chunk also says that the warp is done with the tile before
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const int c = buffer ? i : 3 - i;
+        float v[32];
+        if (nk > 0) {
+          tc::tmem_load32(d + 32 * c, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+        }
+        if (i == 0) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if ((threadIdx.x & 31) == 0) tc::mbar_arrive_cluster(sums_free, 0);
+        }
+        store_row32(p, row, col0 + 32 * c, v);
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after_sync();
+  if (threadIdx.x == 0 && *gave_up != 0) report_given_up(q.given_up);
+  if (warp == 1) tc::tmem_free<2>(tmem, 512);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_pair(const GemmParams& g, unsigned* given_up, const DeviceInfo& dev, cudaStream_t stream,
+                             const char** what) {
+  PairParams q{};
+  q.g = g;
+  q.given_up = given_up;
+  cudaError_t e = operand_map(g.a, g.k, 128, &q.a, what);
+  if (e == cudaSuccess) e = operand_map(g.b, g.k, 128, &q.b, what);
+  if (e == cudaSuccess) e = scale_map(g.a, g.k, 1, &q.sa, what);
+  if (e == cudaSuccess) e = scale_map(g.b, g.k, 2, &q.sb, what);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_gemm_pair), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((g.m + 255) / 256) * ((g.n + 255) / 256);
+  const int64_t pairs = dev.sms / 2;
+  const unsigned grid = 2 * unsigned(tiles < pairs ? tiles : pairs);
+  return launch_kernel(k_gemm_pair, dim3(grid), dim3(kThreads), kSmem, stream, q);
+}
+
+}  // namespace mxfp8
