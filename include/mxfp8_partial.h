@@ -531,12 +531,12 @@ MXFP8_API int mxfp8_gemm(const mxfp8_tensor* a, const mxfp8_tensor* a_scale, con
                int32_t b_block, void* stream);
 
 /*
- * Health of the products: waits for `stream`, then returns 0, or MXFP8_ERR_CUDA when a product
- * on the current device gave up a wait on its own copies or tensor-core work since the last
- * call (each wait inside the kernels ends after about two seconds; the outputs of such a
- * product are invalid).  Not for use during stream capture.
+ * Health of the operators' kernels: waits for `stream`, then returns 0, or MXFP8_ERR_CUDA when
+ * a product or a layer norm on the current device gave up a wait on its own copies or
+ * tensor-core work since the last call (every wait inside these kernels ends after about two
+ * seconds; the outputs of such a call are invalid).  Not for use during stream capture.
  */
-MXFP8_API int mxfp8_gemm_status(void* stream);
+MXFP8_API int mxfp8_device_status(void* stream);
 
 /*
  * Layer norm of each row: output = (x - mean) * rstd * weight + bias, mean and rstd =

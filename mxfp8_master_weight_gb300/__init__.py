@@ -14,7 +14,7 @@ raises if the library was not built.
 """
 from .api import (block_shapes, mxfp8_amax_max_reduce, mxfp8_amax_max_reduce_update_scales,
                   mxfp8_amax_max_reduce_update_scales_ranged, mxfp8_checkpoint_restore,
-                  mxfp8_checkpoint_save, mxfp8_gemm, mxfp8_gemm_status, mxfp8_layer_norm_backward,
+                  mxfp8_checkpoint_save, mxfp8_gemm, mxfp8_device_status, mxfp8_layer_norm_backward,
                   mxfp8_layer_norm_forward, mxfp8_layer_norm_workspace_size, mxfp8_partial_amax,
                   mxfp8_partial_amax_batched, mxfp8_partial_cast, mxfp8_partial_cast_batched,
                   mxfp8_quantize_whole_blocks, mxfp8_quantize_whole_blocks_batched,
@@ -28,5 +28,5 @@ __all__ = ["mxfp8_partial_amax", "mxfp8_amax_max_reduce", "mxfp8_amax_max_reduce
            "mxfp8_partial_cast_batched", "mxfp8_quantize_whole_blocks",
            "mxfp8_quantize_whole_blocks_batched", "mxfp8_swizzle_scales",
            "mxfp8_swizzled_scales_size", "block_shapes", "mxfp8_checkpoint_save",
-           "mxfp8_checkpoint_restore", "mxfp8_gemm", "mxfp8_gemm_status", "mxfp8_layer_norm_forward",
+           "mxfp8_checkpoint_restore", "mxfp8_gemm", "mxfp8_device_status", "mxfp8_layer_norm_forward",
            "mxfp8_layer_norm_backward", "mxfp8_layer_norm_workspace_size"]

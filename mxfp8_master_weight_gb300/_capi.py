@@ -25,7 +25,7 @@ EXPORTED = ("mxfp8_partial_amax", "mxfp8_amax_max_reduce", "mxfp8_update_scales"
             "mxfp8_amax_max_reduce_update_scales", "mxfp8_amax_max_reduce_update_scales_ranged",
             "mxfp8_sharded_update_noalloc", "nvfp4_partial_amax", "nvfp4_update_scales",
             "nvfp4_partial_cast", "mxfp8_checkpoint_save", "mxfp8_checkpoint_restore", "mxfp8_gemm",
-            "mxfp8_gemm_status", "mxfp8_layer_norm_forward", "mxfp8_layer_norm_backward",
+            "mxfp8_device_status", "mxfp8_layer_norm_forward", "mxfp8_layer_norm_backward",
             "mxfp8_layer_norm_workspace_size", "mxfp8_last_error", "mxfp8_version")
 
 
@@ -121,12 +121,12 @@ def load(path: str | None = None):
         lib.mxfp8_checkpoint_save.argtypes = [T, T, T, T, T, i64, i64, vp]
         lib.mxfp8_checkpoint_restore.argtypes = [T, T, T, i64, i64, i32, vp]
         lib.mxfp8_gemm.argtypes = [T, T, T, T, T, T, i64, i64, i64, i32, i32, i32, i32, vp]
-        lib.mxfp8_gemm_status.argtypes = [vp]
+        lib.mxfp8_device_status.argtypes = [vp]
         lib.mxfp8_layer_norm_forward.argtypes = [T, T, T, T, T, T, i64, i64, ctypes.c_float, vp]
         lib.mxfp8_layer_norm_backward.argtypes = [T] * 10 + [i64, i64, vp]
         lib.mxfp8_layer_norm_workspace_size.argtypes = [i64, i64]
         lib.mxfp8_layer_norm_workspace_size.restype = i64
-        for name in ("mxfp8_checkpoint_save", "mxfp8_checkpoint_restore", "mxfp8_gemm", "mxfp8_gemm_status",
+        for name in ("mxfp8_checkpoint_save", "mxfp8_checkpoint_restore", "mxfp8_gemm", "mxfp8_device_status",
                      "mxfp8_layer_norm_forward", "mxfp8_layer_norm_backward"):
             getattr(lib, name).restype = ctypes.c_int
         lib.mxfp8_device_can_access.argtypes = [vp, i64]

@@ -580,10 +580,10 @@ def prepare_gemm(a, a_scale, b, b_scale, addend, out, m, n, k, a_colwise=False, 
                     [t for t in (out, a, a_scale, b, b_scale, addend) if t is not None])
 
 
-def mxfp8_gemm_status(device=None, stream=None) -> None:
-    """Waits for the stream; raises when a product gave up a wait since the last call."""
+def mxfp8_device_status(device=None, stream=None) -> None:
+    """Waits for the stream; raises when a product or a layer norm gave up a wait since the last call."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    _call("mxfp8_gemm_status", dev, _stream(torch.cuda.current_stream(dev) if stream is None else stream, None))
+    _call("mxfp8_device_status", dev, _stream(torch.cuda.current_stream(dev) if stream is None else stream, None))
 
 
 def _layer_norm_forward_args(input, weight, bias, output, mean, rstd, rows, cols):

@@ -168,14 +168,14 @@ __global__ void __launch_bounds__(kAnyLoaders + 32) k_gemm_any(const __grid_cons
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (t == 0 && *gave_up != 0) report_given_up(&g_given_up);
+  if (t == 0 && *gave_up != 0) tc::report_given_up(&g_given_up);
   if (warp == 8) tc::tmem_free<1>(tmem, kAnyTmemCols);
 }
 
 }  // namespace
 
 // Device address of g_given_up for the current device, looked up once per device.
-static cudaError_t given_up_address(int device, unsigned** out) {
+cudaError_t given_up_address(int device, unsigned** out) {
   constexpr int kMaxDevices = 64;
   static std::atomic<unsigned*> known[kMaxDevices];
   unsigned* p = device < kMaxDevices ? known[device].load() : nullptr;
@@ -205,7 +205,7 @@ cudaError_t launch_gemm(const GemmParams& p, const DeviceInfo& dev, cudaStream_t
   return launch_kernel(k_gemm_any, dim3(static_cast<unsigned>(tiles)), dim3(kAnyLoaders + 32), kAnySmem, stream, p);
 }
 
-cudaError_t gemm_given_up(cudaStream_t stream, unsigned* count) {
+cudaError_t waits_given_up(cudaStream_t stream, unsigned* count) {
   cudaError_t e = cudaMemcpyFromSymbolAsync(count, g_given_up, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, stream);
   if (e != cudaSuccess) return e;
   e = cudaStreamSynchronize(stream);

@@ -76,7 +76,4 @@ __device__ __forceinline__ void store_row32(const GemmParams& p, int64_t row, in
   }
 }
 
-// Count of products that gave up a wait on this device (see mxfp8_gemm_status).
-__device__ __forceinline__ void report_given_up(unsigned* counter) { atomicAdd(counter, 1u); }
-
 }  // namespace mxfp8

@@ -185,7 +185,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::cluster_sync();
   tc::fence_after_sync();
-  if (threadIdx.x == 0 && *gave_up != 0) report_given_up(q.given_up);
+  if (threadIdx.x == 0 && *gave_up != 0) tc::report_given_up(q.given_up);
   if (warp == 1) tc::tmem_free<2>(tmem, 512);
 }
 

@@ -95,15 +95,16 @@ cudaError_t launch_checkpoint_restore(const CheckpointRestoreParams& p, int dtyp
 // *what names the step that failed when it is not the launch itself.
 cudaError_t launch_gemm(const GemmParams& p, const DeviceInfo& dev, cudaStream_t stream,
                         const char** what);
-// Reads and clears the current device's count of given-up waits (waits for the stream).
-cudaError_t gemm_given_up(cudaStream_t stream, unsigned* count);
+// Kernels that gave up a wait count themselves at this address (of the current device).
+cudaError_t given_up_address(int device, unsigned** out);
+// Reads and clears that count (waits for the stream).
+cudaError_t waits_given_up(cudaStream_t stream, unsigned* count);
 // dtype: of x / dy; wdtype: of weight and bias (0 = F32, 1 = BF16).
 cudaError_t launch_norm_forward(const NormForwardParams& p, int dtype, int wdtype,
                                 const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormBackwardParams& p, int dtype, int wdtype,
                                  const DeviceInfo& dev, cudaStream_t stream);
-// Partial sums of the backward pass: at most this many rows of 2 * cols floats.
-constexpr int64_t kNormMaxPartials = 304;
+// Rows of partial sums (2 * cols floats each) that the backward pass leaves, at most.
 int64_t norm_partials(int64_t rows, int64_t cols);
 
 }  // namespace mxfp8

@@ -1,6 +1,6 @@
 // C entry points of the training operators around the MXFP8 weights (declared in
 // include/mxfp8_partial.h): argument validation and dispatch.  No entry point allocates
-// memory, and only mxfp8_gemm_status waits for the GPU.
+// memory, and only mxfp8_device_status waits for the GPU.
 #include <cmath>
 #include <cstdint>
 
@@ -213,11 +213,11 @@ int mxfp8_gemm(const mxfp8_tensor* a, const mxfp8_tensor* a_scale, const mxfp8_t
   return cuda_status(e, what);
 }
 
-int mxfp8_gemm_status(void* stream) {
+int mxfp8_device_status(void* stream) {
   unsigned n = 0;
-  const cudaError_t e = mxfp8::gemm_given_up(static_cast<cudaStream_t>(stream), &n);
-  if (e != cudaSuccess) return cuda_status(e, "gemm status");
-  if (n != 0) return fail(MXFP8_ERR_CUDA, "a product gave up waiting for its own work: its output is invalid");
+  const cudaError_t e = mxfp8::waits_given_up(static_cast<cudaStream_t>(stream), &n);
+  if (e != cudaSuccess) return cuda_status(e, "device status");
+  if (n != 0) return fail(MXFP8_ERR_CUDA, "a kernel gave up waiting for its own work: its output is invalid");
   return ok();
 }
 

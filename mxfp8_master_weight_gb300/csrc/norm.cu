@@ -16,8 +16,11 @@
 // running dw and db of its columns in registers over all rows of its block; a block leaves one
 // row of partial sums, and a second kernel adds the partial rows in their order, so
 // the sums do not depend on the run.
+#include <type_traits>
+
 #include "common.cuh"
 #include "linear.h"
+#include "tensor_core.cuh"
 
 namespace mxfp8 {
 namespace {
@@ -85,7 +88,7 @@ __device__ __forceinline__ void store_eight(void* base, int64_t at, const Eight&
 }
 
 // E4M3 codes [0, n) of p as floats times f.
-__device__ __forceinline__ Eight load_codes(const uint8_t* p, int n, bool vec, float f) {
+__device__ __forceinline__ Eight load_codes(const uint8_t* p, int n, bool vec, float f = 1.0f) {
   uint2 q = make_uint2(0, 0);
   if (vec && n >= 8) {
     q = *reinterpret_cast<const uint2*>(p);
@@ -108,11 +111,38 @@ __device__ __forceinline__ Eight load_codes(const uint8_t* p, int n, bool vec, f
   return e;
 }
 
-// 2^(s - 127) of the rowwise checkpoint scale of (row, column); NaN for 255.
+// 2^(v - 127); NaN for 255.
+__device__ __forceinline__ float scale_value(uint32_t v) {
+  return __uint_as_float(v == 255u ? 0x7fc00000u : (v == 0u ? 0x00400000u : v << 23));
+}
+// That of the rowwise checkpoint scale of (row, column).
 __device__ __forceinline__ float checkpoint_scale(const uint8_t* s, int64_t row, int64_t col, int64_t cols) {
   const int64_t b = col / kCkptBlock, tcols = scale_tile_cols((cols + kCkptBlock - 1) / kCkptBlock);
-  const uint32_t v = s[((row >> 7) * tcols + (b >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (b & 3)];
-  return __uint_as_float(v == 255u ? 0x7fc00000u : (v == 0u ? 0x00400000u : v << 23));
+  return scale_value(s[((row >> 7) * tcols + (b >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (b & 3)]);
+}
+
+// Two F32 operations in one instruction.
+struct Two {
+  uint64_t v;
+  __device__ __forceinline__ Two() {}
+  __device__ __forceinline__ Two(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ explicit Two(float both) : Two(both, both) {}
+  __device__ __forceinline__ void get(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+};
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -147,24 +177,59 @@ __device__ __forceinline__ int valid(int64_t cols, int64_t col) {
 }
 
 // ------------------------------------------------------------------------------ forward
+// The columns of a thread's pieces.  Where the columns are a multiple of 8: 8 neighbours per piece,
+// one or two 16-byte loads of an aligned row.  Else (rows then start anywhere): neighbours across
+// the threads, so that single loads and stores still fill whole sectors.  The choice goes by the
+// shape alone, so that a result does not change with the alignment of a buffer.
+template <bool kVec>
+struct Columns {
+  int64_t cols;
+  int lane, width;
+  bool aligned;
+  __device__ __forceinline__ int64_t at(int i, int k) const {
+    return kVec ? int64_t(lane + i * width) * 8 + k : int64_t(i * 8 + k) * width + lane;
+  }
+  __device__ __forceinline__ bool in(int i, int k) const { return at(i, k) < cols; }
+  template <class T>
+  __device__ __forceinline__ Eight load(const void* base, int64_t row, int i) const {
+    if constexpr (kVec) return load_eight<T>(base, row + at(i, 0), valid(cols, at(i, 0)), aligned);
+    Eight e;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t b = in(i, k) ? load_bits<T>(base, row + at(i, k)) : 0u;
+      e.v[k] = T::kBytes == 4 ? __uint_as_float(b) : __uint_as_float(b << 16);
+    }
+    return e;
+  }
+  __device__ __forceinline__ Eight param(const void* base, int bf16, int i) const {
+    return bf16 ? load<BF16T>(base, 0, i) : load<F32T>(base, 0, i);
+  }
+  template <class T>
+  __device__ __forceinline__ void store(void* base, int64_t row, int i, const Eight& e) const {
+    if constexpr (kVec) {
+      store_eight<T>(base, row + at(i, 0), e, valid(cols, at(i, 0)), aligned);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (in(i, k)) store_bits<T>(base, row + at(i, k), T::kBytes == 4 ? __float_as_uint(e.v[k]) : bf16x2_rn(e.v[k], 0.0f));
+    }
+  }
+};
+
 // A row in registers: NV pieces of 8 columns per thread.
-template <class T, bool kBlock, int NV>
+template <class T, bool kBlock, bool kVec, int NV>
 __global__ void __launch_bounds__(kBlock ? 1024 : 256) k_norm_forward(const __grid_constant__ NormForwardParams p,
                                                                       int wbf16) {
   __shared__ float buf[2][32];
   grid_dependency_sync();
-  const int width = kBlock ? blockDim.x : 32;
-  const int lane = kBlock ? threadIdx.x : threadIdx.x & 31;
+  const Columns<kVec> c{p.cols, int(kBlock ? threadIdx.x : threadIdx.x & 31), int(kBlock ? blockDim.x : 32), p.vec != 0};
   const int64_t row = kBlock ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (row >= p.rows) return;  // whole warps only
   int half = 0;
   Eight x[NV];
   float s[1] = {0.0f};
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t col = int64_t(lane + i * width) * 8;
-    x[i] = load_eight<T>(p.x, row * p.ld_x + col, valid(p.cols, col), p.vec);
-  }
+  for (int i = 0; i < NV; ++i) x[i] = c.template load<T>(p.x, row * p.ld_x, i);
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -174,35 +239,27 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) k_norm_forward(const __gr
   s[0] = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int n = valid(p.cols, int64_t(lane + i * width) * 8);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      x[i].v[k] = k < n ? x[i].v[k] - mean : 0.0f;
+      x[i].v[k] = c.in(i, k) ? x[i].v[k] - mean : 0.0f;
       s[0] += x[i].v[k] * x[i].v[k];
     }
   }
   group_sum<kBlock>(s, &buf[0][0], half);
   const float rstd = __frsqrt_rn(s[0] / float(p.cols) + p.eps);
-  if (lane == 0) {
+  if (c.lane == 0) {
     p.mean[row] = mean;
     p.rstd[row] = rstd;
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t col = int64_t(lane + i * width) * 8;
-    const int n = valid(p.cols, col);
-    if (n == 0) continue;
-    const Eight w = load_param(p.weight, wbf16, col, n, p.vec);
-    Eight y;
-    if (p.bias != nullptr) {
-      const Eight b = load_param(p.bias, wbf16, col, n, p.vec);
+    if (!c.in(i, 0)) continue;
+    const Eight w = c.param(p.weight, wbf16, i);
+    Eight b = {}, y;
+    if (p.bias != nullptr) b = c.param(p.bias, wbf16, i);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) y.v[k] = x[i].v[k] * rstd * w.v[k] + b.v[k];
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y.v[k] = x[i].v[k] * rstd * w.v[k];
-    }
-    store_eight<T>(p.y, row * p.ld_y + col, y, n, p.vec);
+    for (int k = 0; k < 8; ++k) y.v[k] = x[i].v[k] * rstd * w.v[k] + b.v[k];
+    c.template store<T>(p.y, row * p.ld_y, i, y);
   }
 }
 
@@ -266,14 +323,35 @@ __device__ __forceinline__ Eight load_input(const NormBackwardParams& p, int64_t
   }
 }
 
-template <class T, bool kCodes, bool kBlock, int NV>
-__global__ void __launch_bounds__(kBlock ? 1024 : 256) k_norm_backward(const __grid_constant__ NormBackwardParams p,
-                                                                       int wbf16) {
+template <class T, bool kCodes, bool kVec>
+__device__ __forceinline__ Eight load_input(const NormBackwardParams& p, const Columns<kVec>& c, int64_t row, int i) {
+  if constexpr (kVec) {
+    return load_input<T, kCodes>(p, row, c.at(i, 0), valid(p.cols, c.at(i, 0)));
+  } else if constexpr (kCodes) {
+    const uint8_t* q = static_cast<const uint8_t*>(p.x) + row * p.ld_x;
+    Eight e;
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const bool in0 = c.in(i, k), in1 = c.in(i, k + 1);
+      const uint32_t two = (in0 ? q[c.at(i, k)] : 0u) | (in1 ? uint32_t(q[c.at(i, k + 1)]) << 8 : 0u);
+      uint32_t h;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+      e.v[k] = in0 ? f16_lo(h) * checkpoint_scale(p.x_scale, row, c.at(i, k), p.cols) : 0.0f;
+      e.v[k + 1] = in1 ? f16_hi(h) * checkpoint_scale(p.x_scale, row, c.at(i, k + 1), p.cols) : 0.0f;
+    }
+    return e;
+  } else {
+    return c.template load<T>(p.x, row * p.ld_x, i);
+  }
+}
+
+template <class T, bool kCodes, bool kBlock, bool kVec, int NV>
+__global__ void __launch_bounds__(kBlock ? (NV == 1 ? 512 : 1024) : 256)
+    k_norm_backward(const __grid_constant__ NormBackwardParams p, int wbf16) {
   __shared__ float buf[2][2 * 32];
-  extern __shared__ float s_acc[];  // warp per row: [8 warps][cols of dw, then db], padded to 8
+  extern __shared__ float s_acc[];  // warp per row: [8 warps][dw of the columns, then db]
   grid_dependency_sync();
-  const int width = kBlock ? blockDim.x : 32;
-  const int lane = kBlock ? threadIdx.x : threadIdx.x & 31;
+  const Columns<kVec> c{p.cols, int(kBlock ? threadIdx.x : threadIdx.x & 31), int(kBlock ? blockDim.x : 32), p.vec != 0};
   const int warp = threadIdx.x >> 5;
   int half = 0;
   const float inv = 1.0f / float(p.cols);
@@ -281,8 +359,7 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) k_norm_backward(const __g
   Eight w[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t col = int64_t(lane + i * width) * 8;
-    w[i] = load_param(p.weight, wbf16, col, valid(p.cols, col), p.vec);
+    w[i] = c.param(p.weight, wbf16, i);
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[i][k] = db[i][k] = 0.0f;
   }
@@ -294,10 +371,8 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) k_norm_backward(const __g
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t col = int64_t(lane + i * width) * 8;
-      const int n = valid(p.cols, col);
-      dy[i] = load_eight<T>(p.dy, row * p.ld_dy + col, n, p.vec);
-      xh[i] = load_input<T, kCodes>(p, row, col, n);
+      dy[i] = c.template load<T>(p.dy, row * p.ld_dy, i);
+      xh[i] = load_input<T, kCodes, kVec>(p, c, row, i);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -315,49 +390,34 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) k_norm_backward(const __g
     const float mg = s[0] * inv, mgx = s[1] * inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t col = int64_t(lane + i * width) * 8;
-      const int n = valid(p.cols, col);
-      if (n == 0) continue;
+      if (!c.in(i, 0)) continue;
       Eight dx;
 #pragma unroll
       for (int k = 0; k < 8; ++k) dx.v[k] = rstd * (dy[i].v[k] * w[i].v[k] - mg - xh[i].v[k] * mgx);
-      store_eight<T>(p.dx, row * p.ld_dx + col, dx, n, p.vec);
+      c.template store<T>(p.dx, row * p.ld_dx, i, dx);
     }
   }
   // one row of partial sums per block: [blocks][2][cols]
   float* out = p.workspace + int64_t(blockIdx.x) * 2 * p.cols;
-  if constexpr (kBlock) {
+  const int cols = int(p.cols);
+  float* mine = kBlock ? out : s_acc + warp * 2 * cols;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t col = int64_t(lane + i * width) * 8;
+  for (int i = 0; i < NV; ++i) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (col + k < p.cols) {
-          out[col + k] = dw[i][k];
-          out[p.cols + col + k] = db[i][k];
-        }
+    for (int k = 0; k < 8; ++k) {
+      if (c.in(i, k)) {
+        mine[c.at(i, k)] = dw[i][k];
+        mine[cols + c.at(i, k)] = db[i][k];
       }
     }
-  } else {
-    const int pc = int((p.cols + 7) / 8 * 8);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = (lane + i * 32) * 8;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (col < pc) {
-          s_acc[warp * 2 * pc + col + k] = dw[i][k];
-          s_acc[warp * 2 * pc + pc + col + k] = db[i][k];
-        }
-      }
-    }
+  }
+  if constexpr (!kBlock) {
     __syncthreads();
-    for (int c = threadIdx.x; c < 2 * pc; c += blockDim.x) {
+    for (int e = threadIdx.x; e < 2 * cols; e += blockDim.x) {
       float v = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v += s_acc[k * 2 * pc + c];
-      const int col = c < pc ? c : c - pc;
-      if (col < p.cols) out[(c < pc ? 0 : p.cols) + col] = v;
+      for (int k = 0; k < 8; ++k) v += s_acc[k * 2 * cols + e];
+      out[e] = v;
     }
   }
 }
@@ -407,15 +467,348 @@ __global__ void __launch_bounds__(1024) k_norm_backward_long(const __grid_consta
   }
 }
 
-// Adds the partial rows in their order: a block owns 32 entries of [2][cols], its 8 warps an
-// eighth of the rows each, added up through shared memory.
-__global__ void __launch_bounds__(256) k_norm_partials(const float* __restrict__ part, int nparts, int64_t cols,
-                                                       float* dweight, float* dbias) {
-  __shared__ float s[8][32];
+// ------------------------------------------------------------------------------ rings
+// Many aligned rows of up to 8192 columns: persistent blocks, each with a ring of rows in shared
+// memory that thread 0 keeps full with bulk copies, so about 200 KB per SM are in flight
+// whatever the warps wait for.  A thread owns fixed columns, NV pieces of 8, and keeps what
+// belongs to a column (weight, bias, running gradients) in registers over all rows.  A row takes
+// two barriers (one backward) of its block; the first of them also says that a slot has been
+// read, and thread 0 refills it.  Several blocks per SM fill each other's waits, so the blocks are
+// as small as a row allows: TH threads.
+constexpr int kRingBytes = 216 * 1024;  // shared memory of an SM that the rings of its blocks share
+constexpr int kRingMaxSlots = 8;
+constexpr int kRingHead = 384;          // barriers and sums
+
+struct Ring {
+  int32_t slots, slot_bytes, second;  // rows in flight; bytes of a slot; offset of the second operand
+  uint32_t smem;
+};
+// first, second: bytes of a row of each operand (multiples of 16); blocks: per SM.
+Ring ring_of(int64_t first, int64_t second, int blocks) {
+  Ring r{};
+  r.second = int32_t((first + 127) / 128 * 128);
+  r.slot_bytes = int32_t(r.second + (second + 127) / 128 * 128);
+  const int n = (kRingBytes / blocks - 1024 - kRingHead) / r.slot_bytes;  // 1 KB per block is the system's
+  r.slots = n < kRingMaxSlots ? n : kRingMaxSlots;
+  r.smem = uint32_t(kRingHead + r.slots * r.slot_bytes);
+  return r;
+}
+
+struct RingHead {
+  uint64_t full[kRingMaxSlots];
+  float sums[2][2][16];
+};
+static_assert(sizeof(RingHead) <= kRingHead, "ring head");
+
+// Sums of N values over the TH threads that own a row.
+template <int TH, int N>
+__device__ __forceinline__ void ring_sum(float (&v)[N], RingHead* h, int& half) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = warp_sum(v[k]);
+  if constexpr (TH > 32) {
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) h->sums[half][k][threadIdx.x >> 5] = v[k];
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(TH) : "memory");
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < TH / 32; w += 2) {
+        const float2 a = *reinterpret_cast<const float2*>(&h->sums[half][k][w]);
+        t += a.x + a.y;
+      }
+      v[k] = t;
+    }
+    half ^= 1;
+  }
+}
+
+// What thread 0 fetches: rows blockIdx.x, blockIdx.x + gridDim.x, ... of one or two operands, in
+// that order, into the slots in turn.
+struct RingFeed {
+  RingHead* h;
+  char* slots;
+  const char *a, *b;
+  int64_t a_pitch, b_pitch, row, rows;
+  uint32_t a_bytes, b_bytes, issued;
+  __device__ __forceinline__ void next(const Ring& ring) {
+    if (row >= rows) return;
+    const uint32_t s = issued % uint32_t(ring.slots);
+    const uint32_t bar = tc::smem_addr(&h->full[s]), dst = tc::smem_addr(slots + s * ring.slot_bytes);
+    tc::mbar_expect(bar, a_bytes + b_bytes);
+    tc::bulk_load(dst, a + row * a_pitch, a_bytes, bar);
+    if (b_bytes != 0) tc::bulk_load(dst + ring.second, b + row * b_pitch, b_bytes, bar);
+    ++issued;
+    row += gridDim.x;
+  }
+  // After a wait was given up: lets the copies in flight land (or a bounded time pass).
+  __device__ __forceinline__ void settle(const Ring& ring) const {
+    const long long t0 = clock64();
+    for (uint32_t i = 0; i < uint32_t(ring.slots) && i < issued; ++i) {
+      const uint32_t c = issued - 1 - i;
+      while (!tc::mbar_try(tc::smem_addr(&h->full[c % uint32_t(ring.slots)]), (c / uint32_t(ring.slots)) & 1) &&
+             clock64() - t0 < tc::kWaitCycles) {
+      }
+    }
+  }
+};
+
+// Barriers and the first fills.
+__device__ __forceinline__ void ring_start(RingFeed& feed, uint32_t* gave_up, const Ring& ring) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ring.slots; ++i) tc::mbar_init(tc::smem_addr(&feed.h->full[i]), 1);
+    *gave_up = 0;
+    tc::mbar_init_fence();
+    for (int i = 0; i < ring.slots; ++i) feed.next(ring);
+  }
+  __syncthreads();
+}
+
+template <class T, int TH, int NV, int BLOCKS>
+__global__ void __launch_bounds__(TH, BLOCKS)
+    k_norm_forward_ring(const __grid_constant__ NormForwardParams p, int wbf16, Ring ring, unsigned* given_up) {
+  extern __shared__ __align__(128) char smem[];
+  __shared__ uint32_t s_gave_up;
+  volatile uint32_t* gave_up = &s_gave_up;
+  RingHead* h = reinterpret_cast<RingHead*>(smem);
+  char* slots = smem + kRingHead;
+  grid_dependency_sync();
+  RingFeed feed{h, slots, static_cast<const char*>(p.x), nullptr, p.ld_x * T::kBytes, 0, blockIdx.x, p.rows,
+                uint32_t(p.cols * T::kBytes), 0, 0};
+  ring_start(feed, &s_gave_up, ring);
+  const int t = threadIdx.x;
+  {
+    const int cols = int(p.cols);
+    const float inv = 1.0f / float(cols);
+    Eight w[NV], b[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (t + i * TH) * 8;
+      w[i] = load_param(p.weight, wbf16, col, valid(cols, col), true);
+      b[i] = {};
+      if (p.bias != nullptr) b[i] = load_param(p.bias, wbf16, col, valid(cols, col), true);
+    }
+    int s = 0, half = 0;
+    uint32_t phase = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+      // a thread whose wait was given up still goes through the row's barriers, so that no other
+      // waits for it; the row is not written
+      const bool good = tc::mbar_wait(tc::smem_addr(&h->full[s]), phase, gave_up);
+      const char* src = slots + s * ring.slot_bytes;
+      Eight x[NV];
+      float sum[1] = {0.0f};
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int col = (t + i * TH) * 8;
+        x[i] = load_eight<T>(src, col, col < cols ? 8 : 0, true);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[0] += x[i].v[k];
+      }
+      ring_sum<TH>(sum, h, half);
+      if (t == 0) feed.next(ring);  // every thread has the row in registers
+      const float mean = sum[0] * inv;
+      sum[0] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const bool in = (t + i * TH) * 8 < cols;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          x[i].v[k] = in ? x[i].v[k] - mean : 0.0f;
+          sum[0] += x[i].v[k] * x[i].v[k];
+        }
+      }
+      ring_sum<TH>(sum, h, half);
+      const float rstd = __frsqrt_rn(sum[0] * inv + p.eps);
+      if (t == 0) {
+        p.mean[row] = mean;
+        p.rstd[row] = rstd;
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int col = (t + i * TH) * 8;
+        if (col < cols && good) {
+          Eight y;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y.v[k] = x[i].v[k] * rstd * w[i].v[k] + b[i].v[k];
+          store_eight<T>(p.y, row * p.ld_y + col, y, 8, true);
+        }
+      }
+      if (++s == ring.slots) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+  }
+  __syncthreads();
+  if (t == 0 && *gave_up != 0) {
+    feed.settle(ring);
+    tc::report_given_up(given_up);
+  }
+}
+
+// xh = (x - mean) rstd of two values.  F32 input keeps the difference; BF16 values and codes,
+// whose own grid is coarser than an F32 rounding of the mean by 2^16 and more, take one fused operation
+// x (f rstd) - mean rstd (f: the code's scale, a power of two).
+template <bool kFused>
+__device__ __forceinline__ Two normalised(Two x, Two mul, Two shift) {
+  if constexpr (kFused) return fma2(x, mul, shift);
+  else return (x + shift) * mul;
+}
+
+template <class T, bool kCodes, int TH, int NV, int BLOCKS>
+__global__ void __launch_bounds__(TH, BLOCKS)
+    k_norm_backward_ring(const __grid_constant__ NormBackwardParams p, int wbf16, Ring ring, unsigned* given_up) {
+  extern __shared__ __align__(128) char smem[];
+  __shared__ uint32_t s_gave_up;
+  volatile uint32_t* gave_up = &s_gave_up;
+  RingHead* h = reinterpret_cast<RingHead*>(smem);
+  char* slots = smem + kRingHead;
+  constexpr int kXBytes = kCodes ? 1 : T::kBytes;
+  constexpr bool kFused = kCodes || T::kBytes == 2;
+  grid_dependency_sync();
+  RingFeed feed{h, slots, static_cast<const char*>(p.dy), static_cast<const char*>(p.x), p.ld_dy * T::kBytes,
+                p.ld_x * kXBytes, blockIdx.x, p.rows, uint32_t(p.cols * T::kBytes), uint32_t(p.cols * kXBytes), 0};
+  ring_start(feed, &s_gave_up, ring);
+  const int t = threadIdx.x;
+  {
+    const int cols = int(p.cols);
+    const float inv = 1.0f / float(cols);
+    Two dw[NV][4], db[NV][4], w[NV][4];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (t + i * TH) * 8;
+      const Eight e = load_param(p.weight, wbf16, col, valid(cols, col), true);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        w[i][k] = Two(e.v[2 * k], e.v[2 * k + 1]);
+        dw[i][k] = db[i][k] = Two(0.0f);
+      }
+    }
+    // the statistics and scales of a row are fetched a whole row ahead: their latency passes
+    // behind the row before
+    struct Stats {
+      float mean, rstd;
+      uint32_t scale[NV];
+    };
+    int at[NV];  // byte of a piece's scale inside a row's tiles
+    if constexpr (kCodes) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int b = (t + i * TH) * 8 / kCkptBlock;
+        at[i] = (b >> 2) * 512 + (b & 3);
+      }
+    }
+    const int64_t row_tiles = scale_tile_cols((cols + kCkptBlock - 1) / kCkptBlock) * 512;
+    auto fetch = [&](int64_t row, Stats& st) {
+      if (row >= p.rows) return;
+      st.mean = p.mean[row];
+      st.rstd = p.rstd[row];
+      if constexpr (kCodes) {
+        const uint8_t* sr = p.x_scale + (row >> 7) * row_tiles + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if ((t + i * TH) * 8 < cols) st.scale[i] = sr[at[i]];
+      }
+    };
+    Stats next = {};
+    fetch(blockIdx.x, next);
+    int s = 0, half = 0;
+    uint32_t phase = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+      const Stats now = next;
+      fetch(row + gridDim.x, next);
+      const bool good = tc::mbar_wait(tc::smem_addr(&h->full[s]), phase, gave_up);  // as in the forward pass
+      const char* src = slots + s * ring.slot_bytes;
+      const Two shift(kFused ? -now.mean * now.rstd : -now.mean);
+      // the piece's dy and xh, as pairs
+      auto piece = [&](int i, int col, Two (&dy)[4], Two (&xh)[4]) {
+        const Eight e = load_eight<T>(src, col, 8, true);
+        const Two mul(kCodes ? scale_value(now.scale[i]) * now.rstd : now.rstd);
+        Eight x;
+        if constexpr (kCodes) x = load_codes(reinterpret_cast<const uint8_t*>(src) + ring.second + col, 8, true);
+        else x = load_eight<T>(src + ring.second, col, 8, true);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          dy[k] = Two(e.v[2 * k], e.v[2 * k + 1]);
+          xh[k] = normalised<kFused>(Two(x.v[2 * k], x.v[2 * k + 1]), mul, shift);
+        }
+      };
+      Two s0(0.0f), s1(0.0f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int col = (t + i * TH) * 8;
+        if (col >= cols) continue;
+        Two dy[4], xh[4];
+        piece(i, col, dy, xh);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const Two g = dy[k] * w[i][k];
+          s0 = s0 + g;
+          s1 = fma2(g, xh[k], s1);
+          dw[i][k] = fma2(dy[k], xh[k], dw[i][k]);
+          db[i][k] = db[i][k] + dy[k];
+        }
+      }
+      float sum[2], lo, hi;
+      s0.get(lo, hi);
+      sum[0] = lo + hi;
+      s1.get(lo, hi);
+      sum[1] = lo + hi;
+      ring_sum<TH>(sum, h, half);
+      if (t == 0 && row != blockIdx.x) feed.next(ring);  // every thread is past the row before
+      // dx = rstd g - rstd mean(g) - xh rstd mean(g xh)
+      const Two r2(now.rstd), c0(-now.rstd * (sum[0] * inv)), c1(-now.rstd * (sum[1] * inv));
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int col = (t + i * TH) * 8;
+        if (col >= cols) continue;
+        Two dy[4], xh[4];
+        piece(i, col, dy, xh);
+        Eight dx;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) fma2(xh[k], c1, fma2(dy[k] * w[i][k], r2, c0)).get(dx.v[2 * k], dx.v[2 * k + 1]);
+        if (good) store_eight<T>(p.dx, row * p.ld_dx + col, dx, 8, true);
+      }
+      if (++s == ring.slots) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+    float* out = p.workspace + int64_t(blockIdx.x) * 2 * cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (t + i * TH) * 8;
+      if (col >= cols) continue;
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        float4 a, c;
+        dw[i][k].get(a.x, a.y);
+        dw[i][k + 1].get(a.z, a.w);
+        db[i][k].get(c.x, c.y);
+        db[i][k + 1].get(c.z, c.w);
+        *reinterpret_cast<float4*>(out + col + 2 * k) = a;
+        *reinterpret_cast<float4*>(out + cols + col + 2 * k) = c;
+      }
+    }
+  }
+  __syncthreads();
+  if (t == 0 && *gave_up != 0) {
+    feed.settle(ring);
+    tc::report_given_up(given_up);
+  }
+}
+
+// Adds the partial rows in their order: a block owns 32 entries of [2][cols], each of its 32 warps a
+// 32nd of the rows, added up through shared memory.
+__global__ void __launch_bounds__(1024) k_norm_partials(const float* __restrict__ part, int nparts, int64_t cols,
+                                                        float* dweight, float* dbias) {
+  __shared__ float s[32][33];
   grid_dependency_sync();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t e = int64_t(blockIdx.x) * 32 + lane;
-  const int lo = nparts * warp / 8, hi = nparts * (warp + 1) / 8;
+  const int lo = nparts * warp / 32, hi = nparts * (warp + 1) / 32;
   float v = 0.0f;
   if (e < 2 * cols) {
 #pragma unroll 8
@@ -423,12 +816,11 @@ __global__ void __launch_bounds__(256) k_norm_partials(const float* __restrict__
   }
   s[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && e < 2 * cols) {
-    v = s[0][lane];
-#pragma unroll
-    for (int k = 1; k < 8; ++k) v += s[k][lane];
-    if (e < cols) dweight[e] = v;
-    else if (dbias != nullptr) dbias[e - cols] = v;
+  v = warp_sum(s[lane][warp]);  // this warp: entry `warp` of the block
+  const int64_t mine = int64_t(blockIdx.x) * 32 + warp;
+  if (lane == 0 && mine < 2 * cols) {
+    if (mine < cols) dweight[mine] = v;
+    else if (dbias != nullptr) dbias[mine - cols] = v;
   }
 }
 
@@ -451,67 +843,132 @@ Spread spread_of(int64_t cols, int max_nv) {
   return {true, 0, 1024};
 }
 
+// Whether rows of `cols` columns can go through a ring: enough of them for the prologue of a
+// persistent block to pay, and every row a whole number of 16-byte units.
+bool ring_rows(int64_t rows, int64_t cols, const DeviceInfo& dev) { return cols <= 8192 && rows >= 4 * int64_t(dev.sms); }
+
+template <class T, int TH, int NV, int BLOCKS>
+cudaError_t forward_ring(const NormForwardParams& p, int wdtype, const DeviceInfo& dev, unsigned* given_up,
+                         cudaStream_t stream) {
+  const Ring ring = ring_of(p.cols * T::kBytes, 0, BLOCKS);
+  auto kernel = k_norm_forward_ring<T, TH, NV, BLOCKS>;
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring.smem));
+  if (e != cudaSuccess) return e;
+  const int64_t most = BLOCKS * dev.sms;
+  return launch_kernel(kernel, dim3(unsigned(p.rows < most ? p.rows : most)), dim3(TH), ring.smem, stream, p, wdtype,
+                       ring, given_up);
+}
+
 template <class T>
-cudaError_t forward(const NormForwardParams& p, int wdtype, cudaStream_t stream) {
-  const Spread s = spread_of(p.cols, 4);
-  const dim3 block(s.threads);
-  if (!s.block) {
-    const dim3 grid(static_cast<unsigned>((p.rows + 7) / 8));
-    if (s.nv == 1) return launch_kernel(k_norm_forward<T, false, 1>, grid, block, 0, stream, p, wdtype);
-    if (s.nv == 2) return launch_kernel(k_norm_forward<T, false, 2>, grid, block, 0, stream, p, wdtype);
-    return launch_kernel(k_norm_forward<T, false, 4>, grid, block, 0, stream, p, wdtype);
+cudaError_t forward(const NormForwardParams& p, int wdtype, const DeviceInfo& dev, cudaStream_t stream) {
+  const int64_t pieces = (p.cols + 7) / 8;
+  auto launch = [&](auto kernel, int64_t blocks, int threads) {
+    return launch_kernel(kernel, dim3(unsigned(blocks)), dim3(threads), 0, stream, p, wdtype);
+  };
+  if (p.vec && p.cols % 8 == 0 && ring_rows(p.rows, p.cols, dev)) {
+    unsigned* given_up = nullptr;
+    const cudaError_t e = given_up_address(dev.device, &given_up);
+    if (e != cudaSuccess) return e;
+    if (pieces <= 32) return forward_ring<T, 32, 1, 24>(p, wdtype, dev, given_up, stream);
+    if (pieces <= 64) return forward_ring<T, 32, 2, 20>(p, wdtype, dev, given_up, stream);
+    if (pieces <= 128) return forward_ring<T, 64, 2, 12>(p, wdtype, dev, given_up, stream);
+    if (pieces <= 256) return forward_ring<T, 128, 2, 6>(p, wdtype, dev, given_up, stream);
+    if (pieces <= 512) return forward_ring<T, 256, 2, 3>(p, wdtype, dev, given_up, stream);
+    if (pieces <= 768) return forward_ring<T, 256, 3, 2>(p, wdtype, dev, given_up, stream);
+    return forward_ring<T, 256, 4, 2>(p, wdtype, dev, given_up, stream);
   }
-  const dim3 grid(static_cast<unsigned>(p.rows));
-  if (s.nv == 1) return launch_kernel(k_norm_forward<T, true, 1>, grid, block, 0, stream, p, wdtype);
-  if (s.nv == 2) return launch_kernel(k_norm_forward<T, true, 2>, grid, block, 0, stream, p, wdtype);
-  if (s.nv == 4) return launch_kernel(k_norm_forward<T, true, 4>, grid, block, 0, stream, p, wdtype);
-  return launch_kernel(k_norm_forward_long<T>, grid, block, 0, stream, p, wdtype);
+  auto direct = [&](auto vec) {
+    constexpr bool kVec = decltype(vec)::value;
+    if (pieces <= 32) return launch(k_norm_forward<T, false, kVec, 1>, (p.rows + 7) / 8, 256);
+    if (pieces <= 64) return launch(k_norm_forward<T, false, kVec, 2>, (p.rows + 7) / 8, 256);
+    if (pieces <= 128) return launch(k_norm_forward<T, false, kVec, 4>, (p.rows + 7) / 8, 256);
+    auto threads = [&](int nv) { return int(((pieces + nv - 1) / nv + 31) / 32 * 32); };
+    if (pieces <= 512) return launch(k_norm_forward<T, true, kVec, 1>, p.rows, threads(1));
+    if (pieces <= 1024) return launch(k_norm_forward<T, true, kVec, 2>, p.rows, threads(2));
+    return launch(k_norm_forward<T, true, kVec, 4>, p.rows, threads(4));
+  };
+  if (pieces <= 4096) return p.cols % 8 == 0 ? direct(std::true_type{}) : direct(std::false_type{});
+  return launch_kernel(k_norm_forward_long<T>, dim3(unsigned(p.rows)), dim3(1024), 0, stream, p, wdtype);
+}
+
+template <class T, bool kCodes, int TH, int NV, int BLOCKS>
+cudaError_t backward_ring(const NormBackwardParams& p, int wdtype, const DeviceInfo& dev, unsigned* given_up,
+                          unsigned* blocks, cudaStream_t stream) {
+  const Ring ring = ring_of(p.cols * T::kBytes, p.cols * (kCodes ? 1 : T::kBytes), BLOCKS);
+  auto kernel = k_norm_backward_ring<T, kCodes, TH, NV, BLOCKS>;
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring.smem));
+  if (e != cudaSuccess) return e;
+  const int64_t most = BLOCKS * dev.sms, room = norm_partials(p.rows, p.cols);
+  *blocks = unsigned(most < room ? most : room);
+  return launch_kernel(kernel, dim3(*blocks), dim3(TH), ring.smem, stream, p, wdtype, ring, given_up);
 }
 
 template <class T, bool kCodes>
-cudaError_t backward(const NormBackwardParams& p, int wdtype, cudaStream_t stream) {
+cudaError_t backward(const NormBackwardParams& p, int wdtype, const DeviceInfo& dev, cudaStream_t stream) {
   const Spread s = spread_of(p.cols, 2);
-  const dim3 block(s.threads), grid(static_cast<unsigned>(norm_partials(p.rows, p.cols)));
+  const int64_t pieces = (p.cols + 7) / 8, room = norm_partials(p.rows, p.cols), work = s.block ? p.rows : (p.rows + 7) / 8;
+  unsigned blocks = unsigned(work < room ? work : room);
+  const dim3 block(s.threads), grid(blocks);
+  const bool units = p.vec && p.cols % (kCodes ? 16 : 8) == 0 && (!kCodes || p.ld_x % 16 == 0) &&
+                     reinterpret_cast<uintptr_t>(p.x) % 16 == 0;
   cudaError_t e;
-  if (!s.block) {
-    const size_t smem = size_t(8) * 2 * size_t((p.cols + 7) / 8 * 8) * 4;
-    auto run = [&](auto kernel) {
-      const cudaError_t a = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
-      return a != cudaSuccess ? a : launch_kernel(kernel, grid, block, smem, stream, p, wdtype);
-    };
-    e = s.nv == 1 ? run(k_norm_backward<T, kCodes, false, 1>)
-                  : (s.nv == 2 ? run(k_norm_backward<T, kCodes, false, 2>) : run(k_norm_backward<T, kCodes, false, 4>));
-  } else if (s.nv == 1) {
-    e = launch_kernel(k_norm_backward<T, kCodes, true, 1>, grid, block, 0, stream, p, wdtype);
-  } else if (s.nv == 2) {
-    e = launch_kernel(k_norm_backward<T, kCodes, true, 2>, grid, block, 0, stream, p, wdtype);
-  } else {
+  if (units && ring_rows(p.rows, p.cols, dev)) {
+    unsigned* given_up = nullptr;
+    e = given_up_address(dev.device, &given_up);
+    if (e != cudaSuccess) return e;
+    e = pieces <= 32    ? backward_ring<T, kCodes, 32, 1, 20>(p, wdtype, dev, given_up, &blocks, stream)
+        : pieces <= 64  ? backward_ring<T, kCodes, 32, 2, 16>(p, wdtype, dev, given_up, &blocks, stream)
+        : pieces <= 128 ? backward_ring<T, kCodes, 64, 2, 8>(p, wdtype, dev, given_up, &blocks, stream)
+        : pieces <= 256 ? backward_ring<T, kCodes, 128, 2, 4>(p, wdtype, dev, given_up, &blocks, stream)
+        : pieces <= 512 ? backward_ring<T, kCodes, 256, 2, 2>(p, wdtype, dev, given_up, &blocks, stream)
+        : pieces <= 768 ? backward_ring<T, kCodes, 256, 3, 2>(p, wdtype, dev, given_up, &blocks, stream)
+                        : backward_ring<T, kCodes, 512, 2, 1>(p, wdtype, dev, given_up, &blocks, stream);
+  } else if (s.nv == 0) {
     e = launch_kernel(k_norm_backward_long<T, kCodes>, grid, block, 0, stream, p, wdtype);
+  } else {
+    auto direct = [&](auto vec) {
+      constexpr bool kVec = decltype(vec)::value;
+      auto run = [&](auto kernel, size_t smem) {
+        const cudaError_t a = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
+        return a != cudaSuccess ? a : launch_kernel(kernel, grid, block, smem, stream, p, wdtype);
+      };
+      if (s.block)
+        return s.nv == 1 ? run(k_norm_backward<T, kCodes, true, kVec, 1>, 0) : run(k_norm_backward<T, kCodes, true, kVec, 2>, 0);
+      const size_t smem = size_t(8) * 2 * size_t(p.cols) * 4;
+      if (s.nv == 1) return run(k_norm_backward<T, kCodes, false, kVec, 1>, smem);
+      if (s.nv == 2) return run(k_norm_backward<T, kCodes, false, kVec, 2>, smem);
+      return run(k_norm_backward<T, kCodes, false, kVec, 4>, smem);
+    };
+    e = p.cols % 8 == 0 ? direct(std::true_type{}) : direct(std::false_type{});
   }
   if (e != cudaSuccess) return e;
   const dim3 rgrid(static_cast<unsigned>((2 * p.cols + 31) / 32));
-  return launch_kernel(k_norm_partials, rgrid, dim3(256), 0, stream, static_cast<const float*>(p.workspace),
-                       int(grid.x), p.cols, p.dweight, p.dbias);
+  return launch_kernel(k_norm_partials, rgrid, dim3(1024), 0, stream, static_cast<const float*>(p.workspace),
+                       int(blocks), p.cols, p.dweight, p.dbias);
 }
 
 }  // namespace
 
+// Two blocks per SM for long rows; more of the small blocks of short ones.
 int64_t norm_partials(int64_t rows, int64_t cols) {
-  const int64_t blocks = spread_of(cols, 2).block ? rows : (rows + 7) / 8;
-  return blocks < kNormMaxPartials ? blocks : kNormMaxPartials;
+  const int64_t most = cols <= 256 ? 3040 : (cols <= 512 ? 2432 : (cols <= 1024 ? 1216 : (cols <= 2048 ? 608 : 304)));
+  return rows < most ? rows : most;
 }
 
-cudaError_t launch_norm_forward(const NormForwardParams& p, int dtype, int wdtype, const DeviceInfo&,
+cudaError_t launch_norm_forward(const NormForwardParams& p, int dtype, int wdtype, const DeviceInfo& dev,
                                 cudaStream_t stream) {
-  return dtype == 0 ? forward<F32T>(p, wdtype, stream) : forward<BF16T>(p, wdtype, stream);
+  return dtype == 0 ? forward<F32T>(p, wdtype, dev, stream) : forward<BF16T>(p, wdtype, dev, stream);
 }
 
-cudaError_t launch_norm_backward(const NormBackwardParams& p, int dtype, int wdtype, const DeviceInfo&,
+cudaError_t launch_norm_backward(const NormBackwardParams& p, int dtype, int wdtype, const DeviceInfo& dev,
                                  cudaStream_t stream) {
   const bool codes = p.x_scale != nullptr;
-  if (dtype == 0) return codes ? backward<F32T, true>(p, wdtype, stream) : backward<F32T, false>(p, wdtype, stream);
-  return codes ? backward<BF16T, true>(p, wdtype, stream) : backward<BF16T, false>(p, wdtype, stream);
+  if (dtype == 0)
+    return codes ? backward<F32T, true>(p, wdtype, dev, stream) : backward<F32T, false>(p, wdtype, dev, stream);
+  return codes ? backward<BF16T, true>(p, wdtype, dev, stream) : backward<BF16T, false>(p, wdtype, dev, stream);
 }
 
 }  // namespace mxfp8

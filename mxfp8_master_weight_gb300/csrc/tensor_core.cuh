@@ -1,4 +1,4 @@
-// PTX wrappers of the block-scaled product kernels (sm_103a): mbarriers with bounded waits, TMA
+// PTX wrappers of the training operators' kernels (sm_103a): mbarriers with bounded waits, TMA
 // loads, tensor memory, and the block-scaled tcgen05 matrix instruction.
 #pragma once
 
@@ -62,6 +62,9 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
   return true;
 }
+
+// Counts a kernel that gave up a wait (see mxfp8_device_status).
+__device__ __forceinline__ void report_given_up(unsigned* counter) { atomicAdd(counter, 1u); }
 
 // ------------------------------------------------------------------------------ fences
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -199,6 +202,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+// Untiled copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void prefetch_map(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");

@@ -53,7 +53,7 @@ def run(m, n, k, acol=False, bcol=False, ablk=128, bblk=128, dtype="f32", pitch=
     out = torch.full((m, n + 3), -3.0, dtype=DT[dtype], device="cuda")
     c = torch.randn(m, n, device="cuda") * k if addend else None
     api.mxfp8_gemm(qa, sa, qb, sb, c, out[:, :n], m, n, k, acol, bcol, ablk, bblk)
-    api.mxfp8_gemm_status()
+    api.mxfp8_device_status()
     check(out[:, :n], a, b, k, None if c is None else ref.as64(c))
     assert bool((out[:, n:] == -3.0).all())
 
