@@ -90,7 +90,6 @@ __global__ void __launch_bounds__(kAnyLoaders + 32) k_gemm_any(const __grid_cons
   volatile uint32_t* gave_up = tmem_slot + 1;
   const int t = threadIdx.x, warp = t >> 5;
   const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kAnyStages, done = empty + 8 * kAnyStages;
-  grid_dependency_sync();
   if (t == 0) {
     for (int s = 0; s < kAnyStages; ++s) {
       tc::mbar_init(full + 8 * s, kAnyLoaders);
@@ -104,6 +103,7 @@ __global__ void __launch_bounds__(kAnyLoaders + 32) k_gemm_any(const __grid_cons
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  tc::grid_wait_then_release();
   const uint32_t tmem = *tmem_slot;
   int64_t tm, tn;
   tile_at(blockIdx.x, (p.m + 127) / 128, (p.n + 127) / 128, tm, tn);
@@ -151,18 +151,17 @@ __global__ void __launch_bounds__(kAnyLoaders + 32) k_gemm_any(const __grid_cons
   if (warp < 8) {
     tc::mbar_wait(done, 0, gave_up);
     tc::fence_after_sync();
-    const int64_t row = tm * 128 + 32 * (warp & 3) + (t & 31);
+    // the stages are free again: every copy into them has been used
+    const int width = p.out_f32 ? 32 : 64;
+    for (int c = 64 * (warp >> 2); c < 64 * (warp >> 2) + 64; c += width) {
+      write_rows(p, smem + warp * 4096, tm * 128 + 32 * (warp & 3), tn * 128 + c, [&](int e, float(&v)[32]) {
+        if (nk > 0) {
+          tc::tmem_load32(tmem + (uint32_t(32 * (warp & 3)) << 16) + c + e, v);
+        } else {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int col = 64 * (warp >> 2) + 32 * c;
-      float v[32];
-      if (nk > 0) {
-        tc::tmem_load32(tmem + (uint32_t(32 * (warp & 3)) << 16) + col, v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-      }
-      store_row32(p, row, tn * 128 + col, v);
+          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+        }
+      });
     }
   }
   tc::fence_before_sync();
@@ -192,7 +191,14 @@ cudaError_t launch_gemm(const GemmParams& p, const DeviceInfo& dev, cudaStream_t
   if (p.a.aligned && p.b.aligned) {
     unsigned* given_up = nullptr;
     const cudaError_t e = given_up_address(dev.device, &given_up);
-    return e == cudaSuccess ? launch_gemm_pair(p, given_up, dev, stream, what) : e;
+    if (e != cudaSuccess) return e;
+    // Split over k: outputs of at most 64 rows or columns (a tile of the pair kernel would stay mostly
+    // empty: 64 x 4096 x 4096 8.6 us split, 10.3 us by pairs), and few tiles with a long k, where it
+    // finds work for every SM (160 x 96 x 2048 7.5 / 11.0 us).  Everything else by pairs
+    // (1024^3 9.4 / 6.0 us, 256 x 4096 x 4096 14.8 / 10.5 us, 2048^3 12.4 / 10.8 us).
+    const int64_t halves = ((p.m + 255) / 256) * ((p.n + 127) / 128);
+    const bool split = p.m <= 64 || p.n <= 64 || (8 * halves <= dev.sms && p.k >= 16 * kBlockK);
+    return split ? launch_gemm_split(p, given_up, dev, stream, what) : launch_gemm_pair(p, given_up, dev, stream, what);
   }
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_gemm_any),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kAnySmem);

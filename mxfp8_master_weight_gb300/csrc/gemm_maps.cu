@@ -41,11 +41,21 @@ cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const v
 
 }  // namespace
 
-cudaError_t operand_map(const GemmOperand& o, int64_t k, int rows, CUtensorMap* map, const char** what) {
+static cudaError_t codes_map(const GemmOperand& o, int64_t k, int bytes, int rows, CUtensorMapSwizzle swizzle,
+                             CUtensorMap* map, const char** what) {
   const cuuint64_t dims[2] = {cuuint64_t(o.colwise ? o.mn : k), cuuint64_t(o.colwise ? k : o.mn)};
   const cuuint64_t strides[1] = {cuuint64_t(o.ld)};
-  const cuuint32_t box[2] = {128, cuuint32_t(rows)};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, o.codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, what);
+  const cuuint32_t box[2] = {cuuint32_t(bytes), cuuint32_t(rows)};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, o.codes, dims, strides, box, swizzle, what);
+}
+
+cudaError_t operand_map(const GemmOperand& o, int64_t k, int rows, CUtensorMap* map, const char** what) {
+  return codes_map(o, k, 128, rows, CU_TENSOR_MAP_SWIZZLE_128B, map, what);
+}
+
+cudaError_t half_operand_map(const GemmOperand& o, int64_t k, CUtensorMap* map, const char** what) {
+  return o.colwise ? codes_map(o, k, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B, map, what)
+                   : codes_map(o, k, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B, map, what);
 }
 
 cudaError_t scale_map(const GemmOperand& o, int64_t k, int row_tiles, CUtensorMap* map, const char** what) {

@@ -10,6 +10,9 @@ namespace mxfp8 {
 
 // Boxes of `rows` stored rows by 128 bytes under the 128-byte swizzle; zeros past the matrix.
 cudaError_t operand_map(const GemmOperand& o, int64_t k, int rows, CUtensorMap* map, const char** what);
+// Boxes of half as many m or n: 64 rows by 128 bytes, or (columnwise) 128 rows by 64 bytes under the
+// 64-byte swizzle.
+cudaError_t half_operand_map(const GemmOperand& o, int64_t k, CUtensorMap* map, const char** what);
 // Boxes of `row_tiles` 512-byte scale tiles, one above the other: coordinates (0, tile along k,
 // 128-row block).
 cudaError_t scale_map(const GemmOperand& o, int64_t k, int row_tiles, CUtensorMap* map, const char** what);
@@ -17,5 +20,7 @@ cudaError_t scale_map(const GemmOperand& o, int64_t k, int row_tiles, CUtensorMa
 // The kernels for aligned operands.
 cudaError_t launch_gemm_pair(const GemmParams& g, unsigned* given_up, const DeviceInfo& dev, cudaStream_t stream,
                              const char** what);
+cudaError_t launch_gemm_split(const GemmParams& g, unsigned* given_up, const DeviceInfo& dev, cudaStream_t stream,
+                              const char** what);
 
 }  // namespace mxfp8

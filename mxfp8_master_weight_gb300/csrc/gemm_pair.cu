@@ -5,8 +5,12 @@
 // stage of 128 values of k costs an SM 33.5 KB of copies for 512 cycles of matrix work.  A
 // single-SM tile of 128 x 256 would fetch 50 KB for the same 512 cycles.
 //
-// Roles in a CTA: warp 0 fetches (one thread, TMA, six stages), warp 1 of the leading CTA issues scale
+// Roles in a CTA: warp 0 fetches (one thread, TMA, five stages, or seven of halves), warp 1 of the leading CTA issues scale
 // copies and matrix instructions for both, eight warps write the sums out.
+//
+// When the last round of tiles would occupy at most half of the pairs, its tiles are cut into
+// halves of 256 x 128, one per pair: 4096^3 (256 tiles, 76 pairs: 3.5 rounds instead of 4) 47.4 -> 45.8 us;
+// outputs of few tiles, all of them halves: 256 x 4096 x 4096 13.9 -> 10.5 us.
 //
 // Tensor memory has 512 columns; two buffers of 256 sums and the scales do not fit.  The buffers
 // therefore share 32 columns: buffer 0 is columns 0..255, buffer 1 columns 224..479, two sets of
@@ -20,19 +24,38 @@
 namespace mxfp8 {
 namespace {
 
-constexpr int kStages = 6;
-constexpr int kStageBytes = 2 * kBoxBytes + 3 * kScaleTile;  // A, B, scales of A, scales of both B halves
-constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
+constexpr int kMaxStages = 7;
+constexpr int kScaleBytes = 3 * kScaleTile;  // of A, and of both 128-row halves of B
 constexpr int kWriters = 8;
+constexpr int kWriterBytes = 4096;  // a writer's 32 rows of 128 bytes
+constexpr int kSmem = 226 * 1024;
+// What is left for stages: a stage is A's box, B's box (half a box where every tile is a half) and
+// the scales, each kind in an array of its own, which keeps the boxes on 1024-byte boundaries.
+constexpr int kStageRoom = kSmem - 1024 - kWriters * kWriterBytes - 256;
 constexpr int kThreads = 64 + 32 * kWriters;
 constexpr int kSecondBuffer = 224;  // first column of the second buffer of sums
 constexpr int kScaleCol = 480;
 
 struct PairParams {
   GemmParams g;
-  CUtensorMap a, b, sa, sb;
+  CUtensorMap a, b, b_half, sa, sb;
   unsigned* given_up;
+  int64_t whole, units;  // whole tiles first, then halves
+  int32_t stages, b_bytes;
 };
+
+struct Tile {
+  int64_t tm, col;  // 256-row block; first column
+  bool half;
+};
+__device__ __forceinline__ Tile tile_of(const PairParams& q, int64_t unit, int64_t tiles_m, int64_t tiles_n) {
+  Tile t;
+  int64_t tn;
+  t.half = unit >= q.whole;
+  tile_at(t.half ? q.whole + (unit - q.whole) / 2 : unit, tiles_m, tiles_n, t.tm, tn);
+  t.col = tn * 256 + (t.half ? 128 * ((unit - q.whole) & 1) : 0);
+  return t;
+}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_gemm_pair(const __grid_constant__ PairParams q) {
@@ -40,16 +63,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const GemmParams& p = q.g;
   // the same offset in both CTAs: their dynamic shared memory starts alike
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 3);
+  char* b_boxes = smem + q.stages * kBoxBytes;
+  char* scales = b_boxes + q.stages * q.b_bytes;
+  char* writers = scales + q.stages * kScaleBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(writers + kWriters * kWriterBytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 3);
   volatile uint32_t* gave_up = tmem_slot + 1;
-  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages, sums_full = empty + 8 * kStages,
+  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kMaxStages, sums_full = empty + 8 * kMaxStages,
                  sums_free = sums_full + 16;
   const int warp = threadIdx.x >> 5;
   const uint32_t rank = tc::cluster_rank();
-  grid_dependency_sync();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < q.stages; ++s) {
       tc::mbar_init(full + 8 * s, 1);
       tc::mbar_init(empty + 8 * s, 1);
     }
@@ -60,6 +85,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::mbar_init_fence();
     tc::prefetch_map(&q.a);
     tc::prefetch_map(&q.b);
+    tc::prefetch_map(&q.b_half);
     tc::prefetch_map(&q.sa);
     tc::prefetch_map(&q.sb);
   }
@@ -68,8 +94,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::cluster_sync();
   tc::fence_after_sync();
+  tc::grid_wait_then_release();
   const uint32_t tmem = *tmem_slot;
-  const int64_t tiles_m = (p.m + 255) / 256, tiles_n = (p.n + 255) / 256, ntiles = tiles_m * tiles_n;
+  const int64_t tiles_m = (p.m + 255) / 256, tiles_n = (p.n + 255) / 256;
   const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
   const int64_t nk = (p.k + kBlockK - 1) / kBlockK;
 
@@ -79,21 +106,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int s = 0;
       uint32_t phase = 1;
       int64_t issued = 0;
-      for (int64_t tile = first; tile < ntiles && *gave_up == 0; tile += step) {
-        int64_t tm, tn;
-        tile_at(tile, tiles_m, tiles_n, tm, tn);
-        const int am = int(tm * 256 + rank * 128), bn = int(tn * 256 + rank * 128);
+      for (int64_t unit = first; unit < q.units && *gave_up == 0; unit += step) {
+        const Tile t = tile_of(q, unit, tiles_m, tiles_n);
+        const int am = int(t.tm * 256 + rank * 128), bn = int(t.col + rank * (t.half ? 64 : 128));
+        const uint32_t bytes = kBoxBytes + (t.half ? kBoxBytes / 2 : kBoxBytes) + kScaleBytes;
         for (int64_t kb = 0; kb < nk; ++kb) {
           if (!tc::mbar_wait(empty + 8 * s, phase, gave_up)) break;
-          const uint32_t st = tc::smem_addr(smem + s * kStageBytes), bar = lead_full + 8 * s;
+          const uint32_t at_a = tc::smem_addr(smem + s * kBoxBytes), at_b = tc::smem_addr(b_boxes + s * q.b_bytes),
+                         at_s = tc::smem_addr(scales + s * kScaleBytes), bar = lead_full + 8 * s;
           const int k0 = int(kb * kBlockK);
-          if (rank == 0) tc::mbar_expect(full + 8 * s, 2 * kStageBytes);
-          tc::tma_load_2d_pair(st, &q.a, p.a.colwise ? am : k0, p.a.colwise ? k0 : am, bar);
-          tc::tma_load_2d_pair(st + kBoxBytes, &q.b, p.b.colwise ? bn : k0, p.b.colwise ? k0 : bn, bar);
-          tc::tma_load_3d_pair(st + 2 * kBoxBytes, &q.sa, 0, int(scale_tile_of(kb, p.a.block)), int(2 * tm + rank), bar);
-          tc::tma_load_3d_pair(st + 2 * kBoxBytes + kScaleTile, &q.sb, 0, int(scale_tile_of(kb, p.b.block)), int(2 * tn), bar);
+          if (rank == 0) tc::mbar_expect(full + 8 * s, 2 * bytes);
+          tc::tma_load_2d_pair(at_a, &q.a, p.a.colwise ? am : k0, p.a.colwise ? k0 : am, bar);
+          tc::tma_load_2d_pair(at_b, t.half ? &q.b_half : &q.b, p.b.colwise ? bn : k0, p.b.colwise ? k0 : bn, bar);
+          tc::tma_load_3d_pair(at_s, &q.sa, 0, int(scale_tile_of(kb, p.a.block)), int(2 * t.tm + rank), bar);
+          tc::tma_load_3d_pair(at_s + kScaleTile, &q.sb, 0, int(scale_tile_of(kb, p.b.block)), int(t.col >> 7), bar);
           ++issued;
-          if (++s == kStages) {
+          if (++s == q.stages) {
             s = 0;
             phase ^= 1;
           }
@@ -102,41 +130,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // a wait was given up: let the copies in flight land (or a bounded time pass) before leaving
       if (*gave_up != 0 && rank == 0) {
         const long long t0 = clock64();
-        for (int i = 0; i < kStages && i < issued; ++i) {
+        for (int i = 0; i < q.stages && i < issued; ++i) {
           const int64_t c = issued - 1 - i;
-          while (!tc::mbar_try(full + 8 * int(c % kStages), uint32_t(c / kStages) & 1) && clock64() - t0 < tc::kWaitCycles) {
+          while (!tc::mbar_try(full + 8 * int(c % q.stages), uint32_t(c / q.stages) & 1) && clock64() - t0 < tc::kWaitCycles) {
           }
         }
       }
     }
   } else if (warp == 1) {
     if (rank == 0 && tc::elect_one()) {
-      const uint32_t idesc = tc::instr_desc(256, 256, p.a.colwise, p.b.colwise);
-      const uint32_t astep = p.a.colwise ? 4096 : 32, bstep = p.b.colwise ? 4096 : 32;
+      const uint32_t astep = p.a.colwise ? 4096 : 32;
       int s = 0;
       uint32_t phase = 0, nth = 0, set = 0;
       bool good = true;
-      for (int64_t tile = first; tile < ntiles && good; tile += step, ++nth) {
+      for (int64_t unit = first; unit < q.units && good; unit += step, ++nth) {
         if (nth > 0) good = tc::mbar_wait(sums_free, (nth - 1) & 1, gave_up);
         tc::fence_after_sync();
         const uint32_t d = tmem + (nth & 1 ? kSecondBuffer : 0);
+        const bool half = unit >= q.whole, narrow = half && p.b.colwise;  // rows of 64 bytes
+        const uint32_t idesc = tc::instr_desc(256, half ? 128 : 256, p.a.colwise, p.b.colwise);
+        const uint32_t bstep = narrow ? 2048 : (p.b.colwise ? 4096 : 32);
         for (int64_t kb = 0; kb < nk && good; ++kb) {
           good = tc::mbar_wait(full + 8 * s, phase, gave_up);
           if (!good) break;
           tc::fence_after_sync();
-          const uint32_t st = tc::smem_addr(smem + s * kStageBytes);
+          const uint32_t at_a = tc::smem_addr(smem + s * kBoxBytes), at_b = tc::smem_addr(b_boxes + s * q.b_bytes),
+                         at_s = tc::smem_addr(scales + s * kScaleBytes);
           const uint32_t sa = tmem + kScaleCol + 16 * set, sb = sa + 4;
           set ^= 1;
-          tc::copy_scales<2>(sa, tc::scale_desc(st + 2 * kBoxBytes));
-          tc::copy_scales<2>(sb, tc::scale_desc(st + 2 * kBoxBytes + kScaleTile));
-          tc::copy_scales<2>(sb + 4, tc::scale_desc(st + 2 * kBoxBytes + 2 * kScaleTile));
+          tc::copy_scales<2>(sa, tc::scale_desc(at_s));
+          tc::copy_scales<2>(sb, tc::scale_desc(at_s + kScaleTile));
+          tc::copy_scales<2>(sb + 4, tc::scale_desc(at_s + 2 * kScaleTile));
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc::mma_scaled<2>(d, tc::operand_desc(st + j * astep), tc::operand_desc(st + kBoxBytes + j * bstep),
+            tc::mma_scaled<2>(d, tc::operand_desc(at_a + j * astep),
+                              narrow ? tc::operand_desc64(at_b + j * bstep) : tc::operand_desc(at_b + j * bstep),
                               tc::with_scale_ids(idesc, scale_id_of(kb, j, p.a.block), scale_id_of(kb, j, p.b.block)),
                               sa, sb, kb > 0 || j > 0);
           tc::commit_pair(empty + 8 * s, 3);
-          if (++s == kStages) {
+          if (++s == q.stages) {
             s = 0;
             phase ^= 1;
           }
@@ -145,38 +177,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    const int half = (warp - 2) >> 2;  // columns 128 half .. + 127
+    const int side = (warp - 2) >> 2;  // the first or second half of the columns
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
     uint32_t nth = 0;
-    for (int64_t tile = first; tile < ntiles; tile += step, ++nth) {
-      int64_t tm, tn;
-      tile_at(tile, tiles_m, tiles_n, tm, tn);
+    for (int64_t unit = first; unit < q.units; unit += step, ++nth) {
+      const Tile t = tile_of(q, unit, tiles_m, tiles_n);
+      const int cols = t.half ? 64 : 128;  // this warp's
       const uint32_t buffer = nth & 1;
       // no two tiles' sums are ready at once that this warp has not drained: the next tile's
       // instructions wait for sums_free
       if (!tc::mbar_wait(sums_full + 8 * buffer, (nth >> 1) & 1, gave_up)) break;
       tc::fence_after_sync();
-      const int64_t row = tm * 256 + 128 * rank + 32 * (warp & 3) + (threadIdx.x & 31);
-      const int64_t col0 = tn * 256 + 128 * half;
-      const uint32_t d = tmem + lanes + (buffer ? kSecondBuffer : 0) + 128 * half;
+      const int64_t row0 = t.tm * 256 + 128 * rank + 32 * (warp & 3), col0 = t.col + cols * side;
+      const uint32_t d = tmem + lanes + (buffer ? kSecondBuffer : 0) + cols * side;
       // the shared columns, the last of buffer 0 and the first of buffer 1, come first; the arrival
       // after the first chunk also says that the warp is done with the tile before
+      const int width = p.out_f32 ? 32 : 64, chunks = cols / width;
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int c = buffer ? i : 3 - i;
-        float v[32];
-        if (nk > 0) {
-          tc::tmem_load32(d + 32 * c, v);
-        } else {
+      for (int i = 0; i < chunks; ++i) {
+        const int c = width * (buffer ? i : chunks - 1 - i);
+        int left = i == 0 ? width / 32 : 0;  // loads until the first chunk is drained
+        write_rows(p, writers + (warp - 2) * kWriterBytes, row0, col0 + c, [&](int e, float(&v)[32]) {
+          if (nk > 0) {
+            tc::tmem_load32(d + c + e, v);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0.0f;
-        }
-        if (i == 0) {
-          tc::fence_before_sync();
-          __syncwarp();
-          if ((threadIdx.x & 31) == 0) tc::mbar_arrive_cluster(sums_free, 0);
-        }
-        store_row32(p, row, col0 + 32 * c, v);
+            for (int k = 0; k < 32; ++k) v[k] = 0.0f;
+          }
+          if (left != 0 && --left == 0) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) tc::mbar_arrive_cluster(sums_free, 0);
+          }
+        });
       }
     }
   }
@@ -198,14 +231,20 @@ cudaError_t launch_gemm_pair(const GemmParams& g, unsigned* given_up, const Devi
   q.given_up = given_up;
   cudaError_t e = operand_map(g.a, g.k, 128, &q.a, what);
   if (e == cudaSuccess) e = operand_map(g.b, g.k, 128, &q.b, what);
+  if (e == cudaSuccess) e = half_operand_map(g.b, g.k, &q.b_half, what);
   if (e == cudaSuccess) e = scale_map(g.a, g.k, 1, &q.sa, what);
   if (e == cudaSuccess) e = scale_map(g.b, g.k, 2, &q.sb, what);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_gemm_pair), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((g.m + 255) / 256) * ((g.n + 255) / 256);
-  const int64_t pairs = dev.sms / 2;
-  const unsigned grid = 2 * unsigned(tiles < pairs ? tiles : pairs);
+  const int64_t pairs = dev.sms / 2, last = tiles % pairs;
+  q.whole = last != 0 && 2 * last <= pairs ? tiles - last : tiles;
+  q.units = q.whole + 2 * (tiles - q.whole);
+  q.b_bytes = q.whole == 0 ? kBoxBytes / 2 : kBoxBytes;
+  const int fit = kStageRoom / (kBoxBytes + q.b_bytes + kScaleBytes);
+  q.stages = fit < kMaxStages ? fit : kMaxStages;
+  const unsigned grid = 2 * unsigned(q.units < pairs ? q.units : pairs);
   return launch_kernel(k_gemm_pair, dim3(grid), dim3(kThreads), kSmem, stream, q);
 }
 

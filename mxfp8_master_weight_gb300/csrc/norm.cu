@@ -192,14 +192,17 @@ struct Columns {
   __device__ __forceinline__ bool in(int i, int k) const { return at(i, k) < cols; }
   template <class T>
   __device__ __forceinline__ Eight load(const void* base, int64_t row, int i) const {
-    if constexpr (kVec) return load_eight<T>(base, row + at(i, 0), valid(cols, at(i, 0)), aligned);
-    Eight e;
+    if constexpr (kVec) {
+      return load_eight<T>(base, row + at(i, 0), valid(cols, at(i, 0)), aligned);
+    } else {
+      Eight e;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t b = in(i, k) ? load_bits<T>(base, row + at(i, k)) : 0u;
-      e.v[k] = T::kBytes == 4 ? __uint_as_float(b) : __uint_as_float(b << 16);
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t b = in(i, k) ? load_bits<T>(base, row + at(i, k)) : 0u;
+        e.v[k] = T::kBytes == 4 ? __uint_as_float(b) : __uint_as_float(b << 16);
+      }
+      return e;
     }
-    return e;
   }
   __device__ __forceinline__ Eight param(const void* base, int bf16, int i) const {
     return bf16 ? load<BF16T>(base, 0, i) : load<F32T>(base, 0, i);

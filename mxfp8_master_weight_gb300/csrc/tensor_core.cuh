@@ -109,6 +109,19 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // ------------------------------------------------------------------------------ descriptors
 // Shared-memory operand in rows of 128 bytes under the 128-byte swizzle (a 16-byte unit c of row
 // r sits at unit c ^ (r % 8)); 8 rows make an atom of 1024 bytes, atoms follow one another.  The
@@ -118,6 +131,12 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
   constexpr uint64_t kSwizzle128 = 2;
   return uint64_t((addr & 0x3ffffu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
          (uint64_t(1) << 46) | (kSwizzle128 << 61);
+}
+// The same in rows of 64 bytes under the 64-byte swizzle (unit c of row r at c ^ (r / 2 % 4)).
+__device__ __forceinline__ uint64_t operand_desc64(uint32_t addr) {
+  constexpr uint64_t kSwizzle64 = 4;
+  return uint64_t((addr & 0x3ffffu) >> 4) | (uint64_t(1) << 16) | (uint64_t(512 >> 4) << 32) |
+         (uint64_t(1) << 46) | (kSwizzle64 << 61);
 }
 // A 512-byte scale tile: 32 rows of 16 bytes, no swizzle, 8 rows per 128 bytes.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
@@ -217,6 +236,16 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t cta) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
   return r;
+}
+
+// ------------------------------------------------------------------------------ launch order
+// The two halves of grid_dependency_sync() for kernels with a prologue worth hiding: barriers and
+// tensor memory are set up before the wait, while the grid before drains.  Every block holds
+// its tensor memory before it lets the next grid in, so a block of that grid, which allocates before its
+// own wait, can only take what is left and keeps nothing that this grid still needs.
+__device__ __forceinline__ void grid_wait_then_release() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ------------------------------------------------------------------------------ clusters
