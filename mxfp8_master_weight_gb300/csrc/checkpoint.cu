@@ -29,16 +29,6 @@ __device__ __forceinline__ int64_t scale_byte(int64_t r, int64_t b, int64_t tcol
   return ((r >> 7) * tcols + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
 }
 
-// Stores the scale of row r of the tile's block b; the row's last block also zeroes the
-// padding entries up to a whole group of four.
-__device__ __forceinline__ void store_scale(uint8_t* s, int64_t r, int64_t b, int64_t nblocks, uint32_t byte) {
-  uint8_t* p = s + scale_byte(r, b, scale_tile_cols(nblocks));
-  *p = static_cast<uint8_t>(byte);
-  if (b == nblocks - 1) {
-    for (int64_t i = (b & 3) + 1; i < 4; ++i) *++p = 0;
-  }
-}
-
 // Eight consecutive elements as 32-bit words: BF16 pairs or F32 values.
 template <class T>
 struct Eight {
@@ -96,68 +86,121 @@ __device__ __forceinline__ uint2 encode(const Eight<T>& v, const float (&mult)[8
                     e4m3x2_rn_sat(p[4], p[5]) | (e4m3x2_rn_sat(p[6], p[7]) << 16));
 }
 
+// |x| of a pair or value, as the maxima take it: non-negative bit patterns order as their values,
+// NaN above infinity.  BF16 keeps two per word.
+template <class T>
+__device__ __forceinline__ uint32_t abs_bits(uint32_t w) { return w & T::kAbsMask; }
+template <class T>
+__device__ __forceinline__ uint32_t max_bits(uint32_t a, uint32_t b) {
+  if constexpr (T::kBytes == 4) return max(a, b); else return __vmaxu2(a, b);
+}
+// Scale byte of one |x| pattern of T.
+template <class T>
+__device__ __forceinline__ uint32_t scale_of(uint32_t bits) { return e8m0_from_bits<T>(bits); }
+
+// The tile's 128 scales of one direction, which lie 4 bytes apart in one 512-byte scale tile: entry
+// r of block `b`.  The last block also zeroes the padding entries up to a whole group of four.
+__device__ __forceinline__ void store_scales(uint8_t* s, int64_t r128, int64_t b, int64_t nblocks, int r, uint32_t byte) {
+  uint8_t* p = s + (r128 * scale_tile_cols(nblocks) + (b >> 2)) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3);
+  *p = static_cast<uint8_t>(byte);
+  if (b == nblocks - 1) {
+    for (int i = int(b & 3) + 1; i < 4; ++i) *++p = 0;
+  }
+}
+
 template <class T, bool kRow, bool kCol>
 __global__ void __launch_bounds__(kThreads) k_checkpoint_save(const __grid_constant__ CheckpointSaveParams p) {
-  __shared__ uint32_t s_max[kThreads / 32][kTile];  // per warp: column maxima of |x| (F32 bits)
-  __shared__ float s_mult[kTile];
+  constexpr int W = Eight<T>::W, kPerWord = 4 / T::kBytes;
+  __shared__ uint32_t s_max[kThreads / 32][kTile / kPerWord];  // per warp: column maxima of |x|
+  __shared__ __align__(16) float s_mult[kTile];
+  __shared__ uint8_t s_row[kTile];
   grid_dependency_sync();
-  const int64_t tcols = (p.cols + kTile - 1) / kTile;
-  const int64_t rb = blockIdx.x / tcols, cb = blockIdx.x % tcols;
+  const uint32_t tcols = uint32_t((p.cols + kTile - 1) / kTile);
+  const uint32_t rb = blockIdx.x / tcols, cb = blockIdx.x % tcols;
   const int t = threadIdx.x, c8 = t % 16 * 8, r0 = t / 16;
-  const int64_t col = cb * kTile + c8;
+  const int64_t col = int64_t(cb) * kTile + c8, row = int64_t(rb) * kTile + r0;
   const int n = int(p.cols - col < 8 ? (p.cols > col ? p.cols - col : 0) : 8);
+  const int left = int(p.rows - row < kTile ? (p.rows > row ? p.rows - row : 0) : kTile);  // rows from this thread's first
   Eight<T> v[kPasses];
+  const char* src = static_cast<const char*>(p.in) + (row * p.ld + col) * T::kBytes;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int64_t r = rb * kTile + r0 + kRowStep * i;
-    v[i] = load_eight<T>(static_cast<const char*>(p.in) + (r * p.ld + col) * T::kBytes, r < p.rows ? n : 0, p.vec_in);
-  }
-  uint32_t cm[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // column maxima over this thread's rows
+  for (int i = 0; i < kPasses; ++i)
+    v[i] = load_eight<T>(src + i * kRowStep * p.ld * T::kBytes, kRowStep * i < left ? n : 0, p.vec_in);
+  uint32_t cm[W], rm[kPasses];
+#pragma unroll
+  for (int k = 0; k < W; ++k) cm[k] = 0;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     uint32_t m = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t a = __float_as_uint(v[i].get(k)) & 0x7fffffffu;
-      m = max(m, a);
-      if constexpr (kCol) cm[k] = max(cm[k], a);
+    for (int k = 0; k < W; ++k) {
+      const uint32_t a = abs_bits<T>(v[i].w[k]);
+      if constexpr (kRow) m = max_bits<T>(m, a);
+      if constexpr (kCol) cm[k] = max_bits<T>(cm[k], a);
     }
-    if constexpr (kRow) {
+    rm[i] = T::kBytes == 4 ? m : max(m & 0xffffu, m >> 16);
+  }
+  if constexpr (kRow) {
+    // over the row's 16 threads; BF16: two rows per word
+    if constexpr (T::kBytes == 2) {
 #pragma unroll
-      for (int off = 1; off < 16; off <<= 1) m = max(m, __shfl_xor_sync(kFullMask, m, off));
-      const uint32_t s = e8m0_from_bits<F32T>(m);
-      const int64_t r = rb * kTile + r0 + kRowStep * i;
-      if (c8 == 0) store_scale(p.s_r, r, cb, tcols, s);  // rows past the last: padding, s = 0
+      for (int i = 0; i < kPasses; i += 2) {
+        uint32_t m = rm[i] | (rm[i + 1] << 16);
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1) m = __vmaxu2(m, __shfl_xor_sync(kFullMask, m, off));
+        rm[i] = m & 0xffffu;
+        rm[i + 1] = m >> 16;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1) rm[i] = max(rm[i], __shfl_xor_sync(kFullMask, rm[i], off));
+      }
+    }
+    uint8_t* q = p.q_r + row * p.ld_r + col;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const uint32_t s = scale_of<T>(rm[i]);
+      if (c8 == 0) s_row[r0 + kRowStep * i] = static_cast<uint8_t>(s);
       const float f = scale_multiplier(s);
       const float mult[8] = {f, f, f, f, f, f, f, f};
-      if (r < p.rows) store_codes(p.q_r + r * p.ld_r + col, encode<T>(v[i], mult), n, p.vec_r);
+      if (kRowStep * i < left) store_codes(q + i * kRowStep * p.ld_r, encode<T>(v[i], mult), n, p.vec_r);
     }
   }
   if constexpr (kCol) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) cm[k] = max(cm[k], __shfl_xor_sync(kFullMask, cm[k], 16));
+    for (int k = 0; k < W; ++k) cm[k] = max_bits<T>(cm[k], __shfl_xor_sync(kFullMask, cm[k], 16));
     if (t % 32 < 16) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s_max[t / 32][c8 + k] = cm[k];
+      for (int k = 0; k < W; ++k) s_max[t / 32][c8 / kPerWord + k] = cm[k];
     }
-    __syncthreads();
+  }
+  __syncthreads();
+  if constexpr (kRow) {  // rows past the last are padding: their maxima are 0, and so is the byte
+    if (t >= kTile) store_scales(p.s_r, rb, cb, tcols, t - kTile, s_row[t - kTile]);
+  }
+  if constexpr (kCol) {
     if (t < kTile) {
       uint32_t m = 0;
 #pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) m = max(m, s_max[w][t]);
-      const uint32_t s = e8m0_from_bits<F32T>(m);
+      for (int w = 0; w < kThreads / 32; ++w) m = max_bits<T>(m, s_max[w][t / kPerWord]);
+      if constexpr (T::kBytes == 2) m = t & 1 ? m >> 16 : m & 0xffffu;
+      const uint32_t s = scale_of<T>(m);
       s_mult[t] = scale_multiplier(s);
-      store_scale(p.s_c, cb * kTile + t, rb, (p.rows + kTile - 1) / kTile, s);
+      store_scales(p.s_c, cb, rb, (p.rows + kTile - 1) / kTile, t, s);
     }
     __syncthreads();
     float mult[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) mult[k] = s_mult[c8 + k];
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int64_t r = rb * kTile + r0 + kRowStep * i;
-      if (r < p.rows) store_codes(p.q_c + r * p.ld_c + col, encode<T>(v[i], mult), n, p.vec_c);
+    for (int k = 0; k < 8; k += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(&s_mult[c8 + k]);
+      mult[k] = f.x; mult[k + 1] = f.y; mult[k + 2] = f.z; mult[k + 3] = f.w;
     }
+    uint8_t* q = p.q_c + row * p.ld_c + col;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      if (kRowStep * i < left) store_codes(q + i * kRowStep * p.ld_c, encode<T>(v[i], mult), n, p.vec_c);
   }
 }
 

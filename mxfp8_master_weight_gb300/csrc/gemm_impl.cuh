@@ -47,13 +47,25 @@ __device__ __forceinline__ void store_one(const GemmParams& p, int64_t i, int64_
 // `sums` is called with the first of 32 columns and gives this lane's row.
 template <class Sums>
 __device__ __forceinline__ void write_rows(const GemmParams& p, char* stage, int64_t row0, int64_t col, Sums sums) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, unit = lane & 7;
+  const int width = p.out_f32 ? 32 : 64;
+  const bool vec = p.vec_out && col + width <= p.n;
+  float4 c[8];
+  const bool add = p.out_f32 && p.addend != nullptr && vec;
+  if (add) {  // on their way before the sums are
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      c[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (row0 + r < p.m) c[i] = *reinterpret_cast<const float4*>(p.addend + (row0 + r) * p.ld_c + col + 4 * unit);
+    }
+  }
   if (p.out_f32) {
     float v[32];
     sums(0, v);
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      *reinterpret_cast<float4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    for (int u = 0; u < 8; ++u)
+      *reinterpret_cast<float4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -65,27 +77,23 @@ __device__ __forceinline__ void write_rows(const GemmParams& p, char* stage, int
           if (col + 32 * h + i < p.n) v[i] += p.addend[(row0 + lane) * p.ld_c + col + 32 * h + i];
       }
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * h + c) ^ (lane & 7)) << 4)) =
-            make_uint4(bf16x2_rn(v[8 * c], v[8 * c + 1]), bf16x2_rn(v[8 * c + 2], v[8 * c + 3]),
-                       bf16x2_rn(v[8 * c + 4], v[8 * c + 5]), bf16x2_rn(v[8 * c + 6], v[8 * c + 7]));
+      for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * h + u) ^ (lane & 7)) << 4)) =
+            make_uint4(bf16x2_rn(v[8 * u], v[8 * u + 1]), bf16x2_rn(v[8 * u + 2], v[8 * u + 3]),
+                       bf16x2_rn(v[8 * u + 4], v[8 * u + 5]), bf16x2_rn(v[8 * u + 6], v[8 * u + 7]));
     }
   }
   __syncwarp();
-  const int width = p.out_f32 ? 32 : 64;
-  if (p.vec_out && col + width <= p.n) {
-    const int unit = lane & 7;
+  if (vec) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = 4 * i + (lane >> 3);
       if (row0 + r >= p.m) continue;
       uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((unit ^ (r & 7)) << 4));
       if (p.out_f32) {
-        if (p.addend != nullptr) {
-          const float4 a = *reinterpret_cast<const float4*>(p.addend + (row0 + r) * p.ld_c + col + 4 * unit);
-          w = make_uint4(__float_as_uint(__uint_as_float(w.x) + a.x), __float_as_uint(__uint_as_float(w.y) + a.y),
-                         __float_as_uint(__uint_as_float(w.z) + a.z), __float_as_uint(__uint_as_float(w.w) + a.w));
-        }
+        if (add)
+          w = make_uint4(__float_as_uint(__uint_as_float(w.x) + c[i].x), __float_as_uint(__uint_as_float(w.y) + c[i].y),
+                         __float_as_uint(__uint_as_float(w.z) + c[i].z), __float_as_uint(__uint_as_float(w.w) + c[i].w));
         *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + (row0 + r) * p.ld_o + col + 4 * unit) = w;
       } else {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (row0 + r) * p.ld_o + col + 8 * unit) = w;
