@@ -23,7 +23,7 @@ struct CheckpointSaveParams {
   uint8_t* q_c;        // columnwise codes or nullptr
   int64_t ld_c;
   uint8_t* s_c;
-  int32_t vec_in;      // base and row stride are multiples of 16 bytes
+  int32_t vec_in;      // base and row stride are multiples of 8 elements' bytes (16 or 32)
   int32_t vec_r, vec_c;  // codes take 8-byte stores
 };
 
@@ -35,7 +35,7 @@ struct CheckpointRestoreParams {
   int64_t ld_o;
   int32_t colwise;
   int32_t vec_q;       // codes take 8-byte loads
-  int32_t vec_out;     // output takes 16-byte stores
+  int32_t vec_out;     // likewise of the output
 };
 
 // One operand of a product: `codes` is the matrix [mn][k] (rowwise) or [k][mn] (columnwise).

@@ -130,7 +130,7 @@ int mxfp8_checkpoint_save(const mxfp8_tensor* input, mxfp8_tensor* codes_rowwise
   p.in = input->data;
   p.rows = rows;
   p.cols = cols;
-  p.vec_in = aligned(p.in, p.ld, elem_bytes(input->dtype), 16);
+  p.vec_in = aligned(p.in, p.ld, elem_bytes(input->dtype), 8 * elem_bytes(input->dtype));
   return cuda_status(mxfp8::launch_checkpoint_save(p, dtype_index(input->dtype), static_cast<cudaStream_t>(stream)),
                      "checkpoint save launch");
 }
@@ -155,7 +155,7 @@ int mxfp8_checkpoint_restore(const mxfp8_tensor* codes, const mxfp8_tensor* scal
   p.out = output->data;
   p.colwise = colwise;
   p.vec_q = aligned(p.q, p.ld_q, 1, 8);
-  p.vec_out = aligned(p.out, p.ld_o, elem_bytes(output->dtype), 16);
+  p.vec_out = aligned(p.out, p.ld_o, elem_bytes(output->dtype), 8 * elem_bytes(output->dtype));
   return cuda_status(mxfp8::launch_checkpoint_restore(p, dtype_index(output->dtype), static_cast<cudaStream_t>(stream)),
                      "checkpoint restore launch");
 }
