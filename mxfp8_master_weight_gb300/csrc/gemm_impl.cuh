@@ -101,15 +101,24 @@ __device__ __forceinline__ void write_rows(const GemmParams& p, char* stage, int
     }
   } else {  // rows that start anywhere, or end inside: an element per lane
     const int rows = p.m - row0 < 32 ? int(p.m - row0) : 32;
-    for (int r = 0; r < rows; ++r) {
-      for (int e = lane; e < width && col + e < p.n; e += 32) {
-        if (p.out_f32) {
-          const float v = *reinterpret_cast<const float*>(stage + r * 128 + (((e >> 2) ^ (r & 7)) << 4) + 4 * (e & 3));
-          store_one(p, row0 + r, col + e, v + load_addend(p, row0 + r, col + e));
-        } else {
-          static_cast<uint16_t*>(p.out)[(row0 + r) * p.ld_o + col + e] =
-              *reinterpret_cast<const uint16_t*>(stage + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + 2 * (e & 7));
-        }
+    const bool in0 = col + lane < p.n, in1 = !p.out_f32 && col + 32 + lane < p.n;
+    if (p.out_f32) {
+      const float* c = p.addend != nullptr ? p.addend + row0 * p.ld_c + col + lane : nullptr;
+      float* o = static_cast<float*>(p.out) + row0 * p.ld_o + col + lane;
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r) {
+        const float v = *reinterpret_cast<const float*>(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3));
+        if (r < rows && in0) o[r * p.ld_o] = v + (c != nullptr ? c[r * p.ld_c] : 0.0f);
+      }
+    } else {
+      uint16_t* o = static_cast<uint16_t*>(p.out) + row0 * p.ld_o + col + lane;
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r) {
+        const char* line = stage + r * 128 + 2 * (lane & 7);
+        const uint16_t v0 = *reinterpret_cast<const uint16_t*>(line + (((lane >> 3) ^ (r & 7)) << 4));
+        const uint16_t v1 = *reinterpret_cast<const uint16_t*>(line + (((4 + (lane >> 3)) ^ (r & 7)) << 4));
+        if (r < rows && in0) o[r * p.ld_o] = v0;
+        if (r < rows && in1) o[r * p.ld_o + 32] = v1;
       }
     }
   }

@@ -2,6 +2,7 @@
 #include "gemm_maps.h"
 
 #include "gemm_impl.cuh"
+#include "gemm_realign.cuh"
 
 namespace mxfp8 {
 namespace {
@@ -56,6 +57,21 @@ cudaError_t operand_map(const GemmOperand& o, int64_t k, int rows, CUtensorMap* 
 cudaError_t half_operand_map(const GemmOperand& o, int64_t k, CUtensorMap* map, const char** what) {
   return o.colwise ? codes_map(o, k, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B, map, what)
                    : codes_map(o, k, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B, map, what);
+}
+
+cudaError_t residue_maps(const GemmOperand& o, int64_t k, CUtensorMap* maps, const char** what) {
+  const int64_t rows = o.colwise ? k : o.mn, cols = o.colwise ? o.mn : k;
+  const cuuint64_t strides[1] = {cuuint64_t(16 * o.ld)};
+  const cuuint32_t box[2] = {kRawRow, 8};
+  for (int s = 0; s < kResidues; ++s) {
+    // a residue without rows takes row 0's bytes; its boxes land in rows that the matrix has not
+    const uintptr_t first = reinterpret_cast<uintptr_t>(o.codes) + (s < rows ? s * o.ld : 0);
+    const cuuint64_t dims[2] = {cuuint64_t(first % 16 + cols), cuuint64_t(s < rows ? (rows - s + 15) / 16 : 1)};
+    const cudaError_t e = encode(&maps[s], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, reinterpret_cast<const void*>(first / 16 * 16),
+                                 dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE, what);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t scale_map(const GemmOperand& o, int64_t k, int row_tiles, CUtensorMap* map, const char** what) {

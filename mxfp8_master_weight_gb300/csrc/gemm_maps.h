@@ -13,6 +13,9 @@ cudaError_t operand_map(const GemmOperand& o, int64_t k, int rows, CUtensorMap* 
 // Boxes of half as many m or n: 64 rows by 128 bytes, or (columnwise) 128 rows by 64 bytes under the
 // 64-byte swizzle.
 cudaError_t half_operand_map(const GemmOperand& o, int64_t k, CUtensorMap* map, const char** what);
+// 16 maps of an operand that is not aligned: map s has the rows 16 q + s, in boxes of 8 rows by 160
+// bytes from the 16-byte unit that holds a row's first byte.
+cudaError_t residue_maps(const GemmOperand& o, int64_t k, CUtensorMap* maps, const char** what);
 // Boxes of `row_tiles` 512-byte scale tiles, one above the other: coordinates (0, tile along k,
 // 128-row block).
 cudaError_t scale_map(const GemmOperand& o, int64_t k, int row_tiles, CUtensorMap* map, const char** what);

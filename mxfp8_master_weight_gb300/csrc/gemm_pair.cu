@@ -16,23 +16,33 @@
 // therefore share 32 columns: buffer 0 is columns 0..255, buffer 1 columns 224..479, two sets of
 // scales 480..511.  The writers drain the shared columns of a tile first; then the next
 // tile's instructions start in the other buffer while they write the rest.
+#include <type_traits>
+
 #include <cuda.h>
 
 #include "gemm_impl.cuh"
 #include "gemm_maps.h"
+#include "gemm_realign.cuh"
 
 namespace mxfp8 {
 namespace {
 
 constexpr int kMaxStages = 7;
+constexpr int kRawDepth = 3;  // raw boxes
 constexpr int kScaleBytes = 3 * kScaleTile;  // of A, and of both 128-row halves of B
-constexpr int kWriters = 8;
+// Writers: eight warps; four where eight others realign an operand.
+template <bool kRealign>
+constexpr int kWriters = kRealign ? 4 : 8;
+constexpr int kRealignGroups = 2;  // of four warps, which take the stages in turn
+constexpr int kRealignWarps = 4 * kRealignGroups + 1;  // and one that fetches
 constexpr int kWriterBytes = 4096;  // a writer's 32 rows of 128 bytes
 constexpr int kSmem = 226 * 1024;
 // What is left for stages: a stage is A's box, B's box (half a box where every tile is a half) and
 // the scales, each kind in an array of its own, which keeps the boxes on 1024-byte boundaries.
-constexpr int kStageRoom = kSmem - 1024 - kWriters * kWriterBytes - 256;
-constexpr int kThreads = 64 + 32 * kWriters;
+template <bool kRealign>
+constexpr int kStageRoom = kSmem - 1024 - kWriters<kRealign> * kWriterBytes - (kRealign ? kRawDepth * kRawBox : 0) - 384;
+template <bool kRealign>
+constexpr int kThreads = 64 + 32 * (kWriters<kRealign> + (kRealign ? kRealignWarps : 0));
 constexpr int kSecondBuffer = 224;  // first column of the second buffer of sums
 constexpr int kScaleCol = 480;
 
@@ -43,6 +53,8 @@ struct PairParams {
   int64_t whole, units;  // whole tiles first, then halves
   int32_t stages, b_bytes;
 };
+
+struct PairParamsRealign : PairParams, Residues {};
 
 struct Tile {
   int64_t tm, col;  // 256-row block; first column
@@ -57,8 +69,51 @@ __device__ __forceinline__ Tile tile_of(const PairParams& q, int64_t unit, int64
   return t;
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    k_gemm_pair(const __grid_constant__ PairParams q) {
+// The boxes that are realigned: all of them for the fetching thread (`stride` 1), for a group of writing
+// warps those of every kRealignGroups-th stage.
+struct PairWalk {
+  const PairParams& q;
+  RealignShape shape;
+  int64_t unit, step, tiles_m, tiles_n;
+  int32_t nk, kb, a_mn, b_mn;  // a_mn, b_mn: first rows of A and B of this CTA
+  uint32_t rank, a_box, b_box;
+  RingAt stage;
+  int32_t stages, stride;
+  bool second, half;
+  __device__ __forceinline__ bool valid() const { return unit < q.units && nk > 0; }
+  __device__ __forceinline__ bool first() const { return second != shape.a; }
+  __device__ __forceinline__ bool last() const { return second == shape.b; }
+  __device__ __forceinline__ RealignItem item() const {
+    return shape.item(second, second ? b_mn : a_mn, kb * kBlockK, second && half ? 64 : 128,
+                      second ? b_box + stage.slot * q.b_bytes : a_box + stage.slot * kBoxBytes);
+  }
+  __device__ __forceinline__ void tile() {
+    if (unit >= q.units) return;
+    const Tile t = tile_of(q, unit, tiles_m, tiles_n);
+    half = t.half;
+    a_mn = int32_t(t.tm * 256 + rank * 128);
+    b_mn = int32_t(t.col + rank * (half ? 64 : 128));
+  }
+  __device__ __forceinline__ void skip(int by) {  // `by` stages on
+    stage.on(by, stages);
+    kb += by;
+    if (kb < nk) return;
+    for (; kb >= nk && unit < q.units; kb -= nk) unit += step;
+    tile();
+  }
+  __device__ __forceinline__ void next() {
+    if (!last()) {
+      second = true;
+      return;
+    }
+    second = !shape.a;
+    skip(stride);
+  }
+};
+
+template <bool kRealign>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kRealign>, 1)
+    k_gemm_pair(const __grid_constant__ std::conditional_t<kRealign, PairParamsRealign, PairParams> q) {
   extern __shared__ char raw[];
   const GemmParams& p = q.g;
   // the same offset in both CTAs: their dynamic shared memory starts alike
@@ -66,30 +121,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   char* b_boxes = smem + q.stages * kBoxBytes;
   char* scales = b_boxes + q.stages * q.b_bytes;
   char* writers = scales + q.stages * kScaleBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(writers + kWriters * kWriterBytes);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 3);
+  char* raw_boxes = writers + kWriters<kRealign> * kWriterBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(raw_boxes + (kRealign ? kRawDepth * kRawBox : 0));
+  uint64_t* raw_bars = bars + 3 * kMaxStages + 3;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_bars + (kRealign ? 2 * kRawDepth : 0));
+  const RealignRing ring{raw_boxes, tc::smem_addr(raw_bars), tc::smem_addr(raw_bars + kRawDepth), kRawDepth};
   volatile uint32_t* gave_up = tmem_slot + 1;
   const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kMaxStages, sums_full = empty + 8 * kMaxStages,
-                 sums_free = sums_full + 16;
+                 sums_free = sums_full + 16, ready = sums_free + 8;
   const int warp = threadIdx.x >> 5;
   const uint32_t rank = tc::cluster_rank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < q.stages; ++s) {
-      tc::mbar_init(full + 8 * s, 1);
+      // the expected copies; realigned, also four warps of the leading CTA and the other one's word
+      tc::mbar_init(full + 8 * s, 1 + (kRealign ? 4 + 1 : 0));
+      if constexpr (kRealign) tc::mbar_init(ready + 8 * s, 4);
       tc::mbar_init(empty + 8 * s, 1);
     }
+    if constexpr (kRealign) ring.init();
     tc::mbar_init(sums_full, 1);
     tc::mbar_init(sums_full + 8, 1);
-    tc::mbar_init(sums_free, 2 * kWriters);
+    tc::mbar_init(sums_free, 2 * kWriters<kRealign>);
     *gave_up = 0;
     tc::mbar_init_fence();
-    tc::prefetch_map(&q.a);
-    tc::prefetch_map(&q.b);
-    tc::prefetch_map(&q.b_half);
-    tc::prefetch_map(&q.sa);
-    tc::prefetch_map(&q.sb);
+    if (p.k > 0) {
+      if (!kRealign || p.a.aligned) tc::prefetch_map(&q.a);
+      if (!kRealign || p.b.aligned) {
+        tc::prefetch_map(&q.b);
+        tc::prefetch_map(&q.b_half);
+      }
+      tc::prefetch_map(&q.sa);
+      tc::prefetch_map(&q.sb);
+    }
   }
   if (warp == 1) tc::tmem_alloc<2>(tc::smem_addr(tmem_slot), 512);
+  if constexpr (kRealign) {
+    if (warp == 2) prefetch_residues(q.residues, !p.a.aligned, !p.b.aligned);
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::cluster_sync();
@@ -109,15 +177,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int64_t unit = first; unit < q.units && *gave_up == 0; unit += step) {
         const Tile t = tile_of(q, unit, tiles_m, tiles_n);
         const int am = int(t.tm * 256 + rank * 128), bn = int(t.col + rank * (t.half ? 64 : 128));
-        const uint32_t bytes = kBoxBytes + (t.half ? kBoxBytes / 2 : kBoxBytes) + kScaleBytes;
+        const bool tma_a = !kRealign || p.a.aligned, tma_b = !kRealign || p.b.aligned;
+        const uint32_t bytes = (tma_a ? kBoxBytes : 0) + (tma_b ? (t.half ? kBoxBytes / 2 : kBoxBytes) : 0) + kScaleBytes;
         for (int64_t kb = 0; kb < nk; ++kb) {
           if (!tc::mbar_wait(empty + 8 * s, phase, gave_up)) break;
           const uint32_t at_a = tc::smem_addr(smem + s * kBoxBytes), at_b = tc::smem_addr(b_boxes + s * q.b_bytes),
                          at_s = tc::smem_addr(scales + s * kScaleBytes), bar = lead_full + 8 * s;
           const int k0 = int(kb * kBlockK);
           if (rank == 0) tc::mbar_expect(full + 8 * s, 2 * bytes);
-          tc::tma_load_2d_pair(at_a, &q.a, p.a.colwise ? am : k0, p.a.colwise ? k0 : am, bar);
-          tc::tma_load_2d_pair(at_b, t.half ? &q.b_half : &q.b, p.b.colwise ? bn : k0, p.b.colwise ? k0 : bn, bar);
+          if (tma_a) tc::tma_load_2d_pair(at_a, &q.a, p.a.colwise ? am : k0, p.a.colwise ? k0 : am, bar);
+          if (tma_b) tc::tma_load_2d_pair(at_b, t.half ? &q.b_half : &q.b, p.b.colwise ? bn : k0, p.b.colwise ? k0 : bn, bar);
           tc::tma_load_3d_pair(at_s, &q.sa, 0, int(scale_tile_of(kb, p.a.block)), int(2 * t.tm + rank), bar);
           tc::tma_load_3d_pair(at_s + kScaleTile, &q.sb, 0, int(scale_tile_of(kb, p.b.block)), int(t.col >> 7), bar);
           ++issued;
@@ -176,13 +245,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::commit_pair(sums_full + 8 * (nth & 1), 3);
       }
     }
+    if (kRealign && rank == 1 && tc::elect_one()) {
+      // The other CTA's realigned stages, passed on to the leading one: an arrival there is a release
+      // to the cluster, which holds a warp up for 800 cycles.
+      RingAt at{0, 0};
+      bool good = true;
+      for (int64_t unit = first; unit < q.units && good; unit += step) {
+        for (int64_t kb = 0; kb < nk && good; ++kb) {
+          good = tc::mbar_wait(ready + 8 * at.slot, at.parity, gave_up);
+          if (good) tc::mbar_arrive_cluster(full + 8 * at.slot, 0);
+          at.on(1, q.stages);
+        }
+      }
+    }
+  } else if (kRealign && warp >= 2 + kWriters<kRealign>) {
+    if constexpr (kRealign) {
+      const int w = warp - 2 - kWriters<kRealign>;
+      const bool fetches = w >= 4 * kRealignGroups;
+      const RealignShape shape(p);
+      PairWalk walk{q, shape, first, step, tiles_m, tiles_n, int32_t(nk), 0, 0, 0, rank, tc::smem_addr(smem),
+                    tc::smem_addr(b_boxes), {0, 0}, q.stages, fetches ? 1 : kRealignGroups, !shape.a, false};
+      walk.tile();
+      if (fetches) {
+        if (tc::elect_one()) realign_fetch(ring, q.residues, walk, gave_up);
+      } else {
+        Realigner ra = {};
+        ra.warp = w & 3;
+        if (shape.a) ra.init(p.a, 0);
+        if (shape.b) ra.init(p.b, 1);
+        if (nk > 0) walk.skip(w >> 2);
+        const uint32_t announce = rank == 0 ? full : ready;
+        realign_write(
+            ring, ra, walk, w >> 2, kRealignGroups, gave_up,
+            [&](const PairWalk& at) { return tc::mbar_wait(empty + 8 * at.stage.slot, at.stage.parity ^ 1, gave_up); },
+            [&](const PairWalk& at) {
+              if ((threadIdx.x & 31) == 0) tc::mbar_arrive(announce + 8 * at.stage.slot);
+            });
+      }
+    }
   } else {
     const int side = (warp - 2) >> 2;  // the first or second half of the columns
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
     uint32_t nth = 0;
     for (int64_t unit = first; unit < q.units; unit += step, ++nth) {
       const Tile t = tile_of(q, unit, tiles_m, tiles_n);
-      const int cols = t.half ? 64 : 128;  // this warp's
+      const int cols = (t.half ? 512 : 1024) / kWriters<kRealign>;  // this warp's
       const uint32_t buffer = nth & 1;
       // no two tiles' sums are ready at once that this warp has not drained: the next tile's
       // instructions wait for sums_free
@@ -226,26 +333,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 cudaError_t launch_gemm_pair(const GemmParams& g, unsigned* given_up, const DeviceInfo& dev, cudaStream_t stream,
                              const char** what) {
-  PairParams q{};
+  PairParamsRealign q{};
   q.g = g;
   q.given_up = given_up;
-  cudaError_t e = operand_map(g.a, g.k, 128, &q.a, what);
-  if (e == cudaSuccess) e = operand_map(g.b, g.k, 128, &q.b, what);
-  if (e == cudaSuccess) e = half_operand_map(g.b, g.k, &q.b_half, what);
-  if (e == cudaSuccess) e = scale_map(g.a, g.k, 1, &q.sa, what);
-  if (e == cudaSuccess) e = scale_map(g.b, g.k, 2, &q.sb, what);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_gemm_pair), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const bool realign = g.k > 0 && !(g.a.aligned && g.b.aligned);
+  cudaError_t e = cudaSuccess;
+  if (g.k > 0) {
+    if (g.a.aligned) e = operand_map(g.a, g.k, 128, &q.a, what);
+    if (e == cudaSuccess && g.b.aligned) e = operand_map(g.b, g.k, 128, &q.b, what);
+    if (e == cudaSuccess && g.b.aligned) e = half_operand_map(g.b, g.k, &q.b_half, what);
+    if (e == cudaSuccess) e = scale_map(g.a, g.k, 1, &q.sa, what);
+    if (e == cudaSuccess) e = scale_map(g.b, g.k, 2, &q.sb, what);
+  }
+  if (e == cudaSuccess && realign && !g.a.aligned) e = residue_maps(g.a, g.k, q.residues, what);
+  if (e == cudaSuccess && realign && !g.b.aligned) e = residue_maps(g.b, g.k, q.residues + kResidues, what);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((g.m + 255) / 256) * ((g.n + 255) / 256);
   const int64_t pairs = dev.sms / 2, last = tiles % pairs;
-  q.whole = last != 0 && 2 * last <= pairs ? tiles - last : tiles;
+  // the realigning warps know boxes with rows of 128 bytes only
+  const bool halves = last != 0 && 2 * last <= pairs && !(realign && !g.b.aligned && g.b.colwise);
+  q.whole = halves ? tiles - last : tiles;
   q.units = q.whole + 2 * (tiles - q.whole);
   q.b_bytes = q.whole == 0 ? kBoxBytes / 2 : kBoxBytes;
-  const int fit = kStageRoom / (kBoxBytes + q.b_bytes + kScaleBytes);
+  const int fit = (realign ? kStageRoom<true> : kStageRoom<false>) / (kBoxBytes + q.b_bytes + kScaleBytes);
   q.stages = fit < kMaxStages ? fit : kMaxStages;
   const unsigned grid = 2 * unsigned(q.units < pairs ? q.units : pairs);
-  return launch_kernel(k_gemm_pair, dim3(grid), dim3(kThreads), kSmem, stream, q);
+  auto run = [&](auto kernel, int threads, const auto& params) {
+    const cudaError_t a = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    return a != cudaSuccess ? a : launch_kernel(kernel, dim3(grid), dim3(threads), kSmem, stream, params);
+  };
+  return realign ? run(k_gemm_pair<true>, kThreads<true>, q)
+                 : run(k_gemm_pair<false>, kThreads<false>, static_cast<const PairParams&>(q));
 }
 
 }  // namespace mxfp8

@@ -8,10 +8,13 @@
 // of k.  Their partial sums stay in shared memory; after a cluster barrier each CTA adds its share of
 // the columns over the cluster in rank order and writes it.  No workspace, no atomics: the
 // result depends on the shape alone.
+#include <type_traits>
+
 #include <cuda.h>
 
 #include "gemm_impl.cuh"
 #include "gemm_maps.h"
+#include "gemm_realign.cuh"
 
 namespace mxfp8 {
 namespace {
@@ -19,6 +22,8 @@ namespace {
 constexpr int kThreads = 192;  // warp 0 fetches, warp 1 issues, four warps write
 constexpr int kMaxSplit = 8;
 constexpr int kMaxStages = 8;
+constexpr int kRealignWarps = 5;  // four write, one fetches
+constexpr int kRawDepth = 2;  // raw boxes
 
 // Stages of a CTA: two CTAs share an SM.  An operand that lies across k has 128 bytes of n per
 // row of its box however small NT is.
@@ -33,6 +38,8 @@ struct SplitParams {
   int32_t swapped;   // out[column][row]: the caller's A is B here
   int32_t stages, b_bytes, split;
 };
+
+struct SplitParamsRealign : SplitParams, Residues {};
 
 // Writes N neighbouring columns, j .. j + N - 1, of row i of the tile's matrix.
 template <int N>
@@ -87,8 +94,35 @@ __device__ __forceinline__ void add_and_store(const SplitParams& q, const float*
   store_columns<N>(q, i, j, v);
 }
 
-template <int NT>
-__global__ void __launch_bounds__(kThreads, 2) k_gemm_split(const __grid_constant__ SplitParams q) {
+// The boxes that are realigned, in the order of the stages.
+struct SplitWalk {
+  RealignShape shape;
+  int32_t am, bn, kb, k_hi;
+  uint32_t a_box, b_box;
+  int32_t b_rows, b_bytes, stages;
+  RingAt stage;
+  bool second;
+  __device__ __forceinline__ bool valid() const { return kb < k_hi; }
+  __device__ __forceinline__ bool first() const { return second != shape.a; }
+  __device__ __forceinline__ bool last() const { return second == shape.b; }
+  __device__ __forceinline__ RealignItem item() const {
+    return shape.item(second, second ? bn : am, kb * kBlockK, second ? b_rows : 128,
+                      second ? b_box + stage.slot * b_bytes : a_box + stage.slot * kBoxBytes);
+  }
+  __device__ __forceinline__ void next() {
+    if (!last()) {
+      second = true;
+      return;
+    }
+    second = !shape.a;
+    ++kb;
+    stage.on(1, stages);
+  }
+};
+
+template <int NT, bool kRealign>
+__global__ void __launch_bounds__(kThreads + (kRealign ? 32 * kRealignWarps : 0), 2) k_gemm_split(
+    const __grid_constant__ std::conditional_t<kRealign, SplitParamsRealign, SplitParams> q) {
   extern __shared__ char raw[];
   const GemmParams& p = q.g;
   constexpr uint32_t kTmemCols = NT <= 32 ? 64 : (NT <= 64 ? 128 : 256);
@@ -97,26 +131,32 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm_split(const __grid_constan
   // boxes of A, boxes of B, scales: an array of each keeps the boxes on 1024-byte boundaries
   char* b_boxes = smem + q.stages * kBoxBytes;
   char* scales = b_boxes + q.stages * q.b_bytes;
-  __shared__ uint64_t bars[2 * kMaxStages + 1];
+  char* raw_boxes = scales + q.stages * 2 * kScaleTile;
+  __shared__ uint64_t bars[2 * kMaxStages + 1 + (kRealign ? 2 * kRawDepth : 0)];
   __shared__ uint32_t tmem_slot, s_gave_up;
   volatile uint32_t* gave_up = &s_gave_up;
   const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kMaxStages, done = empty + 8 * kMaxStages;
+  const RealignRing ring{raw_boxes, done + 8, done + 8 + 8 * kRawDepth, kRawDepth};
   const int warp = threadIdx.x >> 5;
   const uint32_t rank = q.split > 1 ? tc::cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < q.stages; ++s) {
-      tc::mbar_init(full + 8 * s, 1);
+      tc::mbar_init(full + 8 * s, 1 + (kRealign ? 4 : 0));
       tc::mbar_init(empty + 8 * s, 1);
     }
+    if constexpr (kRealign) ring.init();
     tc::mbar_init(done, 1);
     s_gave_up = 0;
     tc::mbar_init_fence();
-    tc::prefetch_map(&q.a);
-    tc::prefetch_map(&q.b);
+    if (!kRealign || p.a.aligned) tc::prefetch_map(&q.a);
+    if (!kRealign || p.b.aligned) tc::prefetch_map(&q.b);
     tc::prefetch_map(&q.sa);
     tc::prefetch_map(&q.sb);
   }
   if (warp == 1) tc::tmem_alloc<1>(tc::smem_addr(&tmem_slot), kTmemCols);
+  if constexpr (kRealign) {
+    if (warp == 2) prefetch_residues(q.residues, !p.a.aligned, !p.b.aligned);
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -133,13 +173,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm_split(const __grid_constan
       uint32_t phase = 1;
       int64_t issued = 0;
       const int am = int(tm * 128), bn = int(tn * NT);
+      const bool tma_a = !kRealign || p.a.aligned, tma_b = !kRealign || p.b.aligned;
       for (int64_t kb = k_lo; kb < k_hi; ++kb) {
         if (!tc::mbar_wait(empty + 8 * s, phase, gave_up)) break;
         const uint32_t at_s = tc::smem_addr(scales + s * 2 * kScaleTile), bar = full + 8 * s;
         const int k0 = int(kb * kBlockK);
-        tc::mbar_expect(bar, uint32_t(kBoxBytes + q.b_bytes + 2 * kScaleTile));
-        tc::tma_load_2d(tc::smem_addr(smem + s * kBoxBytes), &q.a, p.a.colwise ? am : k0, p.a.colwise ? k0 : am, bar);
-        tc::tma_load_2d(tc::smem_addr(b_boxes + s * q.b_bytes), &q.b, p.b.colwise ? bn : k0, p.b.colwise ? k0 : bn, bar);
+        tc::mbar_expect(bar, uint32_t((tma_a ? kBoxBytes : 0) + (tma_b ? q.b_bytes : 0) + 2 * kScaleTile));
+        if (tma_a) tc::tma_load_2d(tc::smem_addr(smem + s * kBoxBytes), &q.a, p.a.colwise ? am : k0, p.a.colwise ? k0 : am, bar);
+        if (tma_b) tc::tma_load_2d(tc::smem_addr(b_boxes + s * q.b_bytes), &q.b, p.b.colwise ? bn : k0, p.b.colwise ? k0 : bn, bar);
         tc::tma_load_3d(at_s, &q.sa, 0, int(scale_tile_of(kb, p.a.block)), int(tm), bar);
         tc::tma_load_3d(at_s + kScaleTile, &q.sb, 0, int(scale_tile_of(kb, p.b.block)), bn >> 7, bar);
         ++issued;
@@ -184,13 +225,34 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm_split(const __grid_constan
       }
       tc::commit(done);
     }
+  } else if (kRealign && warp >= 6) {
+    if constexpr (kRealign) {
+      const RealignShape shape(p);
+      const SplitWalk walk{shape, int32_t(tm * 128), int32_t(tn * NT), int32_t(k_lo), int32_t(k_hi), tc::smem_addr(smem),
+                           tc::smem_addr(b_boxes), p.b.colwise ? 128 : NT, q.b_bytes, q.stages, {0, 0}, !shape.a};
+      if (warp >= 10) {
+        if (tc::elect_one()) realign_fetch(ring, q.residues, walk, gave_up);
+      } else {
+        Realigner ra = {};
+        ra.warp = warp - 6;
+        if (shape.a) ra.init(p.a, 0);
+        if (shape.b) ra.init(p.b, 1);
+        realign_write(
+            ring, ra, walk, 0, 1, gave_up,
+            [&](const SplitWalk& at) { return tc::mbar_wait(empty + 8 * at.stage.slot, at.stage.parity ^ 1, gave_up); },
+            [&](const SplitWalk& at) {
+              if ((threadIdx.x & 31) == 0) tc::mbar_arrive(full + 8 * at.stage.slot);
+            });
+      }
+    }
   }
   __syncwarp();
   // split: the partial sums, [NT columns][128 rows], over the stages' memory
   float* part = reinterpret_cast<float*>(smem);
   const int row = 32 * (warp & 3) + (threadIdx.x & 31);
   const int64_t i = tm * 128 + row, j = tn * NT;
-  if (warp >= 2) {
+  const bool writer = warp >= 2 && warp < 6;
+  if (writer) {
     tc::mbar_wait(done, 0, gave_up);
     tc::fence_after_sync();
 #pragma unroll
@@ -214,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm_split(const __grid_constan
   __syncthreads();
   if (q.split > 1) {
     tc::cluster_sync();
-    if (warp >= 2) {
+    if (writer) {
       const int share = NT / q.split;
       for (int c = share * int(rank); c < share * int(rank + 1);) {
         if (share >= 8) {
@@ -239,25 +301,27 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm_split(const __grid_constan
 
 template <int NT>
 cudaError_t launch(const GemmParams& g, bool swapped, int split, unsigned* given_up, cudaStream_t stream, const char** what) {
-  SplitParams q{};
+  SplitParamsRealign q{};
   q.g = g;
   q.given_up = given_up;
   q.swapped = swapped;
   q.split = split;
   q.b_bytes = columns_bytes<NT>(g.b.colwise != 0);
-  const int stage = kBoxBytes + q.b_bytes + 2 * kScaleTile, fit = (kSmemBudget - 1024) / stage;
+  const bool realign = !(g.a.aligned && g.b.aligned);
+  const int stage = kBoxBytes + q.b_bytes + 2 * kScaleTile, room = kSmemBudget - 1024;
+  const int raw = realign ? kRawDepth * kRawBox : 0, fit = (room - raw) / stage;
   q.stages = fit < kMaxStages ? fit : kMaxStages;
-  const int smem = 1024 + q.stages * stage;
-  cudaError_t e = operand_map(g.a, g.k, 128, &q.a, what);
-  if (e == cudaSuccess) e = operand_map(g.b, g.k, g.b.colwise ? 128 : NT, &q.b, what);
+  const int smem = 1024 + q.stages * stage + raw;
+  cudaError_t e = g.a.aligned ? operand_map(g.a, g.k, 128, &q.a, what) : cudaSuccess;
+  if (e == cudaSuccess && g.b.aligned) e = operand_map(g.b, g.k, g.b.colwise ? 128 : NT, &q.b, what);
   if (e == cudaSuccess) e = scale_map(g.a, g.k, 1, &q.sa, what);
   if (e == cudaSuccess) e = scale_map(g.b, g.k, 1, &q.sb, what);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_gemm_split<NT>), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget);
+  if (e == cudaSuccess && !g.a.aligned) e = residue_maps(g.a, g.k, q.residues, what);
+  if (e == cudaSuccess && !g.b.aligned) e = residue_maps(g.b, g.k, q.residues + kResidues, what);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(((g.m + 127) / 128) * ((g.n + NT - 1) / NT) * split));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads + (realign ? 32 * kRealignWarps : 0));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -269,7 +333,12 @@ cudaError_t launch(const GemmParams& g, bool swapped, int split, unsigned* given
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_gemm_split<NT>, q);
+  auto run = [&](auto kernel, const auto& params) {
+    const cudaError_t a = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget);
+    return a != cudaSuccess ? a : cudaLaunchKernelEx(&cfg, kernel, params);
+  };
+  return realign ? run(k_gemm_split<NT, true>, q) : run(k_gemm_split<NT, false>, static_cast<const SplitParams&>(q));
 }
 
 }  // namespace

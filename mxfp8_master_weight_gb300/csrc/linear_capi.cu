@@ -187,6 +187,7 @@ int mxfp8_gemm(const mxfp8_tensor* a, const mxfp8_tensor* a_scale, const mxfp8_t
     if (int rc = check_scales(s, sname, mn, ceil_div(k, block))) return rc;
     o->codes = static_cast<const uint8_t*>(t->data);
     o->scale = static_cast<const uint8_t*>(s->data);
+    if ((colwise ? k : mn) == 1) o->ld = (o->ld + 15) / 16 * 16;  // no second row: any stride will do
     o->aligned = aligned(o->codes, o->ld, 1, 16);
     return int(MXFP8_OK);
   };
