@@ -271,8 +271,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kRealign>, 
       } else {
         Realigner ra = {};
         ra.warp = w & 3;
-        if (shape.a) ra.init(p.a, 0);
-        if (shape.b) ra.init(p.b, 1);
+        if (shape.a) ra.a = ra.places(p.a);
+        if (shape.b) ra.b = ra.places(p.b);
         if (nk > 0) walk.skip(w >> 2);
         const uint32_t announce = rank == 0 ? full : ready;
         realign_write(
@@ -350,9 +350,7 @@ cudaError_t launch_gemm_pair(const GemmParams& g, unsigned* given_up, const Devi
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((g.m + 255) / 256) * ((g.n + 255) / 256);
   const int64_t pairs = dev.sms / 2, last = tiles % pairs;
-  // the realigning warps know boxes with rows of 128 bytes only
-  const bool halves = last != 0 && 2 * last <= pairs && !(realign && !g.b.aligned && g.b.colwise);
-  q.whole = halves ? tiles - last : tiles;
+  q.whole = last != 0 && 2 * last <= pairs ? tiles - last : tiles;
   q.units = q.whole + 2 * (tiles - q.whole);
   q.b_bytes = q.whole == 0 ? kBoxBytes / 2 : kBoxBytes;
   const int fit = (realign ? kStageRoom<true> : kStageRoom<false>) / (kBoxBytes + q.b_bytes + kScaleBytes);

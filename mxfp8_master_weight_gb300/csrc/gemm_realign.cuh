@@ -15,7 +15,7 @@
 // What bounds it: the raw boxes' way through shared memory, about as much again as the stages' own
 // (1.0 us per 128 values of k of a 256 x 256 tile, 0.3 aligned).  Tried first: a bulk copy per row (128
 // per box, about 30 cycles each) and cp.async of the units (an SM keeps too few of them under way; in
-// the writing warps, the proxy fence waits for them): 8192 x 5001 x 3001 490 and 264 us, with maps 228 us.
+// the writing warps, the proxy fence waits for them): 8192 x 5001 x 3001 490 and 264 us, with maps 232 us.
 #pragma once
 
 #include <type_traits>
@@ -35,6 +35,7 @@ constexpr int kRawBox = kResidues * kRawPart;
 struct RealignItem {
   int32_t row0, col;
   int32_t rows;    // 128, or fewer for narrow tiles
+  bool narrow;     // rows of 64 bytes under the 64-byte swizzle
   int32_t live;    // rows from row0 to the end of the matrix
   uint32_t dst;    // the stage's box in shared memory
   bool second;     // of B
@@ -64,10 +65,11 @@ struct RealignShape {
   __device__ __forceinline__ explicit RealignShape(const GemmParams& p)
       : rows_a(int32_t(p.a.colwise ? p.k : p.m)), rows_b(int32_t(p.b.colwise ? p.k : p.n)), across_a(p.a.colwise),
         across_b(p.b.colwise), a(!p.a.aligned), b(!p.b.aligned) {}
-  __device__ __forceinline__ RealignItem item(bool second, int32_t mn, int32_t k0, int32_t rows, uint32_t dst) const {
+  // A box of `extent` rows of A or B at (mn, k0).
+  __device__ __forceinline__ RealignItem item(bool second, int32_t mn, int32_t k0, int32_t extent, uint32_t dst) const {
     const bool across = second ? across_b : across_a;
     const int32_t row0 = across ? k0 : mn;
-    return {row0, across ? mn : k0, rows, (second ? rows_b : rows_a) - row0, dst, second};
+    return {row0, across ? mn : k0, across ? 128 : extent, across && extent == 64, (second ? rows_b : rows_a) - row0, dst, second};
   }
   __device__ __forceinline__ uint32_t per_stage() const { return a && b ? 2 : 1; }
 };
@@ -121,49 +123,66 @@ __device__ __forceinline__ void realign_fetch(const RealignRing& ring, const CUt
   }
 }
 
-// One of the four warps of a group: residues 4 w .. 4 w + 3 of a box.  Lane l writes word l % 4 of the
-// units of rows 16 (l / 4) + s.
+// Lane l of warp w (0 .. 3) of a group writes word l % 4 of the units of rows 16 (l / 4) + s, s = 4 w .. 4 w + 3.
+// place: for each s the byte in the raw box, and shift << 16, of that word of unit 0.
+template <bool kPlain>
+__device__ __forceinline__ void realign_box(uint4 place, uint32_t from, uint32_t dst, int warp, int rows, int live, bool narrow) {
+  const int lane = threadIdx.x & 31, q = lane >> 2;
+  if (16 * q >= rows) return;
+  const uint32_t p[4] = {place.x, place.y, place.z, place.w};
+  const uint32_t to = dst + 16 * q * 128 + 4 * (lane & 3);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t src = from + (p[g] & 0xffffu), sh = p[g] >> 16, s = 4 * warp + g;
+    uint32_t lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t u = 16 * ((i + q) & 7);
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(lo[i]) : "r"(src + u));
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(hi[i]) : "r"(src + u + 4));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lo[i] = __funnelshift_r(lo[i], hi[i], sh);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t u = (i + q) & 7, r = 16 * q + s;
+      if constexpr (kPlain) {
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + s * 128 + ((u ^ (s & 7)) << 4)), "r"(lo[i]) : "memory");
+      } else {
+        const uint32_t at = narrow ? dst + r * 64 + ((u ^ (r >> 1 & 3)) << 4) + 4 * (lane & 3) : to + s * 128 + ((u ^ (s & 7)) << 4);
+        if (!narrow || u < 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(int(r) < live ? lo[i] : 0u) : "memory");
+      }
+    }
+  }
+}
+// Boxes with rows of 64 bytes, and those whose matrix has fewer than 16 rows left (residues without rows
+// have no map of zeros).  Out of line: inside the loop these cases cost a fifth of the others' rate.
+static __device__ __noinline__ void realign_rare_box(uint4 place, uint32_t from, uint32_t dst, int warp, int rows, int live, bool narrow) {
+  realign_box<false>(place, from, dst, warp, rows, live, narrow);
+}
+
+// One of the four warps of a group.
 struct Realigner {
-  uint32_t place[2][4];  // of A and B: byte in the raw box, and shift << 16, of the lane's word of unit 0
+  uint4 a, b;  // places of A and B
   int warp;
 
-  __device__ __forceinline__ void init(const GemmOperand& o, int side) {
+  __device__ __forceinline__ uint4 places(const GemmOperand& o) const {
     const int lane = threadIdx.x & 31;
     const uint32_t base = uint32_t(reinterpret_cast<uintptr_t>(o.codes)), ld = uint32_t(o.ld);
+    uint32_t p[4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const uint32_t s = 4 * warp + g, off = (base + s * ld) & 15;
-      place[side][g] = (s * kRawPart + (lane >> 2) * kRawRow + (off & ~3u) + 4 * (lane & 3)) | ((off & 3) * 8) << 16;
+      p[g] = (s * kRawPart + (lane >> 2) * kRawRow + (off & ~3u) + 4 * (lane & 3)) | ((off & 3) * 8) << 16;
     }
+    return make_uint4(p[0], p[1], p[2], p[3]);
   }
 
   __device__ __forceinline__ void write(const RealignItem& it, const char* box) const {
-    const int lane = threadIdx.x & 31, q = lane >> 2;
     const uint32_t from = tc::smem_addr(box);
-    const uint32_t dst = it.dst + (16 * q) * 128 + 4 * (lane & 3);
-    if (16 * q >= it.rows) return;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const uint32_t p = it.second ? place[1][g] : place[0][g];
-      const uint32_t src = from + (p & 0xffffu), sh = p >> 16, s = 4 * warp + g;
-      uint32_t lo[8], hi[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t u = 16 * ((i + q) & 7);
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(lo[i]) : "r"(src + u));
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(hi[i]) : "r"(src + u + 4));
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) lo[i] = __funnelshift_r(lo[i], hi[i], sh);
-      if (it.live < kResidues) {  // residues without rows have no map of zeros
-#pragma unroll
-        for (int i = 0; i < 8; ++i) lo[i] = 16 * q + int(s) < it.live ? lo[i] : 0u;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + s * 128 + ((((i + q) & 7) ^ (s & 7)) << 4)), "r"(lo[i])
-                     : "memory");
-    }
+    const uint4 place = make_uint4(it.second ? b.x : a.x, it.second ? b.y : a.y, it.second ? b.z : a.z, it.second ? b.w : a.w);
+    if (!it.narrow && it.live >= kResidues) realign_box<true>(place, from, it.dst, warp, it.rows, 0, false);
+    else realign_rare_box(place, from, it.dst, warp, it.rows, it.live, it.narrow);
   }
 };
 

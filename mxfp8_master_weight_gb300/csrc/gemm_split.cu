@@ -106,7 +106,7 @@ struct SplitWalk {
   __device__ __forceinline__ bool first() const { return second != shape.a; }
   __device__ __forceinline__ bool last() const { return second == shape.b; }
   __device__ __forceinline__ RealignItem item() const {
-    return shape.item(second, second ? bn : am, kb * kBlockK, second ? b_rows : 128,
+    return shape.item(second, second ? bn : am, kb * kBlockK, second && !shape.across_b ? b_rows : 128,
                       second ? b_box + stage.slot * b_bytes : a_box + stage.slot * kBoxBytes);
   }
   __device__ __forceinline__ void next() {
@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(kThreads + (kRealign ? 32 * kRealignWarps : 0)
       } else {
         Realigner ra = {};
         ra.warp = warp - 6;
-        if (shape.a) ra.init(p.a, 0);
-        if (shape.b) ra.init(p.b, 1);
+        if (shape.a) ra.a = ra.places(p.a);
+        if (shape.b) ra.b = ra.places(p.b);
         realign_write(
             ring, ra, walk, 0, 1, gave_up,
             [&](const SplitWalk& at) { return tc::mbar_wait(empty + 8 * at.stage.slot, at.stage.parity ^ 1, gave_up); },
