@@ -50,15 +50,21 @@ __device__ __forceinline__ void write_rows(const GemmParams& p, char* stage, int
   const int lane = threadIdx.x & 31, unit = lane & 7;
   const int width = p.out_f32 ? 32 : 64;
   const bool vec = p.vec_out && col + width <= p.n;
-  float4 c[8];
-  const bool add = p.out_f32 && p.addend != nullptr && vec;
-  if (add) {  // on their way before the sums are
+  const bool add = p.out_f32 && p.addend != nullptr;
+  const int rows = p.m - row0 < 32 ? int(p.m - row0) : 32;
+  float c[32];  // the addend's values, on their way before the sums are: as they will be stored
+  if (add && vec) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = 4 * i + (lane >> 3);
-      c[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (row0 + r < p.m) c[i] = *reinterpret_cast<const float4*>(p.addend + (row0 + r) * p.ld_c + col + 4 * unit);
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (r < rows) a = *reinterpret_cast<const float4*>(p.addend + (row0 + r) * p.ld_c + col + 4 * unit);
+      c[4 * i] = a.x; c[4 * i + 1] = a.y; c[4 * i + 2] = a.z; c[4 * i + 3] = a.w;
     }
+  } else if (add) {
+    const float* a = p.addend + row0 * p.ld_c + col + lane;
+#pragma unroll
+    for (int r = 0; r < 32; ++r, a += p.ld_c) c[r] = r < rows && col + lane < p.n ? *a : 0.0f;
   }
   if (p.out_f32) {
     float v[32];
@@ -88,37 +94,35 @@ __device__ __forceinline__ void write_rows(const GemmParams& p, char* stage, int
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = 4 * i + (lane >> 3);
-      if (row0 + r >= p.m) continue;
+      if (r >= rows) continue;
       uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((unit ^ (r & 7)) << 4));
       if (p.out_f32) {
         if (add)
-          w = make_uint4(__float_as_uint(__uint_as_float(w.x) + c[i].x), __float_as_uint(__uint_as_float(w.y) + c[i].y),
-                         __float_as_uint(__uint_as_float(w.z) + c[i].z), __float_as_uint(__uint_as_float(w.w) + c[i].w));
+          w = make_uint4(__float_as_uint(__uint_as_float(w.x) + c[4 * i]), __float_as_uint(__uint_as_float(w.y) + c[4 * i + 1]),
+                         __float_as_uint(__uint_as_float(w.z) + c[4 * i + 2]), __float_as_uint(__uint_as_float(w.w) + c[4 * i + 3]));
         *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + (row0 + r) * p.ld_o + col + 4 * unit) = w;
       } else {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (row0 + r) * p.ld_o + col + 8 * unit) = w;
       }
     }
   } else {  // rows that start anywhere, or end inside: an element per lane
-    const int rows = p.m - row0 < 32 ? int(p.m - row0) : 32;
     const bool in0 = col + lane < p.n, in1 = !p.out_f32 && col + 32 + lane < p.n;
     if (p.out_f32) {
-      const float* c = p.addend != nullptr ? p.addend + row0 * p.ld_c + col + lane : nullptr;
       float* o = static_cast<float*>(p.out) + row0 * p.ld_o + col + lane;
-#pragma unroll 8
-      for (int r = 0; r < 32; ++r) {
+#pragma unroll
+      for (int r = 0; r < 32; ++r, o += p.ld_o) {
         const float v = *reinterpret_cast<const float*>(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3));
-        if (r < rows && in0) o[r * p.ld_o] = v + (c != nullptr ? c[r * p.ld_c] : 0.0f);
+        if (r < rows && in0) *o = add ? v + c[r] : v;
       }
     } else {
       uint16_t* o = static_cast<uint16_t*>(p.out) + row0 * p.ld_o + col + lane;
 #pragma unroll 8
-      for (int r = 0; r < 32; ++r) {
+      for (int r = 0; r < 32; ++r, o += p.ld_o) {
         const char* line = stage + r * 128 + 2 * (lane & 7);
         const uint16_t v0 = *reinterpret_cast<const uint16_t*>(line + (((lane >> 3) ^ (r & 7)) << 4));
         const uint16_t v1 = *reinterpret_cast<const uint16_t*>(line + (((4 + (lane >> 3)) ^ (r & 7)) << 4));
-        if (r < rows && in0) o[r * p.ld_o] = v0;
-        if (r < rows && in1) o[r * p.ld_o + 32] = v1;
+        if (r < rows && in0) o[0] = v0;
+        if (r < rows && in1) o[32] = v1;
       }
     }
   }
