@@ -265,9 +265,9 @@ __global__ void __launch_bounds__(kThreads) k_checkpoint_restore(const __grid_co
   const uint32_t rb = blockIdx.x / tcols, cb = blockIdx.x % tcols;
   const int t = threadIdx.x, c8 = t % 16 * 8, r0 = t / 16;
   const int64_t col = int64_t(cb) * kTile + c8, row = int64_t(rb) * kTile + r0;
-  if (col >= p.cols || row >= p.rows) return;
-  const int n = int(p.cols - col < 8 ? p.cols - col : 8);
-  const int left = int(p.rows - row < kTile ? p.rows - row : kTile);
+  const int n = int(p.cols - col < 8 ? (p.cols > col ? p.cols - col : 0) : 8);
+  const int left = n == 0 ? 0 : int(p.rows - row < kTile ? (p.rows > row ? p.rows - row : 0) : kTile);
+  if (left == 0 && p.vec_out) return;  // (else the warp's rows go out together)
   const uint8_t* src = p.q + row * p.ld_q + col;
   const int64_t q_step = kRowStep * p.ld_q, o_step = kRowStep * p.ld_o * T::kBytes;
   char* dst = static_cast<char*>(p.out) + (row * p.ld_o + col) * T::kBytes;
@@ -303,6 +303,52 @@ __global__ void __launch_bounds__(kThreads) k_checkpoint_restore(const __grid_co
   if constexpr (kCol) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] = scale_value(byte[k]);
+  }
+  if (!p.vec_out) {
+    // Rows that start anywhere: a warp's two rows go through its own shared memory, and out again as
+    // 32-bit words aligned in the output, neighbours across the lanes (BF16: a lone value at
+    // either end where the row starts between words).
+    __shared__ __align__(16) char s_rows[kThreads / 32][2][kTile * T::kBytes];
+    const int lane = t & 31, width = int(p.cols - int64_t(cb) * kTile < kTile ? p.cols - int64_t(cb) * kTile : kTile);
+    const int wrow = r0 & ~1;  // the warp's first row
+    const int64_t row1 = int64_t(rb) * kTile + wrow;
+    const int wleft = int(p.rows - row1 < kTile ? p.rows - row1 : kTile);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      if constexpr (!kCol) {
+        const float one = scale_value(byte[i]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = one;
+      }
+      const Eight<T> e = decode8<T>(q[i], f);
+#pragma unroll
+      for (int k = 0; k < Eight<T>::W; k += 4)
+        *reinterpret_cast<uint4*>(&s_rows[t / 32][r0 & 1][c8 * T::kBytes + 4 * k]) = make_uint4(e.w[k], e.w[k + 1], e.w[k + 2], e.w[k + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (kRowStep * i + h >= wleft) break;
+        const char* line = s_rows[t / 32][h];
+        char* o = static_cast<char*>(p.out) + ((row1 + kRowStep * i + h) * p.ld_o + int64_t(cb) * kTile) * T::kBytes;
+        if constexpr (T::kBytes == 4) {
+#pragma unroll
+          for (int c = 0; c < kTile; c += 32)
+            if (c + lane < width) reinterpret_cast<uint32_t*>(o)[c + lane] = reinterpret_cast<const uint32_t*>(line)[c + lane];
+        } else {
+          const int head = int(reinterpret_cast<uintptr_t>(o) >> 1) & 1;
+          const uint16_t* l = reinterpret_cast<const uint16_t*>(line) + head;
+          uint32_t* words = reinterpret_cast<uint32_t*>(o + 2 * head);
+          const int n2 = (width - head) / 2;
+#pragma unroll
+          for (int c = 0; c < kTile / 2; c += 32)
+            if (c + lane < n2) words[c + lane] = l[2 * (c + lane)] | uint32_t(l[2 * (c + lane) + 1]) << 16;
+          if (lane == 0 && head) *reinterpret_cast<uint16_t*>(o) = *reinterpret_cast<const uint16_t*>(line);
+          if (lane == 1 && ((width - head) & 1)) reinterpret_cast<uint16_t*>(o)[width - 1] = reinterpret_cast<const uint16_t*>(line)[width - 1];
+        }
+      }
+      __syncwarp();
+    }
+    return;
   }
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {

@@ -529,20 +529,51 @@ __device__ __forceinline__ void ring_sum(float (&v)[N], RingHead* h, int& half) 
 }
 
 // What thread 0 fetches: rows blockIdx.x, blockIdx.x + gridDim.x, ... of one or two operands, in
-// that order, into the slots in turn.
+// that order, into the slots in turn.  Rows that do not start on 16 bytes (kVec false) land as many bytes
+// into their slot as they start into their first 16-byte unit; the units at a row's ends are copied
+// whole, but for those that reach past the matrix, whose bytes the thread copies.
 struct RingFeed {
   RingHead* h;
   char* slots;
   const char *a, *b;
   int64_t a_pitch, b_pitch, row, rows;
   uint32_t a_bytes, b_bytes, issued;
+  struct Units {
+    uintptr_t from, to;
+  };
+  // The whole units of a row of `bytes` (64 at least) that lie inside the matrix; copies the other bytes.
+  __device__ __forceinline__ Units ends(char* slot, const char* m, int64_t pitch, uint32_t bytes) const {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(m), p = lo + row * pitch, end = p + bytes;
+    const uintptr_t hi = lo + (rows - 1) * pitch + bytes, origin = p & ~uintptr_t(15);
+    Units u{origin, (end + 15) & ~uintptr_t(15)};
+    if (u.from < lo) u.from = (p + 15) & ~uintptr_t(15);
+    if (u.to > hi) u.to = end & ~uintptr_t(15);
+    for (uintptr_t q = p; q < u.from; ++q) slot[q - origin] = *reinterpret_cast<const char*>(q);
+    for (uintptr_t q = u.to; q < end; ++q) slot[q - origin] = *reinterpret_cast<const char*>(q);
+    return u;
+  }
+  template <bool kVec>
   __device__ __forceinline__ void next(const Ring& ring) {
     if (row >= rows) return;
     const uint32_t s = issued % uint32_t(ring.slots);
-    const uint32_t bar = tc::smem_addr(&h->full[s]), dst = tc::smem_addr(slots + s * ring.slot_bytes);
-    tc::mbar_expect(bar, a_bytes + b_bytes);
-    tc::bulk_load(dst, a + row * a_pitch, a_bytes, bar);
-    if (b_bytes != 0) tc::bulk_load(dst + ring.second, b + row * b_pitch, b_bytes, bar);
+    char* slot = slots + s * ring.slot_bytes;
+    const uint32_t bar = tc::smem_addr(&h->full[s]), dst = tc::smem_addr(slot);
+    if constexpr (kVec) {
+      tc::mbar_expect(bar, a_bytes + b_bytes);
+      tc::bulk_load(dst, a + row * a_pitch, a_bytes, bar);
+      if (b_bytes != 0) tc::bulk_load(dst + ring.second, b + row * b_pitch, b_bytes, bar);
+    } else {
+      auto copy = [&](uint32_t to, const char* m, int64_t pitch, const Units& u) {
+        const uintptr_t origin = reinterpret_cast<uintptr_t>(m + row * pitch) & ~uintptr_t(15);
+        tc::bulk_load(to + uint32_t(u.from - origin), reinterpret_cast<const void*>(u.from), uint32_t(u.to - u.from), bar);
+      };
+      const Units ua = ends(slot, a, a_pitch, a_bytes);
+      Units ub{0, 0};
+      if (b_bytes != 0) ub = ends(slot + ring.second, b, b_pitch, b_bytes);
+      tc::mbar_expect(bar, uint32_t(ua.to - ua.from) + uint32_t(ub.to - ub.from));
+      copy(dst, a, a_pitch, ua);
+      if (b_bytes != 0) copy(dst + ring.second, b, b_pitch, ub);
+    }
     ++issued;
     row += gridDim.x;
   }
@@ -559,17 +590,67 @@ struct RingFeed {
 };
 
 // Barriers and the first fills.
+template <bool kVec>
 __device__ __forceinline__ void ring_start(RingFeed& feed, uint32_t* gave_up, const Ring& ring) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < ring.slots; ++i) tc::mbar_init(tc::smem_addr(&feed.h->full[i]), 1);
     *gave_up = 0;
     tc::mbar_init_fence();
-    for (int i = 0; i < ring.slots; ++i) feed.next(ring);
+    for (int i = 0; i < ring.slots; ++i) feed.next<kVec>(ring);
   }
   __syncthreads();
 }
 
-template <class T, int TH, int NV, int BLOCKS>
+// Column of element k of piece i: eight neighbours (kVec), or neighbours across the threads.
+template <bool kVec, int TH>
+__device__ __forceinline__ int ring_col(int i, int k) {
+  return kVec ? (int(threadIdx.x) + i * TH) * 8 + k : (i * 8 + k) * TH + int(threadIdx.x);
+}
+// A piece of a row in shared memory; zeros past the row.
+template <class T, bool kVec, int TH>
+__device__ __forceinline__ Eight ring_piece(const char* row, int i, int cols) {
+  if constexpr (kVec) {
+    return load_eight<T>(row, ring_col<true, TH>(i, 0), ring_col<true, TH>(i, 0) < cols ? 8 : 0, true);
+  } else {
+    Eight e;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = ring_col<false, TH>(i, k);
+      const uint32_t b = c < cols ? load_bits<T>(row, c) : 0u;
+      e.v[k] = T::kBytes == 4 ? __uint_as_float(b) : __uint_as_float(b << 16);
+    }
+    return e;
+  }
+}
+template <bool kVec, int TH>
+__device__ __forceinline__ Eight ring_param(const void* base, int bf16, int i, int cols) {
+  if constexpr (kVec) {
+    const int col = ring_col<true, TH>(i, 0);
+    return load_param(base, bf16, col, valid(cols, col), true);
+  } else {
+    const char* p = static_cast<const char*>(base);
+    return bf16 ? ring_piece<BF16T, false, TH>(p, i, cols) : ring_piece<F32T, false, TH>(p, i, cols);
+  }
+}
+template <class T, bool kVec, int TH>
+__device__ __forceinline__ void ring_store(void* base, int64_t row, int i, int cols, const Eight& e) {
+  if constexpr (kVec) {
+    if (ring_col<true, TH>(i, 0) < cols) store_eight<T>(base, row + ring_col<true, TH>(i, 0), e, 8, true);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = ring_col<false, TH>(i, k);
+      if (c < cols) store_bits<T>(base, row + c, T::kBytes == 4 ? __float_as_uint(e.v[k]) : bf16x2_rn(e.v[k], 0.0f));
+    }
+  }
+}
+// Bytes that a row starts into its first 16-byte unit, which is where its slot holds it.
+template <bool kVec>
+__device__ __forceinline__ int ring_offset(const void* base, int64_t byte) {
+  return kVec ? 0 : int((reinterpret_cast<uintptr_t>(base) + byte) & 15);
+}
+
+template <class T, bool kVec, int TH, int NV, int BLOCKS>
 __global__ void __launch_bounds__(TH, BLOCKS)
     k_norm_forward_ring(const __grid_constant__ NormForwardParams p, int wbf16, Ring ring, unsigned* given_up) {
   extern __shared__ __align__(128) char smem[];
@@ -580,7 +661,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
   grid_dependency_sync();
   RingFeed feed{h, slots, static_cast<const char*>(p.x), nullptr, p.ld_x * T::kBytes, 0, blockIdx.x, p.rows,
                 uint32_t(p.cols * T::kBytes), 0, 0};
-  ring_start(feed, &s_gave_up, ring);
+  ring_start<kVec>(feed, &s_gave_up, ring);
   const int t = threadIdx.x;
   {
     const int cols = int(p.cols);
@@ -588,10 +669,9 @@ __global__ void __launch_bounds__(TH, BLOCKS)
     Eight w[NV], b[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (t + i * TH) * 8;
-      w[i] = load_param(p.weight, wbf16, col, valid(cols, col), true);
+      w[i] = ring_param<kVec, TH>(p.weight, wbf16, i, cols);
       b[i] = {};
-      if (p.bias != nullptr) b[i] = load_param(p.bias, wbf16, col, valid(cols, col), true);
+      if (p.bias != nullptr) b[i] = ring_param<kVec, TH>(p.bias, wbf16, i, cols);
     }
     int s = 0, half = 0;
     uint32_t phase = 0;
@@ -599,26 +679,24 @@ __global__ void __launch_bounds__(TH, BLOCKS)
       // a thread whose wait was given up still goes through the row's barriers, so that no other
       // waits for it; the row is not written
       const bool good = tc::mbar_wait(tc::smem_addr(&h->full[s]), phase, gave_up);
-      const char* src = slots + s * ring.slot_bytes;
+      const char* src = slots + s * ring.slot_bytes + ring_offset<kVec>(p.x, row * p.ld_x * T::kBytes);
       Eight x[NV];
       float sum[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int col = (t + i * TH) * 8;
-        x[i] = load_eight<T>(src, col, col < cols ? 8 : 0, true);
+        x[i] = ring_piece<T, kVec, TH>(src, i, cols);
 #pragma unroll
         for (int k = 0; k < 8; ++k) sum[0] += x[i].v[k];
       }
       ring_sum<TH>(sum, h, half);
-      if (t == 0) feed.next(ring);  // every thread has the row in registers
+      if (t == 0) feed.next<kVec>(ring);  // every thread has the row in registers
       const float mean = sum[0] * inv;
       sum[0] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const bool in = (t + i * TH) * 8 < cols;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          x[i].v[k] = in ? x[i].v[k] - mean : 0.0f;
+          x[i].v[k] = ring_col<kVec, TH>(i, kVec ? 0 : k) < cols ? x[i].v[k] - mean : 0.0f;
           sum[0] += x[i].v[k] * x[i].v[k];
         }
       }
@@ -630,13 +708,10 @@ __global__ void __launch_bounds__(TH, BLOCKS)
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int col = (t + i * TH) * 8;
-        if (col < cols && good) {
-          Eight y;
+        Eight y;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) y.v[k] = x[i].v[k] * rstd * w[i].v[k] + b[i].v[k];
-          store_eight<T>(p.y, row * p.ld_y + col, y, 8, true);
-        }
+        for (int k = 0; k < 8; ++k) y.v[k] = x[i].v[k] * rstd * w[i].v[k] + b[i].v[k];
+        if (good) ring_store<T, kVec, TH>(p.y, row * p.ld_y, i, cols, y);
       }
       if (++s == ring.slots) {
         s = 0;
@@ -660,11 +735,14 @@ __device__ __forceinline__ Two normalised(Two x, Two mul, Two shift) {
   else return (x + shift) * mul;
 }
 
-template <class T, bool kCodes, int TH, int NV, int BLOCKS>
+template <class T, bool kCodes, bool kVec, int TH, int NV, int BLOCKS>
 __global__ void __launch_bounds__(TH, BLOCKS)
     k_norm_backward_ring(const __grid_constant__ NormBackwardParams p, int wbf16, Ring ring, unsigned* given_up) {
   extern __shared__ __align__(128) char smem[];
   __shared__ uint32_t s_gave_up;
+  // kVec false: a row's scales, by block.  Three rows: the next one's are written before the barrier
+  // that a row's readers have yet to reach, when none can still be two rows behind.
+  __shared__ float s_scale[kCodes && !kVec ? 3 : 1][64];
   volatile uint32_t* gave_up = &s_gave_up;
   RingHead* h = reinterpret_cast<RingHead*>(smem);
   char* slots = smem + kRingHead;
@@ -673,7 +751,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
   grid_dependency_sync();
   RingFeed feed{h, slots, static_cast<const char*>(p.dy), static_cast<const char*>(p.x), p.ld_dy * T::kBytes,
                 p.ld_x * kXBytes, blockIdx.x, p.rows, uint32_t(p.cols * T::kBytes), uint32_t(p.cols * kXBytes), 0};
-  ring_start(feed, &s_gave_up, ring);
+  ring_start<kVec>(feed, &s_gave_up, ring);
   const int t = threadIdx.x;
   {
     const int cols = int(p.cols);
@@ -681,8 +759,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
     Two dw[NV][4], db[NV][4], w[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (t + i * TH) * 8;
-      const Eight e = load_param(p.weight, wbf16, col, valid(cols, col), true);
+      const Eight e = ring_param<kVec, TH>(p.weight, wbf16, i, cols);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         w[i][k] = Two(e.v[2 * k], e.v[2 * k + 1]);
@@ -691,16 +768,18 @@ __global__ void __launch_bounds__(TH, BLOCKS)
     }
     // the statistics and scales of a row are fetched a whole row ahead: their latency passes
     // behind the row before
+    constexpr int NS = kVec ? NV : 1;  // scales: of a thread's pieces, or of block t
     struct Stats {
       float mean, rstd;
-      uint32_t scale[NV];
+      uint32_t scale[NS];
     };
-    int at[NV];  // byte of a piece's scale inside a row's tiles
+    const int blocks = (cols + kCkptBlock - 1) / kCkptBlock;
+    int at[NS];  // byte of a scale inside a row's tiles
     if constexpr (kCodes) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int b = (t + i * TH) * 8 / kCkptBlock;
-        at[i] = (b >> 2) * 512 + (b & 3);
+      for (int i = 0; i < NS; ++i) {
+        const int b = kVec ? (t + i * TH) * 8 / kCkptBlock : t;
+        at[i] = b < blocks ? (b >> 2) * 512 + (b & 3) : -1;
       }
     }
     const int64_t row_tiles = scale_tile_cols((cols + kCkptBlock - 1) / kCkptBlock) * 512;
@@ -711,40 +790,74 @@ __global__ void __launch_bounds__(TH, BLOCKS)
       if constexpr (kCodes) {
         const uint8_t* sr = p.x_scale + (row >> 7) * row_tiles + (row & 31) * 16 + ((row >> 5) & 3) * 4;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if ((t + i * TH) * 8 < cols) st.scale[i] = sr[at[i]];
+        for (int i = 0; i < NS; ++i)
+          if (at[i] >= 0) st.scale[i] = sr[at[i]];
       }
     };
     Stats next = {};
     fetch(blockIdx.x, next);
+    int third = 0;
+    uint32_t later = 0;  // kVec false: the scale of block t two rows ahead
+    if constexpr (kCodes && !kVec) {
+      if (t < 64) s_scale[0][t] = scale_value(next.scale[0]);
+      Stats st = {};
+      fetch(blockIdx.x + int64_t(gridDim.x), st);
+      later = st.scale[0];
+      __syncthreads();
+    }
     int s = 0, half = 0;
     uint32_t phase = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
       const Stats now = next;
       fetch(row + gridDim.x, next);
+      const float* scales = s_scale[kCodes && !kVec ? third : 0];
+      if constexpr (kCodes && !kVec) {
+        if (++third == 3) third = 0;
+        if (t < 64) s_scale[third][t] = scale_value(later);
+        Stats st = {};
+        fetch(row + 2 * int64_t(gridDim.x), st);
+        later = st.scale[0];
+      }
       const bool good = tc::mbar_wait(tc::smem_addr(&h->full[s]), phase, gave_up);  // as in the forward pass
-      const char* src = slots + s * ring.slot_bytes;
+      const char* slot = slots + s * ring.slot_bytes;
+      const char* dy_row = slot + ring_offset<kVec>(p.dy, row * p.ld_dy * T::kBytes);
+      const char* x_row = slot + ring.second + ring_offset<kVec>(p.x, row * p.ld_x * kXBytes);
       const Two shift(kFused ? -now.mean * now.rstd : -now.mean);
       // the piece's dy and xh, as pairs
-      auto piece = [&](int i, int col, Two (&dy)[4], Two (&xh)[4]) {
-        const Eight e = load_eight<T>(src, col, 8, true);
-        const Two mul(kCodes ? scale_value(now.scale[i]) * now.rstd : now.rstd);
-        Eight x;
-        if constexpr (kCodes) x = load_codes(reinterpret_cast<const uint8_t*>(src) + ring.second + col, 8, true);
-        else x = load_eight<T>(src + ring.second, col, 8, true);
+      auto piece = [&](int i, Two (&dy)[4], Two (&xh)[4]) {
+        const Eight e = ring_piece<T, kVec, TH>(dy_row, i, cols);
+        Eight x, f;
+        if constexpr (kCodes && kVec) {
+          x = load_codes(reinterpret_cast<const uint8_t*>(x_row) + ring_col<true, TH>(i, 0), 8, true);
+        } else if constexpr (kCodes) {
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            const int c0 = ring_col<false, TH>(i, k), c1 = ring_col<false, TH>(i, k + 1);
+            const uint32_t two = (c0 < cols ? uint8_t(x_row[c0]) : 0u) | (c1 < cols ? uint32_t(uint8_t(x_row[c1])) << 8 : 0u);
+            uint32_t h2;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(two)));
+            x.v[k] = f16_lo(h2);
+            x.v[k + 1] = f16_hi(h2);
+            f.v[k] = c0 < cols ? scales[c0 / kCkptBlock] * now.rstd : 0.0f;
+            f.v[k + 1] = c1 < cols ? scales[c1 / kCkptBlock] * now.rstd : 0.0f;
+          }
+        } else {
+          x = ring_piece<T, kVec, TH>(x_row, i, cols);
+        }
+        const float one = kCodes && kVec ? scale_value(now.scale[kVec ? i : 0]) * now.rstd : now.rstd;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           dy[k] = Two(e.v[2 * k], e.v[2 * k + 1]);
+          const Two mul = kCodes && !kVec ? Two(f.v[2 * k], f.v[2 * k + 1]) : Two(one);
           xh[k] = normalised<kFused>(Two(x.v[2 * k], x.v[2 * k + 1]), mul, shift);
         }
       };
       Two s0(0.0f), s1(0.0f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int col = (t + i * TH) * 8;
-        if (col >= cols) continue;
-        Two dy[4], xh[4];
-        piece(i, col, dy, xh);
+        if (ring_col<kVec, TH>(i, 0) >= cols) continue;
+        Two dy[4], xh[4];  // past the row dy is 0, and adds nothing
+        piece(i, dy, xh);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const Two g = dy[k] * w[i][k];
@@ -760,19 +873,18 @@ __global__ void __launch_bounds__(TH, BLOCKS)
       s1.get(lo, hi);
       sum[1] = lo + hi;
       ring_sum<TH>(sum, h, half);
-      if (t == 0 && row != blockIdx.x) feed.next(ring);  // every thread is past the row before
+      if (t == 0 && row != blockIdx.x) feed.next<kVec>(ring);  // every thread is past the row before
       // dx = rstd g - rstd mean(g) - xh rstd mean(g xh)
       const Two r2(now.rstd), c0(-now.rstd * (sum[0] * inv)), c1(-now.rstd * (sum[1] * inv));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int col = (t + i * TH) * 8;
-        if (col >= cols) continue;
-        Two dy[4], xh[4];
-        piece(i, col, dy, xh);
+        if (ring_col<kVec, TH>(i, 0) >= cols) continue;
+        Two dy[4], xh[4];  // past the row dy is 0, and adds nothing
+        piece(i, dy, xh);
         Eight dx;
 #pragma unroll
         for (int k = 0; k < 4; ++k) fma2(xh[k], c1, fma2(dy[k] * w[i][k], r2, c0)).get(dx.v[2 * k], dx.v[2 * k + 1]);
-        if (good) store_eight<T>(p.dx, row * p.ld_dx + col, dx, 8, true);
+        if (good) ring_store<T, kVec, TH>(p.dx, row * p.ld_dx, i, cols, dx);
       }
       if (++s == ring.slots) {
         s = 0;
@@ -782,18 +894,14 @@ __global__ void __launch_bounds__(TH, BLOCKS)
     float* out = p.workspace + int64_t(blockIdx.x) * 2 * cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (t + i * TH) * 8;
-      if (col >= cols) continue;
+      Eight a, c;
 #pragma unroll
-      for (int k = 0; k < 4; k += 2) {
-        float4 a, c;
-        dw[i][k].get(a.x, a.y);
-        dw[i][k + 1].get(a.z, a.w);
-        db[i][k].get(c.x, c.y);
-        db[i][k + 1].get(c.z, c.w);
-        *reinterpret_cast<float4*>(out + col + 2 * k) = a;
-        *reinterpret_cast<float4*>(out + cols + col + 2 * k) = c;
+      for (int k = 0; k < 4; ++k) {
+        dw[i][k].get(a.v[2 * k], a.v[2 * k + 1]);
+        db[i][k].get(c.v[2 * k], c.v[2 * k + 1]);
       }
+      ring_store<F32T, kVec, TH>(out, 0, i, cols, a);
+      ring_store<F32T, kVec, TH>(out + cols, 0, i, cols, c);
     }
   }
   __syncthreads();
@@ -846,15 +954,18 @@ Spread spread_of(int64_t cols, int max_nv) {
   return {true, 0, 1024};
 }
 
-// Whether rows of `cols` columns can go through a ring: enough of them for the prologue of a
-// persistent block to pay, and every row a whole number of 16-byte units.
-bool ring_rows(int64_t rows, int64_t cols, const DeviceInfo& dev) { return cols <= 8192 && rows >= 4 * int64_t(dev.sms); }
+// Whether rows of `cols` columns go through a ring: enough of them for the prologue of a persistent
+// block to pay (odd widths: backward 1001x1023 F32 9.8 us, direct 7.3; 4096x1001 13.7 and 16.4), and rows of
+// 64 bytes or more.
+bool ring_rows(int64_t rows, int64_t cols, bool odd, const DeviceInfo& dev) {
+  return cols <= 8192 && (cols % 16 == 0 || cols >= 64) && rows >= (odd ? 12 : 4) * int64_t(dev.sms);
+}
 
-template <class T, int TH, int NV, int BLOCKS>
+template <class T, bool kVec, int TH, int NV, int BLOCKS>
 cudaError_t forward_ring(const NormForwardParams& p, int wdtype, const DeviceInfo& dev, unsigned* given_up,
                          cudaStream_t stream) {
-  const Ring ring = ring_of(p.cols * T::kBytes, 0, BLOCKS);
-  auto kernel = k_norm_forward_ring<T, TH, NV, BLOCKS>;
+  const Ring ring = ring_of(p.cols * T::kBytes + (kVec ? 0 : 30), 0, BLOCKS);
+  auto kernel = k_norm_forward_ring<T, kVec, TH, NV, BLOCKS>;
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring.smem));
   if (e != cudaSuccess) return e;
@@ -869,17 +980,24 @@ cudaError_t forward(const NormForwardParams& p, int wdtype, const DeviceInfo& de
   auto launch = [&](auto kernel, int64_t blocks, int threads) {
     return launch_kernel(kernel, dim3(unsigned(blocks)), dim3(threads), 0, stream, p, wdtype);
   };
-  if (p.vec && p.cols % 8 == 0 && ring_rows(p.rows, p.cols, dev)) {
+  if (ring_rows(p.rows, p.cols, p.cols % 8 != 0, dev) && (p.cols % 8 != 0 || p.vec)) {
     unsigned* given_up = nullptr;
     const cudaError_t e = given_up_address(dev.device, &given_up);
     if (e != cudaSuccess) return e;
-    if (pieces <= 32) return forward_ring<T, 32, 1, 24>(p, wdtype, dev, given_up, stream);
-    if (pieces <= 64) return forward_ring<T, 32, 2, 20>(p, wdtype, dev, given_up, stream);
-    if (pieces <= 128) return forward_ring<T, 64, 2, 12>(p, wdtype, dev, given_up, stream);
-    if (pieces <= 256) return forward_ring<T, 128, 2, 6>(p, wdtype, dev, given_up, stream);
-    if (pieces <= 512) return forward_ring<T, 256, 2, 3>(p, wdtype, dev, given_up, stream);
-    if (pieces <= 768) return forward_ring<T, 256, 3, 2>(p, wdtype, dev, given_up, stream);
-    return forward_ring<T, 256, 4, 2>(p, wdtype, dev, given_up, stream);
+    if (p.cols % 8 != 0) {
+      if (pieces <= 64) return forward_ring<T, false, 64, 1, 12>(p, wdtype, dev, given_up, stream);
+      if (pieces <= 128) return forward_ring<T, false, 128, 1, 6>(p, wdtype, dev, given_up, stream);
+      if (pieces <= 256) return forward_ring<T, false, 256, 1, 4>(p, wdtype, dev, given_up, stream);
+      if (pieces <= 512) return forward_ring<T, false, 256, 2, 3>(p, wdtype, dev, given_up, stream);
+      return forward_ring<T, false, 512, 2, 1>(p, wdtype, dev, given_up, stream);
+    }
+    if (pieces <= 32) return forward_ring<T, true, 32, 1, 24>(p, wdtype, dev, given_up, stream);
+    if (pieces <= 64) return forward_ring<T, true, 32, 2, 20>(p, wdtype, dev, given_up, stream);
+    if (pieces <= 128) return forward_ring<T, true, 64, 2, 12>(p, wdtype, dev, given_up, stream);
+    if (pieces <= 256) return forward_ring<T, true, 128, 2, 6>(p, wdtype, dev, given_up, stream);
+    if (pieces <= 512) return forward_ring<T, true, 256, 2, 3>(p, wdtype, dev, given_up, stream);
+    if (pieces <= 768) return forward_ring<T, true, 256, 3, 2>(p, wdtype, dev, given_up, stream);
+    return forward_ring<T, true, 256, 4, 2>(p, wdtype, dev, given_up, stream);
   }
   auto direct = [&](auto vec) {
     constexpr bool kVec = decltype(vec)::value;
@@ -895,11 +1013,12 @@ cudaError_t forward(const NormForwardParams& p, int wdtype, const DeviceInfo& de
   return launch_kernel(k_norm_forward_long<T>, dim3(unsigned(p.rows)), dim3(1024), 0, stream, p, wdtype);
 }
 
-template <class T, bool kCodes, int TH, int NV, int BLOCKS>
+template <class T, bool kCodes, bool kVec, int TH, int NV, int BLOCKS>
 cudaError_t backward_ring(const NormBackwardParams& p, int wdtype, const DeviceInfo& dev, unsigned* given_up,
                           unsigned* blocks, cudaStream_t stream) {
-  const Ring ring = ring_of(p.cols * T::kBytes, p.cols * (kCodes ? 1 : T::kBytes), BLOCKS);
-  auto kernel = k_norm_backward_ring<T, kCodes, TH, NV, BLOCKS>;
+  constexpr int kPad = kVec ? 0 : 30;
+  const Ring ring = ring_of(p.cols * T::kBytes + kPad, p.cols * (kCodes ? 1 : T::kBytes) + kPad, BLOCKS);
+  auto kernel = k_norm_backward_ring<T, kCodes, kVec, TH, NV, BLOCKS>;
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring.smem));
   if (e != cudaSuccess) return e;
@@ -914,20 +1033,29 @@ cudaError_t backward(const NormBackwardParams& p, int wdtype, const DeviceInfo& 
   const int64_t pieces = (p.cols + 7) / 8, room = norm_partials(p.rows, p.cols), work = s.block ? p.rows : (p.rows + 7) / 8;
   unsigned blocks = unsigned(work < room ? work : room);
   const dim3 block(s.threads), grid(blocks);
-  const bool units = p.vec && p.cols % (kCodes ? 16 : 8) == 0 && (!kCodes || p.ld_x % 16 == 0) &&
+  // codes: 8-byte units serve the direct kernels, the ring copies 16
+  const bool odd = p.cols % (kCodes ? 16 : 8) != 0, units = p.vec && !odd && (!kCodes || p.ld_x % 16 == 0) &&
                      reinterpret_cast<uintptr_t>(p.x) % 16 == 0;
   cudaError_t e;
-  if (units && ring_rows(p.rows, p.cols, dev)) {
+  if ((units || odd) && ring_rows(p.rows, p.cols, odd, dev)) {
     unsigned* given_up = nullptr;
     e = given_up_address(dev.device, &given_up);
     if (e != cudaSuccess) return e;
-    e = pieces <= 32    ? backward_ring<T, kCodes, 32, 1, 20>(p, wdtype, dev, given_up, &blocks, stream)
-        : pieces <= 64  ? backward_ring<T, kCodes, 32, 2, 16>(p, wdtype, dev, given_up, &blocks, stream)
-        : pieces <= 128 ? backward_ring<T, kCodes, 64, 2, 8>(p, wdtype, dev, given_up, &blocks, stream)
-        : pieces <= 256 ? backward_ring<T, kCodes, 128, 2, 4>(p, wdtype, dev, given_up, &blocks, stream)
-        : pieces <= 512 ? backward_ring<T, kCodes, 256, 2, 2>(p, wdtype, dev, given_up, &blocks, stream)
-        : pieces <= 768 ? backward_ring<T, kCodes, 256, 3, 2>(p, wdtype, dev, given_up, &blocks, stream)
-                        : backward_ring<T, kCodes, 512, 2, 1>(p, wdtype, dev, given_up, &blocks, stream);
+    if (odd) {
+      e = pieces <= 64    ? backward_ring<T, kCodes, false, 64, 1, 8>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 128 ? backward_ring<T, kCodes, false, 128, 1, 5>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 256 ? backward_ring<T, kCodes, false, 256, 1, 3>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 512 ? backward_ring<T, kCodes, false, 256, 2, 2>(p, wdtype, dev, given_up, &blocks, stream)
+                          : backward_ring<T, kCodes, false, 512, 2, 1>(p, wdtype, dev, given_up, &blocks, stream);
+    } else {
+      e = pieces <= 32    ? backward_ring<T, kCodes, true, 32, 1, 20>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 64  ? backward_ring<T, kCodes, true, 32, 2, 16>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 128 ? backward_ring<T, kCodes, true, 64, 2, 8>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 256 ? backward_ring<T, kCodes, true, 128, 2, 4>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 512 ? backward_ring<T, kCodes, true, 256, 2, 2>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 768 ? backward_ring<T, kCodes, true, 256, 3, 2>(p, wdtype, dev, given_up, &blocks, stream)
+                          : backward_ring<T, kCodes, true, 512, 2, 1>(p, wdtype, dev, given_up, &blocks, stream);
+    }
   } else if (s.nv == 0) {
     e = launch_kernel(k_norm_backward_long<T, kCodes>, grid, block, 0, stream, p, wdtype);
   } else {

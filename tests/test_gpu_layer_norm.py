@@ -234,3 +234,27 @@ def test_empty_and_refusals():
     assert status(g, x, x.to(torch.uint8), None, w, m, m, x, dw, db, ws, 4, 64) == 4
     assert status(g, x, x, ws, w, m, m, x, dw, db, ws, 4, 64) == 1
     assert status(g, x, x, None, w, m, m, x, dw.bfloat16(), db, ws, 4, 64) == 3
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [64, 72, 129, 255, 512, 1000, 1024, 1537, 3000, 4095, 6144, 8190, 8192])
+def test_many_rows(cols, dtype):
+    """Enough rows for persistent blocks: forward, and backward from the input and from its checkpoint
+    (odd widths, whose rows start anywhere, among them), from buffers off 16 bytes too."""
+    rows = 1900
+    for shift in (0, 1):
+        flat = lambda: torch.empty(rows * cols + 8, dtype=DT[dtype], device="cuda")[shift:shift + rows * cols].view(rows, cols)  # noqa: E731
+        x, w, b = data(rows, cols, dtype, "f32")
+        xs, dy, y = flat(), flat(), flat()
+        xs.copy_(x)
+        dy.copy_(torch.randn(rows, cols, device="cuda"))
+        y, mean, rstd = forward(xs, w, b, y)
+        check_forward(ref.as64(xs), ref.as64(w), ref.as64(b), y, mean, rstd)
+        check_backward(*map(ref.as64, (dy, xs, w, mean, rstd)), *backward(dy, xs, None, w, mean, rstd, out=flat()))
+        q = torch.empty(rows * cols + 8, dtype=torch.uint8, device="cuda")[shift:shift + rows * cols].view(rows, cols)
+        s = torch.empty(api.mxfp8_swizzled_scales_size(rows, -(-cols // 128)), dtype=torch.uint8, device="cuda")
+        api.mxfp8_checkpoint_save(xs, q, s, None, None, rows, cols)
+        kept, dy64 = ref.quantise(ref.as64(xs))[0], ref.as64(dy)
+        got = backward(dy, q, s, w, mean, rstd, out=dy)  # in place
+        check_backward(dy64, kept, ref.as64(w), ref.as64(mean), ref.as64(rstd), *got)
+    api.mxfp8_device_status()
