@@ -1,0 +1,108 @@
+"""A linear layer behind a layer norm, trained on the MXFP8 weights that the cast writes.
+
+    h = LayerNorm(x),  y = h W^T
+
+The FP32 master weight lives in shards and reaches its MXFP8 copies (rowwise and columnwise)
+through ``driver.ShardedCast``; ``refresh`` lays their scales out for the products.  What the
+backward pass needs of the activations is kept in 8 bits: the layer's input as a rowwise
+checkpoint (layer norm's gradients read it) and the normalised input as a columnwise one
+(the weight's gradient contracts over tokens).  A step's calls:
+
+    forward    save(x), layer norm, save(h), y = h W^T
+    backward   save(dy), dh = dy W, dW += dy^T h, layer norm's gradients
+
+All buffers are allocated once; every call goes to the current stream.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import api, driver
+
+
+def _pitch(n: int) -> int:
+    """Row stride of a code buffer: whole 16-byte units, so that TMA can fetch its rows."""
+    return (n + 15) // 16 * 16
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+class Checkpoint:
+    """Buffers of an activation's 8-bit checkpoint, tokens x width, in one or both directions."""
+
+    def __init__(self, tokens: int, width: int, device, rowwise: bool = True, colwise: bool = True):
+        self.tokens, self.width = tokens, width
+        u8 = lambda *shape: torch.empty(*shape, dtype=torch.uint8, device=device)  # noqa: E731
+        self.codes_r = u8(tokens, _pitch(width)) if rowwise else None
+        self.scale_r = u8(api.mxfp8_swizzled_scales_size(tokens, _blocks(width))) if rowwise else None
+        self.codes_c = u8(tokens, _pitch(width)) if colwise else None
+        self.scale_c = u8(api.mxfp8_swizzled_scales_size(width, _blocks(tokens))) if colwise else None
+
+    def save(self, x: torch.Tensor) -> None:
+        api.mxfp8_checkpoint_save(x, self.codes_r, self.scale_r, self.codes_c, self.scale_c, self.tokens, self.width)
+
+    def restore(self, out: torch.Tensor, colwise: bool = False) -> None:
+        codes, scale = (self.codes_c, self.scale_c) if colwise else (self.codes_r, self.scale_r)
+        api.mxfp8_checkpoint_restore(codes, scale, out, self.tokens, self.width, colwise=colwise)
+
+
+class NormLinear:
+    """One layer for ``tokens`` tokens per step, weight [outs][ins], master shards cut at
+    ``bounds`` of the flat weight (default: one shard)."""
+
+    def __init__(self, tokens: int, ins: int, outs: int, device="cuda", dtype=torch.bfloat16, bounds=None,
+                 eps: float = 1e-5):
+        self.tokens, self.ins, self.outs, self.eps = tokens, ins, outs, eps
+        dev = torch.device(device)
+        self.cast = driver.ShardedCast([driver.WeightSpec(outs, ins, True)], bounds or [0, outs * ins], dev)
+        (rr, rc), (cr, cc) = api.block_shapes(outs, ins)
+        self._grids = (rr, rc, cr, cc)
+        self.w_scale_r = torch.empty(api.mxfp8_swizzled_scales_size(rr, rc), dtype=torch.uint8, device=dev)
+        self.w_scale_c = torch.empty(api.mxfp8_swizzled_scales_size(cr, cc, True), dtype=torch.uint8, device=dev)
+        # parameters of the norm and the gradients, which accumulate (weight) or are set (norm)
+        self.norm_weight, self.norm_bias = torch.ones(ins, device=dev), torch.zeros(ins, device=dev)
+        self.grad_weight = torch.zeros(outs, ins, device=dev)
+        self.grad_norm_weight, self.grad_norm_bias = torch.empty(ins, device=dev), torch.empty(ins, device=dev)
+        # kept from forward to backward: 1 byte per value of x and of h, and two floats per token
+        self.x8 = Checkpoint(tokens, ins, dev, colwise=False)
+        self.h8 = Checkpoint(tokens, ins, dev)
+        self.mean, self.rstd = torch.empty(tokens, device=dev), torch.empty(tokens, device=dev)
+        # working buffers of a step
+        self.dy8 = Checkpoint(tokens, outs, dev)
+        self.h = torch.empty(tokens, ins, dtype=dtype, device=dev)
+        self.y = torch.empty(tokens, outs, dtype=dtype, device=dev)
+        self.dh = torch.empty(tokens, ins, dtype=dtype, device=dev)
+        self.dx = torch.empty(tokens, ins, dtype=dtype, device=dev)
+        self.workspace = torch.empty(max(1, api.mxfp8_layer_norm_workspace_size(tokens, ins)), dtype=torch.uint8, device=dev)
+
+    def refresh(self, shards) -> None:
+        """New MXFP8 weights from the master shards."""
+        self.cast.step(shards)
+        rr, rc, cr, cc = self._grids
+        sr, sc = self.cast.scales[0]
+        api.mxfp8_swizzle_scales(sr, self.w_scale_r, rr, rc)
+        api.mxfp8_swizzle_scales(sc, self.w_scale_c, cr, cc, transpose=True)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        """y of this step's input (tokens x ins); valid until the next call."""
+        t, i, o = self.tokens, self.ins, self.outs
+        self.x8.save(x)
+        api.mxfp8_layer_norm_forward(x, self.norm_weight, self.norm_bias, self.h, self.mean, self.rstd, t, i, self.eps)
+        self.h8.save(self.h)
+        api.mxfp8_gemm(self.h8.codes_r, self.h8.scale_r, self.cast.outputs[0][0], self.w_scale_r, None, self.y, t, o, i,
+                       b_block=32)
+        return self.y
+
+    def backward(self, dy: torch.Tensor) -> torch.Tensor:
+        """dx of this step's output gradient; adds to grad_weight, sets the norm's gradients."""
+        t, i, o = self.tokens, self.ins, self.outs
+        self.dy8.save(dy)
+        api.mxfp8_gemm(self.dy8.codes_r, self.dy8.scale_r, self.cast.outputs[0][1], self.w_scale_c, None, self.dh, t, i, o,
+                       b_colwise=True, b_block=32)
+        api.mxfp8_gemm(self.dy8.codes_c, self.dy8.scale_c, self.h8.codes_c, self.h8.scale_c, self.grad_weight,
+                       self.grad_weight, o, i, t, a_colwise=True, b_colwise=True)
+        api.mxfp8_layer_norm_backward(self.dh, self.x8.codes_r, self.x8.scale_r, self.norm_weight, self.mean, self.rstd,
+                                      self.dx, self.grad_norm_weight, self.grad_norm_bias, self.workspace, t, i)
+        return self.dx

@@ -9,6 +9,9 @@ Cases (seeded synthetic inputs of the workloads module):
   sharded     the config-5 batch in four emulated shards (dimensions divided by --scale):
               batched amax -> ranged reduction + scales -> batched cast
   nvfp4       the 16384x6144 FP32 weight through the NVFP4 amax, scale update and cast
+  linear      a training step of a 4096x4096 linear layer behind a layer norm, 4096 tokens
+              (tokens divided by --scale): weight cast, forward and backward pass with 8-bit
+              activation checkpoints
   small       the 160x96 FP32 weight (config 1), one full fragment: amax -> scales -> cast
               (a launch of five tiles: the split kernels)
 
@@ -24,7 +27,7 @@ import argparse
 import numpy as np
 import torch
 
-from . import api, build, driver
+from . import api, build, driver, linear
 from . import workloads as wl
 
 
@@ -100,8 +103,24 @@ def case_small(dev, scale):
     return run
 
 
+def case_linear(dev, scale):
+    w = wl.cfg3_square()
+    tokens = 4096 // scale
+    layer = linear.NormLinear(tokens, w.cols, w.rows, dev)
+    master = torch.from_numpy(w.data).to(dev)
+    g = torch.Generator(device=dev).manual_seed(0)
+    x = torch.randn(tokens, w.cols, generator=g, device=dev).bfloat16()
+    dy = (torch.randn(tokens, w.rows, generator=g, device=dev) * 1e-3).bfloat16()
+
+    def run():
+        layer.refresh([master])
+        layer.forward(x)
+        layer.backward(dy)
+    return run
+
+
 CASES = {"step": case_step, "one_pass": case_one_pass, "sharded": case_sharded, "nvfp4": case_nvfp4,
-         "small": case_small}
+         "small": case_small, "linear": case_linear}
 
 
 def main(argv=None):
