@@ -314,7 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kRealign>, 
           if (left != 0 && --left == 0) {
             tc::fence_before_sync();
             __syncwarp();
-            if ((threadIdx.x & 31) == 0) tc::mbar_arrive_cluster(sums_free, 0);
+            if ((threadIdx.x & 31) == 0) tc::mbar_arrive_cluster_relaxed(sums_free, 0);
           }
         });
       }
