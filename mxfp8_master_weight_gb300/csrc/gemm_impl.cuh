@@ -32,14 +32,6 @@ __host__ __device__ inline int64_t scale_tiles_along_k(int64_t k, int block) {
   return scale_tile_cols((k + block - 1) / block);
 }
 
-__device__ __forceinline__ float load_addend(const GemmParams& p, int64_t i, int64_t j) {
-  return p.addend != nullptr ? p.addend[i * p.ld_c + j] : 0.0f;
-}
-__device__ __forceinline__ void store_one(const GemmParams& p, int64_t i, int64_t j, float v) {
-  if (p.out_f32) static_cast<float*>(p.out)[i * p.ld_o + j] = v;
-  else static_cast<uint16_t*>(p.out)[i * p.ld_o + j] = static_cast<uint16_t>(bf16x2_rn(v, 0.0f));
-}
-
 // Writes 128 bytes of each of 32 output rows (32 F32 or 64 BF16 columns) that a warp holds a row per
 // lane.  A store straight from there would touch 32 lines for 512 bytes; through 4 KB of
 // shared memory of the warp's own (16-byte unit c of row r at c ^ (r % 8)) every store fills

@@ -41,57 +41,95 @@ struct SplitParams {
 
 struct SplitParamsRealign : SplitParams, Residues {};
 
-// Writes N neighbouring columns, j .. j + N - 1, of row i of the tile's matrix.
-template <int N>
-__device__ __forceinline__ void store_columns(const SplitParams& q, int64_t i, int64_t j, const float (&v)[N]) {
+// Where 16-byte unit u of line r lies: units of eight neighbouring lines that threads write at once
+// take different banks.
+template <int NT>
+__device__ __forceinline__ int unit_at(int r, int u) { return u ^ (NT >= 32 ? r & 7 : (r >> 1) & 3); }
+
+// Adds this CTA's share of the tile's output lines over the S CTAs of the cluster, in rank order, and writes
+// them.  The partial sums lie at `part` as lines of the output: 128 lines of NT sums, or with operands
+// that changed places NT lines of 128.  A thread keeps W neighbouring columns, four where the output takes
+// 16-byte stores, else one, and walks down the lines with kLoads loads under way at once.
+template <int NT, int W, int S, int kLoads>
+__device__ __forceinline__ void write_lines(const SplitParams& q, uint32_t part, int64_t i0, int64_t j0, int rank, int thread) {
   const GemmParams& p = q.g;
-  if (i >= p.m) return;
-  if (q.swapped) {  // neighbouring lanes hold neighbouring elements of the output row
+  constexpr int kBatch = kLoads / S;
+  const int width = q.swapped ? 128 : NT, shift = 31 - __clz(width / W), step = 128 >> shift;
+  const int64_t row0 = q.swapped ? j0 : i0, rows = (q.swapped ? p.n : p.m) - row0;
+  const int c = (thread & ((1 << shift) - 1)) * W;
+  const int64_t col = (q.swapped ? i0 : j0) + c, cols = (q.swapped ? p.m : p.n) - col;
+  if (cols <= 0) return;
+  const int per = (q.swapped ? NT : 128) / S;
+  int line = per * rank + (thread >> shift);
+  const int end = per * (rank + 1) < rows ? per * (rank + 1) : int(rows);
+  uint32_t parts[S];
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (j + e < p.n) store_one(p, j + e, i, v[e] + load_addend(p, j + e, i));
-    return;
-  }
-  if (N % 8 == 0 && p.vec_out && p.addend == nullptr && j + N <= p.n) {
+  for (int r = 0; r < S; ++r) parts[r] = S > 1 ? tc::in_cta(part, r) : part;
+  const int64_t size = p.out_f32 ? 4 : 2;
+  char* out = static_cast<char*>(p.out) + ((row0 + line) * p.ld_o + col) * size;
+  const float* addend = p.addend == nullptr ? nullptr : p.addend + (row0 + line) * p.ld_c + col;
+  for (; line < end; line += step * kBatch) {
+    float v[kBatch][W], x[S][kBatch][W];
 #pragma unroll
-    for (int e = 0; e < N; e += 8) {
-      if (p.out_f32) {
-        float* o = static_cast<float*>(p.out) + i * p.ld_o + j + e;
-        *reinterpret_cast<float4*>(o) = make_float4(v[e], v[e + 1 < N ? e + 1 : 0], v[e + 2 < N ? e + 2 : 0], v[e + 3 < N ? e + 3 : 0]);
-        *reinterpret_cast<float4*>(o + 4) = make_float4(v[e + 4 < N ? e + 4 : 0], v[e + 5 < N ? e + 5 : 0], v[e + 6 < N ? e + 6 : 0], v[e + 7 < N ? e + 7 : 0]);
-      } else {
-        uint16_t* o = static_cast<uint16_t*>(p.out) + i * p.ld_o + j + e;
-        *reinterpret_cast<uint4*>(o) = make_uint4(bf16x2_rn(v[e], v[e + 1 < N ? e + 1 : 0]), bf16x2_rn(v[e + 2 < N ? e + 2 : 0], v[e + 3 < N ? e + 3 : 0]),
-                                                  bf16x2_rn(v[e + 4 < N ? e + 4 : 0], v[e + 5 < N ? e + 5 : 0]), bf16x2_rn(v[e + 6 < N ? e + 6 : 0], v[e + 7 < N ? e + 7 : 0]));
+    for (int b = 0; b < kBatch; ++b) {
+      const int at_line = line + step * b;
+      const bool live = at_line < end;
+      const uint32_t at = 4 * (at_line * width + (q.swapped ? c : 4 * unit_at<NT>(at_line, c >> 2) + (c & 3)));
+#pragma unroll
+      for (int r = 0; r < S; ++r) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) x[r][b][e] = 0.0f;
+        if constexpr (W == 4)
+          asm volatile("{ .reg .pred live; setp.ne.u32 live, %5, 0;\n"
+                       "@live ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4]; }"
+                       : "+f"(x[r][b][0]), "+f"(x[r][b][1]), "+f"(x[r][b][2]), "+f"(x[r][b][3])
+                       : "r"(parts[r] + at), "r"(uint32_t(live)));
+        else
+          asm volatile("{ .reg .pred live; setp.ne.u32 live, %2, 0;\n"
+                       "@live ld.shared::cluster.f32 %0, [%1]; }"
+                       : "+f"(x[r][b][0])
+                       : "r"(parts[r] + at), "r"(uint32_t(live)));
+      }
+#pragma unroll
+      for (int e = 0; e < W; ++e) v[b][e] = 0.0f;
+      if (addend != nullptr) {
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (live && e < cols) v[b][e] = addend[e];
+        addend += step * p.ld_c;
       }
     }
-    return;
-  }
 #pragma unroll
-  for (int e = 0; e < N; ++e)
-    if (j + e < p.n) store_one(p, i, j + e, v[e] + load_addend(p, i, j + e));
+    for (int b = 0; b < kBatch; ++b, out += step * p.ld_o * size) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        float sum = x[0][b][e];
+#pragma unroll
+        for (int r = 1; r < S; ++r) sum += x[r][b][e];
+        v[b][e] += sum;
+      }
+      if (line + step * b >= end) continue;
+      if (W == 4 && cols >= W) {
+        if (p.out_f32) *reinterpret_cast<float4*>(out) = make_float4(v[b][0], v[b][W > 1 ? 1 : 0], v[b][W > 2 ? 2 : 0], v[b][W > 3 ? 3 : 0]);
+        else *reinterpret_cast<uint2*>(out) = make_uint2(bf16x2_rn(v[b][0], v[b][W > 1 ? 1 : 0]), bf16x2_rn(v[b][W > 2 ? 2 : 0], v[b][W > 3 ? 3 : 0]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          if (e >= cols) continue;
+          if (p.out_f32) reinterpret_cast<float*>(out)[e] = v[b][e];
+          else reinterpret_cast<uint16_t*>(out)[e] = static_cast<uint16_t>(bf16x2_rn(v[b][e], 0.0f));
+        }
+      }
+    }
+  }
 }
 
-// Adds N columns from `c` of the tile over the cluster, in rank order, and writes them.
-template <int N>
-__device__ __forceinline__ void add_and_store(const SplitParams& q, const float* part, int c, int row, int64_t i, int64_t j) {
-  float v[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) v[e] = 0.0f;
-  const uint32_t at = tc::smem_addr(part + c * 128 + row);
-#pragma unroll
-  for (int r = 0; r < kMaxSplit; ++r) {
-    if (r < q.split) {
-      const uint32_t from = tc::in_cta(at, r);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        float x;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(from + 512 * e) : "memory");
-        v[e] += x;
-      }
-    }
-  }
-  store_columns<N>(q, i, j, v);
+template <int NT, int W, int kLoads>
+__device__ __forceinline__ void write_lines(const SplitParams& q, uint32_t part, int64_t i0, int64_t j0, int rank, int thread) {
+  if (q.split == 1) write_lines<NT, W, 1, kLoads>(q, part, i0, j0, rank, thread);
+  else if (q.split == 2) write_lines<NT, W, 2, kLoads>(q, part, i0, j0, rank, thread);
+  else if (q.split == 4) write_lines<NT, W, 4, kLoads>(q, part, i0, j0, rank, thread);
+  else write_lines<NT, W, 8, kLoads>(q, part, i0, j0, rank, thread);
 }
 
 // The boxes that are realigned, in the order of the stages.
@@ -247,56 +285,39 @@ __global__ void __launch_bounds__(kThreads + (kRealign ? 32 * kRealignWarps : 0)
     }
   }
   __syncwarp();
-  // split: the partial sums, [NT columns][128 rows], over the stages' memory
+  // the sums, as lines of the output, over the stages' memory
   float* part = reinterpret_cast<float*>(smem);
-  const int row = 32 * (warp & 3) + (threadIdx.x & 31);
-  const int64_t i = tm * 128 + row, j = tn * NT;
   const bool writer = warp >= 2 && warp < 6;
   if (writer) {
+    const int row = 32 * (warp & 3) + (threadIdx.x & 31);
     tc::mbar_wait(done, 0, gave_up);
     tc::fence_after_sync();
 #pragma unroll
     for (int c = 0; c < NT; c += 16) {
       float v[16];
-      if (k_hi > k_lo) {
-        tc::tmem_load16(tmem + (uint32_t(32 * (warp & 3)) << 16) + c, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0.0f;
-      }
-      if (q.split == 1) {
-        store_columns<16>(q, i, j + c, v);
-      } else {
+      tc::tmem_load16(tmem + (uint32_t(32 * (warp & 3)) << 16) + c, v);
+      if (q.swapped) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) part[(c + e) * 128 + row] = v[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<float4*>(part + row * NT + 4 * unit_at<NT>(row, (c + e) >> 2)) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
       }
     }
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (q.split > 1) {
-    tc::cluster_sync();
-    if (writer) {
-      const int share = NT / q.split;
-      for (int c = share * int(rank); c < share * int(rank + 1);) {
-        if (share >= 8) {
-          add_and_store<8>(q, part, c, row, i, j + c);
-          c += 8;
-        } else if (share >= 4) {
-          add_and_store<4>(q, part, c, row, i, j + c);
-          c += 4;
-        } else {
-          add_and_store<2>(q, part, c, row, i, j + c);
-          c += 2;
-        }
-      }
-    }
-  }
   tc::fence_after_sync();
-  __syncthreads();
-  if (q.split > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums
-  if (threadIdx.x == 0 && s_gave_up != 0) tc::report_given_up(q.given_up);
   if (warp == 1) tc::tmem_free<1>(tmem, kTmemCols);
+  if (q.split > 1) tc::cluster_sync();
+  if (writer) {
+    if (p.vec_out) write_lines<NT, 4, kRealign ? 8 : 16>(q, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
+    else write_lines<NT, 1, kRealign ? 16 : 32>(q, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
+  }
+  __syncwarp();
+  if (q.split > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums: a release, behind every load
+  if (threadIdx.x == 0 && s_gave_up != 0) tc::report_given_up(q.given_up);
 }
 
 template <int NT>

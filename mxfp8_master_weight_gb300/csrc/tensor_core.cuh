@@ -267,7 +267,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-
 // One thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
