@@ -462,6 +462,8 @@ MXFP8_API int nvfp4_partial_cast(const mxfp8_tensor* input, const mxfp8_tensor* 
  *   mxfp8_swizzled_scales_size bytes, 16-byte aligned.
  * - Outputs must not overlap inputs, unless an argument says so.
  * - A call with no elements to write returns 0 and launches nothing.
+ * - The first product or layer norm on a device loads its kernels and looks up a device address:
+ *   make one such call before a stream capture.
  */
 
 /*
@@ -519,9 +521,9 @@ MXFP8_API int mxfp8_checkpoint_restore(const mxfp8_tensor* codes, const mxfp8_te
  * With y = x W^T, W [outs][ins]: output y: a = x rowwise, b = W rowwise; input gradient
  * dx = dy W: a = dy rowwise, b = W columnwise; weight gradient dW = dy^T x: a = dy columnwise,
  * b = x columnwise.  k may be 0 (operands and scales may then be empty): out = addend or 0.
- * Operands whose base and row stride are multiples of 16 bytes are fetched by TMA; others
- * run a slower kernel.
- * Results do not depend on the run: no atomics, one fixed order of sums per shape.
+ * Operands whose base and row stride are multiples of 16 bytes are fetched as they lie; others
+ * are realigned on the way, which takes longer.
+ * Results do not depend on the run: no atomics, one fixed order of sums per shape and alignment.
  * Errors: 1 bad sizes (m, n, k <= 2^31 - 1024), flags or blocks, unaligned scales, or an addend
  * that overlaps out without being the same matrix; 2 a buffer too small; 3 dtype; 4 missing.
  */
@@ -566,7 +568,8 @@ MXFP8_API int mxfp8_layer_norm_forward(const mxfp8_tensor* input, const mxfp8_te
  * workspace   [out] at least mxfp8_layer_norm_workspace_size(rows, cols) bytes (U8), 16-byte
  *                   aligned; its contents before the call do not matter and after it mean
  *                   nothing.  Calls that overlap on the GPU need workspaces of their own.
- * The sums over rows have one fixed order for a shape: results do not depend on the run.
+ * The sums have one fixed order for a shape and the alignment of the arguments: results do not
+ * depend on the run.
  * rows == 0: the gradients of weight and bias are set to zero.
  * Errors: 1 bad sizes, unaligned scales or workspace; 2 too small; 3 dtype; 4 missing.
  */

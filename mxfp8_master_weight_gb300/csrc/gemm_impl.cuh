@@ -35,7 +35,7 @@ __host__ __device__ inline int64_t scale_tiles_along_k(int64_t k, int block) {
 // Writes 128 bytes of each of 32 output rows (32 F32 or 64 BF16 columns) that a warp holds a row per
 // lane.  A store straight from there would touch 32 lines for 512 bytes; through 4 KB of
 // shared memory of the warp's own (16-byte unit c of row r at c ^ (r % 8)) every store fills
-// four whole lines: 4096^3 with BF16 output 50.5 -> 47.4 us, 8192^3 with F32 output 376 -> 342 us.
+// four whole lines (3 us less for 4096^3 with BF16 output, 34 us for 8192^3 with F32 output).
 // `sums` is called with the first of 32 columns and gives this lane's row.
 template <class Sums>
 __device__ __forceinline__ void write_rows(const GemmParams& p, char* stage, int64_t row0, int64_t col, Sums sums) {

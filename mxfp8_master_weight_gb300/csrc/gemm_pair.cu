@@ -5,17 +5,24 @@
 // stage of 128 values of k costs an SM 33.5 KB of copies for 512 cycles of matrix work.  A
 // single-SM tile of 128 x 256 would fetch 50 KB for the same 512 cycles.
 //
-// Roles in a CTA: warp 0 fetches (one thread, TMA, five stages, or seven of halves), warp 1 of the leading CTA issues scale
-// copies and matrix instructions for both, eight warps write the sums out.
+// Roles in a CTA: warp 0 fetches (one thread, TMA, five stages, or seven where every tile is a half),
+// warp 1 of the leading CTA issues scale copies and matrix instructions for both, eight warps
+// write the sums out.  With an operand to realign four warps write, and nine others fetch and
+// realign.
 //
 // When the last round of tiles would occupy at most half of the pairs, its tiles are cut into
-// halves of 256 x 128, one per pair: 4096^3 (256 tiles, 76 pairs: 3.5 rounds instead of 4) 47.4 -> 45.8 us;
-// outputs of few tiles, all of them halves: 256 x 4096 x 4096 13.9 -> 10.5 us.
+// halves of 256 x 128, one per pair: 4096^3 has 256 tiles for 76 pairs, 3.5 rounds instead of 4
+// (1.6 us less); outputs of few tiles are halves throughout (256 x 4096 x 4096 13.9 -> 10.4 us).
 //
 // Tensor memory has 512 columns; two buffers of 256 sums and the scales do not fit.  The buffers
 // therefore share 32 columns: buffer 0 is columns 0..255, buffer 1 columns 224..479, two sets of
 // scales 480..511.  The writers drain the shared columns of a tile first; then the next
 // tile's instructions start in the other buffer while they write the rest.
+//
+// What bounds it: the matrix instructions and what feeds them.  8192^3 takes 315 us (3.49 PFLOP/s, 0.92 of
+// twice the measured BF16 rate; with both operands across k and F32 output 332 us), 4096^3 44 us (3.13),
+// 2048 x 8192 x 8192 with both across k and F32 output 97 us (2.82): the first and last stages of a
+// launch, about 4 us, and the share of the last round that stays empty are what the smaller ones lose.
 #include <type_traits>
 
 #include <cuda.h>

@@ -5,9 +5,15 @@
 // by HBM, and what counts is that every SM has copies in flight from the start.  The weight's
 // rows take the 128 lanes of the tile (the operands change places when the output has few rows),
 // the tokens its NT = 16 .. 128 columns, and 1 to 8 CTAs share a tile, each with its part
-// of k.  Their partial sums stay in shared memory; after a cluster barrier each CTA adds its share of
-// the columns over the cluster in rank order and writes it.  No workspace, no atomics: the
-// result depends on the shape alone.
+// of k.  Their partial sums stay in shared memory, laid out as lines of the output; after a cluster
+// barrier each CTA adds its share of the lines over the cluster in rank order and writes it.  No
+// workspace, no atomics: the result depends on the shape alone.
+//
+// Measured (launches that follow one another, weights larger than L2 in turn): 1 x 4096 x 4096 5.7 us,
+// 64 x 4096 x 4096 8.2, 1 x 8192 x 8192 14.4 (4.7 TB/s of weight), 64 x 8192 x 8192 16.7.  Streaming the weight
+// takes 10.3 us of the last two; the rest is the start (barriers, tensor memory, first bytes from HBM)
+// and the join.  Reading the sums four at a time, with every rank's reads under way at once, took 1.6 us
+// from the last and 1.2 us from the second: a rank's read costs about 0.4 us when the ranks take turns.
 #include <type_traits>
 
 #include <cuda.h>

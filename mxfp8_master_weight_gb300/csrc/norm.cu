@@ -10,12 +10,18 @@
 // are rounded once.  The variance is the mean squared deviation from the mean (a second pass
 // over registers), not a difference of moments, which would cancel for rows far from zero.
 //
-// Both directions are streaming passes bound by HBM.  A row belongs to one group of threads, which
-// holds it in registers between its reductions, so each value is read once: a warp per row
-// for up to 1024 columns, else a block per row.  In the backward pass a thread keeps the
-// running dw and db of its columns in registers over all rows of its block; a block leaves one
-// row of partial sums, and a second kernel adds the partial rows in their order, so
-// the sums do not depend on the run.
+// Both directions read every value once.  Many rows of up to 8192 columns go through rings of bulk copies
+// in persistent blocks (below); few rows, or longer ones, belong to one group of threads each, which
+// holds the row in registers between its reductions: a warp for up to 1024 columns, else a block; beyond
+// 32768 columns (16384 backward) the row is read again, mostly from L2.  In the backward pass a
+// thread keeps the running dw and db of its columns in registers over all rows of its block; a block
+// leaves one row of partial sums, and a second kernel adds the partial rows in their order, so the
+// sums do not depend on the run.
+//
+// Measured at 16384 x 6144: forward BF16 67.5 us (6.0 TB/s, bound by HBM), backward BF16 92 us, from an
+// 8-bit checkpoint 113 us for 504 MB: there decoding and two passes of arithmetic over the row take 55 %
+// of the issue slots, and two blocks per SM leave waits for statistics and barriers open.  1 x 4096
+// forward: 4.5 us, the time of a call.
 #include <type_traits>
 
 #include "common.cuh"
@@ -180,7 +186,7 @@ __device__ __forceinline__ int valid(int64_t cols, int64_t col) {
 // The columns of a thread's pieces.  Where the columns are a multiple of 8: 8 neighbours per piece,
 // one or two 16-byte loads of an aligned row.  Else (rows then start anywhere): neighbours across
 // the threads, so that single loads and stores still fill whole sectors.  The choice goes by the
-// shape alone, so that a result does not change with the alignment of a buffer.
+// shape alone, so that few rows give the same bits whatever the alignment of a buffer.
 template <bool kVec>
 struct Columns {
   int64_t cols;
@@ -484,13 +490,15 @@ constexpr int kRingHead = 384;          // barriers and sums
 
 struct Ring {
   int32_t slots, slot_bytes, second;  // rows in flight; bytes of a slot; offset of the second operand
+  int32_t side;                       // offset of a row's mean, rstd and scales
   uint32_t smem;
 };
-// first, second: bytes of a row of each operand (multiples of 16); blocks: per SM.
-Ring ring_of(int64_t first, int64_t second, int blocks) {
+// first, second: bytes of a row of each operand (multiples of 16); side: a multiple of 16; blocks: per SM.
+Ring ring_of(int64_t first, int64_t second, int side, int blocks) {
   Ring r{};
   r.second = int32_t((first + 127) / 128 * 128);
-  r.slot_bytes = int32_t(r.second + (second + 127) / 128 * 128);
+  r.side = int32_t(r.second + (second + 127) / 128 * 128);
+  r.slot_bytes = r.side + side;
   const int n = (kRingBytes / blocks - 1024 - kRingHead) / r.slot_bytes;  // 1 KB per block is the system's
   r.slots = n < kRingMaxSlots ? n : kRingMaxSlots;
   r.smem = uint32_t(kRingHead + r.slots * r.slot_bytes);
@@ -577,6 +585,31 @@ struct RingFeed {
     ++issued;
     row += gridDim.x;
   }
+  // The same by a warp, rows on 16 bytes, with what belongs to a row beside its values: its mean and rstd and
+  // (`words` of four) its scales, one word per lane.
+  struct Side {
+    const float *mean, *rstd;
+    const uint8_t* scale;
+    int64_t row_tiles;
+    int words;
+  };
+  __device__ __forceinline__ void next(const Ring& ring, const Side& side) {
+    if (row >= rows) return;
+    const uint32_t s = issued % uint32_t(ring.slots), lane = threadIdx.x & 31;
+    const uint32_t bar = tc::smem_addr(&h->full[s]), dst = tc::smem_addr(slots + s * ring.slot_bytes);
+    if (lane == 0) {
+      tc::mbar_expect(bar, a_bytes + b_bytes);
+      tc::bulk_load(dst, a + row * a_pitch, a_bytes, bar);
+      tc::bulk_load(dst + ring.second, b + row * b_pitch, b_bytes, bar);
+    }
+    if (lane < 2) tc::copy_word(dst + ring.side + 4 * lane, (lane == 0 ? side.mean : side.rstd) + row);
+    if (int(lane) < side.words)
+      tc::copy_word(dst + ring.side + 16 + 4 * lane,
+                    side.scale + (row >> 7) * side.row_tiles + lane * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4);
+    tc::copied_words_arrive(bar);
+    ++issued;
+    row += gridDim.x;
+  }
   // After a wait was given up: lets the copies in flight land (or a bounded time pass).
   __device__ __forceinline__ void settle(const Ring& ring) const {
     const long long t0 = clock64();
@@ -597,6 +630,18 @@ __device__ __forceinline__ void ring_start(RingFeed& feed, uint32_t* gave_up, co
     *gave_up = 0;
     tc::mbar_init_fence();
     for (int i = 0; i < ring.slots; ++i) feed.next<kVec>(ring);
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ void ring_start(RingFeed& feed, uint32_t* gave_up, const Ring& ring, const RingFeed::Side& side) {
+  if (threadIdx.x < 32) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < ring.slots; ++i) tc::mbar_init(tc::smem_addr(&feed.h->full[i]), 1 + 32);
+      *gave_up = 0;
+      tc::mbar_init_fence();
+    }
+    __syncwarp();
+    for (int i = 0; i < ring.slots; ++i) feed.next(ring, side);
   }
   __syncthreads();
 }
@@ -751,7 +796,10 @@ __global__ void __launch_bounds__(TH, BLOCKS)
   grid_dependency_sync();
   RingFeed feed{h, slots, static_cast<const char*>(p.dy), static_cast<const char*>(p.x), p.ld_dy * T::kBytes,
                 p.ld_x * kXBytes, blockIdx.x, p.rows, uint32_t(p.cols * T::kBytes), uint32_t(p.cols * kXBytes), 0};
-  ring_start<kVec>(feed, &s_gave_up, ring);
+  const int64_t row_tiles = scale_tile_cols((p.cols + kCkptBlock - 1) / kCkptBlock) * 512;
+  const RingFeed::Side side{p.mean, p.rstd, p.x_scale, row_tiles, kCodes ? int(row_tiles / 512) : 0};
+  if constexpr (kVec) ring_start(feed, &s_gave_up, ring, side);
+  else ring_start<false>(feed, &s_gave_up, ring);
   const int t = threadIdx.x;
   {
     const int cols = int(p.cols);
@@ -766,62 +814,59 @@ __global__ void __launch_bounds__(TH, BLOCKS)
         dw[i][k] = db[i][k] = Two(0.0f);
       }
     }
-    // the statistics and scales of a row are fetched a whole row ahead: their latency passes
-    // behind the row before
-    constexpr int NS = kVec ? NV : 1;  // scales: of a thread's pieces, or of block t
+    // kVec: a row's statistics and scales come with it.  Else they are fetched a whole row ahead, the scales
+    // two: their latency passes behind the rows before
     struct Stats {
       float mean, rstd;
-      uint32_t scale[NS];
+      uint32_t scale;  // of block t
     };
     const int blocks = (cols + kCkptBlock - 1) / kCkptBlock;
-    int at[NS];  // byte of a scale inside a row's tiles
-    if constexpr (kCodes) {
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const int b = kVec ? (t + i * TH) * 8 / kCkptBlock : t;
-        at[i] = b < blocks ? (b >> 2) * 512 + (b & 3) : -1;
-      }
-    }
-    const int64_t row_tiles = scale_tile_cols((cols + kCkptBlock - 1) / kCkptBlock) * 512;
+    const int at = kCodes && !kVec && t < blocks ? (t >> 2) * 512 + (t & 3) : -1;  // byte of the scale inside a row's tiles
     auto fetch = [&](int64_t row, Stats& st) {
       if (row >= p.rows) return;
       st.mean = p.mean[row];
       st.rstd = p.rstd[row];
-      if constexpr (kCodes) {
-        const uint8_t* sr = p.x_scale + (row >> 7) * row_tiles + (row & 31) * 16 + ((row >> 5) & 3) * 4;
-#pragma unroll
-        for (int i = 0; i < NS; ++i)
-          if (at[i] >= 0) st.scale[i] = sr[at[i]];
-      }
+      if (kCodes && at >= 0) st.scale = p.x_scale[(row >> 7) * row_tiles + (row & 31) * 16 + ((row >> 5) & 3) * 4 + at];
     };
     Stats next = {};
-    fetch(blockIdx.x, next);
+    if constexpr (!kVec) fetch(blockIdx.x, next);
     int third = 0;
-    uint32_t later = 0;  // kVec false: the scale of block t two rows ahead
+    uint32_t later = 0;  // the scale of block t two rows ahead
     if constexpr (kCodes && !kVec) {
-      if (t < 64) s_scale[0][t] = scale_value(next.scale[0]);
+      if (t < 64) s_scale[0][t] = scale_value(next.scale);
       Stats st = {};
       fetch(blockIdx.x + int64_t(gridDim.x), st);
-      later = st.scale[0];
+      later = st.scale;
       __syncthreads();
     }
     int s = 0, half = 0;
     uint32_t phase = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-      const Stats now = next;
-      fetch(row + gridDim.x, next);
+      Stats now = next;
+      if constexpr (!kVec) fetch(row + gridDim.x, next);
       const float* scales = s_scale[kCodes && !kVec ? third : 0];
       if constexpr (kCodes && !kVec) {
         if (++third == 3) third = 0;
         if (t < 64) s_scale[third][t] = scale_value(later);
         Stats st = {};
         fetch(row + 2 * int64_t(gridDim.x), st);
-        later = st.scale[0];
+        later = st.scale;
       }
       const bool good = tc::mbar_wait(tc::smem_addr(&h->full[s]), phase, gave_up);  // as in the forward pass
       const char* slot = slots + s * ring.slot_bytes;
       const char* dy_row = slot + ring_offset<kVec>(p.dy, row * p.ld_dy * T::kBytes);
       const char* x_row = slot + ring.second + ring_offset<kVec>(p.x, row * p.ld_x * kXBytes);
+      float one[NV];  // what a piece's values are multiplied by
+      if constexpr (kVec) {
+        const float2 st = *reinterpret_cast<const float2*>(slot + ring.side);
+        now.mean = st.x;
+        now.rstd = st.y;
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        one[i] = now.rstd;
+        if constexpr (kCodes && kVec) one[i] *= scale_value(reinterpret_cast<const uint8_t*>(slot + ring.side + 16)[(t + i * TH) / (kCkptBlock / 8)]);
+      }
       const Two shift(kFused ? -now.mean * now.rstd : -now.mean);
       // the piece's dy and xh, as pairs
       auto piece = [&](int i, Two (&dy)[4], Two (&xh)[4]) {
@@ -844,11 +889,10 @@ __global__ void __launch_bounds__(TH, BLOCKS)
         } else {
           x = ring_piece<T, kVec, TH>(x_row, i, cols);
         }
-        const float one = kCodes && kVec ? scale_value(now.scale[kVec ? i : 0]) * now.rstd : now.rstd;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           dy[k] = Two(e.v[2 * k], e.v[2 * k + 1]);
-          const Two mul = kCodes && !kVec ? Two(f.v[2 * k], f.v[2 * k + 1]) : Two(one);
+          const Two mul = kCodes && !kVec ? Two(f.v[2 * k], f.v[2 * k + 1]) : Two(one[i]);
           xh[k] = normalised<kFused>(Two(x.v[2 * k], x.v[2 * k + 1]), mul, shift);
         }
       };
@@ -873,7 +917,13 @@ __global__ void __launch_bounds__(TH, BLOCKS)
       s1.get(lo, hi);
       sum[1] = lo + hi;
       ring_sum<TH>(sum, h, half);
-      if (t == 0 && row != blockIdx.x) feed.next<kVec>(ring);  // every thread is past the row before
+      if (row != blockIdx.x) {  // every thread is past the row before
+        if constexpr (kVec) {
+          if (t < 32) feed.next(ring, side);
+        } else {
+          if (t == 0) feed.next<false>(ring);
+        }
+      }
       // dx = rstd g - rstd mean(g) - xh rstd mean(g xh)
       const Two r2(now.rstd), c0(-now.rstd * (sum[0] * inv)), c1(-now.rstd * (sum[1] * inv));
 #pragma unroll
@@ -964,7 +1014,7 @@ bool ring_rows(int64_t rows, int64_t cols, bool odd, const DeviceInfo& dev) {
 template <class T, bool kVec, int TH, int NV, int BLOCKS>
 cudaError_t forward_ring(const NormForwardParams& p, int wdtype, const DeviceInfo& dev, unsigned* given_up,
                          cudaStream_t stream) {
-  const Ring ring = ring_of(p.cols * T::kBytes + (kVec ? 0 : 30), 0, BLOCKS);
+  const Ring ring = ring_of(p.cols * T::kBytes + (kVec ? 0 : 30), 0, 0, BLOCKS);
   auto kernel = k_norm_forward_ring<T, kVec, TH, NV, BLOCKS>;
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring.smem));
@@ -1017,7 +1067,8 @@ template <class T, bool kCodes, bool kVec, int TH, int NV, int BLOCKS>
 cudaError_t backward_ring(const NormBackwardParams& p, int wdtype, const DeviceInfo& dev, unsigned* given_up,
                           unsigned* blocks, cudaStream_t stream) {
   constexpr int kPad = kVec ? 0 : 30;
-  const Ring ring = ring_of(p.cols * T::kBytes + kPad, p.cols * (kCodes ? 1 : T::kBytes) + kPad, BLOCKS);
+  const Ring ring = ring_of(p.cols * T::kBytes + kPad, p.cols * (kCodes ? 1 : T::kBytes) + kPad,
+                            kVec ? (kCodes ? 16 + 64 : 16) : 0, BLOCKS);
   auto kernel = k_norm_backward_ring<T, kCodes, kVec, TH, NV, BLOCKS>;
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring.smem));

@@ -38,6 +38,14 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar, uint32
       "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [r]; }" ::"r"(bar), "r"(cta)
       : "memory");
 }
+// Copies a 32-bit word from global to shared memory in the background; the barrier counts an arrival of
+// the thread (one that its initial count includes) once the words it copied so far are there.
+__device__ __forceinline__ void copy_word(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copied_words_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
