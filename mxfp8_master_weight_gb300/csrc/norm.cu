@@ -1099,11 +1099,15 @@ cudaError_t backward(const NormBackwardParams& p, int wdtype, const DeviceInfo& 
           : pieces <= 512 ? backward_ring<T, kCodes, false, 256, 2, 2>(p, wdtype, dev, given_up, &blocks, stream)
                           : backward_ring<T, kCodes, false, 512, 2, 1>(p, wdtype, dev, given_up, &blocks, stream);
     } else {
+      // blocks per SM: BF16 rows are bound by arithmetic and its waits, which more warps fill; F32 rows by
+      // the bytes under way, which fewer and deeper rings keep up (16384 x 4096 with two and with three
+      // blocks: BF16 72.9 and 65.3 us, from codes 82.0 and 75.7; F32 100.8 and 108.5)
+      constexpr bool kNarrow = T::kBytes == 2;
       e = pieces <= 32    ? backward_ring<T, kCodes, true, 32, 1, 20>(p, wdtype, dev, given_up, &blocks, stream)
-          : pieces <= 64  ? backward_ring<T, kCodes, true, 32, 2, 16>(p, wdtype, dev, given_up, &blocks, stream)
-          : pieces <= 128 ? backward_ring<T, kCodes, true, 64, 2, 8>(p, wdtype, dev, given_up, &blocks, stream)
-          : pieces <= 256 ? backward_ring<T, kCodes, true, 128, 2, 4>(p, wdtype, dev, given_up, &blocks, stream)
-          : pieces <= 512 ? backward_ring<T, kCodes, true, 256, 2, 2>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 64  ? backward_ring<T, kCodes, true, 32, 2, kNarrow ? 20 : 16>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 128 ? backward_ring<T, kCodes, true, 64, 2, kNarrow ? 12 : 8>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 256 ? backward_ring<T, kCodes, true, 128, 2, kNarrow ? 6 : 4>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 512 ? backward_ring<T, kCodes, true, 256, 2, kNarrow ? 3 : 2>(p, wdtype, dev, given_up, &blocks, stream)
           : pieces <= 768 ? backward_ring<T, kCodes, true, 256, 3, 2>(p, wdtype, dev, given_up, &blocks, stream)
                           : backward_ring<T, kCodes, true, 512, 2, 1>(p, wdtype, dev, given_up, &blocks, stream);
     }
@@ -1134,9 +1138,9 @@ cudaError_t backward(const NormBackwardParams& p, int wdtype, const DeviceInfo& 
 
 }  // namespace
 
-// Two blocks per SM for long rows; more of the small blocks of short ones.
+// As many as the blocks of a ring, of BF16 rows, that run at once on 152 SMs.
 int64_t norm_partials(int64_t rows, int64_t cols) {
-  const int64_t most = cols <= 256 ? 3040 : (cols <= 512 ? 2432 : (cols <= 1024 ? 1216 : (cols <= 2048 ? 608 : 304)));
+  const int64_t most = cols <= 512 ? 3040 : (cols <= 1024 ? 1824 : (cols <= 2048 ? 912 : (cols <= 4096 ? 456 : 304)));
   return rows < most ? rows : most;
 }
 
