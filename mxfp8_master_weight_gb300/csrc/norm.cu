@@ -560,10 +560,10 @@ struct RingFeed {
     for (uintptr_t q = u.to; q < end; ++q) slot[q - origin] = *reinterpret_cast<const char*>(q);
     return u;
   }
+  // The next row into slot s.
   template <bool kVec>
-  __device__ __forceinline__ void next(const Ring& ring) {
+  __device__ __forceinline__ void next(const Ring& ring, uint32_t s) {
     if (row >= rows) return;
-    const uint32_t s = issued % uint32_t(ring.slots);
     char* slot = slots + s * ring.slot_bytes;
     const uint32_t bar = tc::smem_addr(&h->full[s]), dst = tc::smem_addr(slot);
     if constexpr (kVec) {
@@ -593,19 +593,19 @@ struct RingFeed {
     int64_t row_tiles;
     int words;
   };
-  __device__ __forceinline__ void next(const Ring& ring, const Side& side) {
+  __device__ __forceinline__ void next(const Ring& ring, uint32_t s, const Side& side) {
     if (row >= rows) return;
-    const uint32_t s = issued % uint32_t(ring.slots), lane = threadIdx.x & 31;
+    const uint32_t lane = threadIdx.x & 31;
     const uint32_t bar = tc::smem_addr(&h->full[s]), dst = tc::smem_addr(slots + s * ring.slot_bytes);
     if (lane == 0) {
       tc::mbar_expect(bar, a_bytes + b_bytes);
       tc::bulk_load(dst, a + row * a_pitch, a_bytes, bar);
       tc::bulk_load(dst + ring.second, b + row * b_pitch, b_bytes, bar);
     }
-    if (lane < 2) tc::copy_word(dst + ring.side + 4 * lane, (lane == 0 ? side.mean : side.rstd) + row);
-    if (int(lane) < side.words)
+    if (int(lane) < side.words)  // 16 at most
       tc::copy_word(dst + ring.side + 16 + 4 * lane,
-                    side.scale + (row >> 7) * side.row_tiles + lane * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4);
+                    side.scale + (row >> 7) * side.row_tiles + (lane * 512 + (uint32_t(row) & 31) * 16 + ((uint32_t(row) >> 3) & 12)));
+    if (lane >= 30) tc::copy_word(dst + ring.side + 4 * (lane - 30), (lane == 30 ? side.mean : side.rstd) + row);
     tc::copied_words_arrive(bar);
     ++issued;
     row += gridDim.x;
@@ -629,7 +629,7 @@ __device__ __forceinline__ void ring_start(RingFeed& feed, uint32_t* gave_up, co
     for (int i = 0; i < ring.slots; ++i) tc::mbar_init(tc::smem_addr(&feed.h->full[i]), 1);
     *gave_up = 0;
     tc::mbar_init_fence();
-    for (int i = 0; i < ring.slots; ++i) feed.next<kVec>(ring);
+    for (int i = 0; i < ring.slots; ++i) feed.next<kVec>(ring, i);
   }
   __syncthreads();
 }
@@ -641,7 +641,7 @@ __device__ __forceinline__ void ring_start(RingFeed& feed, uint32_t* gave_up, co
       tc::mbar_init_fence();
     }
     __syncwarp();
-    for (int i = 0; i < ring.slots; ++i) feed.next(ring, side);
+    for (int i = 0; i < ring.slots; ++i) feed.next(ring, i, side);
   }
   __syncthreads();
 }
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
         for (int k = 0; k < 8; ++k) sum[0] += x[i].v[k];
       }
       ring_sum<TH>(sum, h, half);
-      if (t == 0) feed.next<kVec>(ring);  // every thread has the row in registers
+      if (t == 0) feed.next<kVec>(ring, s);  // every thread has the row in registers
       const float mean = sum[0] * inv;
       sum[0] = 0.0f;
 #pragma unroll
@@ -918,10 +918,11 @@ __global__ void __launch_bounds__(TH, BLOCKS)
       sum[1] = lo + hi;
       ring_sum<TH>(sum, h, half);
       if (row != blockIdx.x) {  // every thread is past the row before
+        const uint32_t before = s == 0 ? ring.slots - 1 : s - 1;
         if constexpr (kVec) {
-          if (t < 32) feed.next(ring, side);
+          if (t < 32) feed.next(ring, before, side);
         } else {
-          if (t == 0) feed.next<false>(ring);
+          if (t == 0) feed.next<false>(ring, before);
         }
       }
       // dx = rstd g - rstd mean(g) - xh rstd mean(g xh)
