@@ -477,14 +477,18 @@ __global__ void __launch_bounds__(1024) k_norm_backward_long(const __grid_consta
 }
 
 // ------------------------------------------------------------------------------ rings
-// Many aligned rows of up to 8192 columns: persistent blocks, each with a ring of rows in shared
-// memory that thread 0 keeps full with bulk copies, so about 200 KB per SM are in flight
-// whatever the warps wait for.  A thread owns fixed columns, NV pieces of 8, and keeps what
-// belongs to a column (weight, bias, running gradients) in registers over all rows.  A row takes
-// two barriers (one backward) of its block; the first of them also says that a slot has been
-// read, and thread 0 refills it.  Several blocks per SM fill each other's waits, so the blocks are
-// as small as a row allows: TH threads.
-constexpr int kRingBytes = 216 * 1024;  // shared memory of an SM that the rings of its blocks share
+// Many rows of up to 8192 columns: persistent blocks, each with a ring of rows in shared memory
+// that thread 0 (with the statistics: warp 0) keeps full with copies in the background, whatever the
+// warps wait for.  A thread owns fixed columns, NV pieces of 8, and keeps what belongs to a column
+// (weight, bias, running gradients) in registers over all rows.  A row takes two barriers (one
+// backward) of its block; the first of them also says that a slot has been read, and it is refilled.
+// Several blocks per SM fill each other's waits, so the blocks are as small as a row allows: TH threads.
+constexpr int kRingBytes = 216 * 1024;  // shared memory of an SM that its blocks take
+// Rows under way: three per block cover the latency; more bytes than this per SM (23 MB in all) make HBM
+// slower (16384 x 6144 backward BF16 with three rows, 147 KB, 99 us, with four 111 us; F32 from codes with two
+// rows, 123 KB, 155 us, with three 171 us).  A single block per SM takes what fits (8192 x 8192 BF16 backward
+// 80 us with three, 71 with six).
+constexpr int kRingFlight = 150 * 1024;
 constexpr int kRingMaxSlots = 8;
 constexpr int kRingHead = 384;          // barriers and sums
 
@@ -499,9 +503,12 @@ Ring ring_of(int64_t first, int64_t second, int side, int blocks) {
   r.second = int32_t((first + 127) / 128 * 128);
   r.side = int32_t(r.second + (second + 127) / 128 * 128);
   r.slot_bytes = r.side + side;
-  const int n = (kRingBytes / blocks - 1024 - kRingHead) / r.slot_bytes;  // 1 KB per block is the system's
-  r.slots = n < kRingMaxSlots ? n : kRingMaxSlots;
-  r.smem = uint32_t(kRingHead + r.slots * r.slot_bytes);
+  const int fit = (kRingBytes / blocks - 1024 - kRingHead) / r.slot_bytes;  // 1 KB per block is the system's
+  const int flight = blocks == 1 ? kRingMaxSlots : kRingFlight / (blocks * r.slot_bytes);
+  const int most = blocks == 1 ? kRingMaxSlots : 3;
+  r.slots = flight < 2 ? 2 : (flight < most ? flight : most);
+  if (fit < r.slots) r.slots = fit;
+  r.smem = uint32_t(kRingBytes / blocks - 1024);  // all of it: with room for one more block on an SM another had one less
   return r;
 }
 
@@ -1046,7 +1053,7 @@ cudaError_t forward(const NormForwardParams& p, int wdtype, const DeviceInfo& de
     if (pieces <= 64) return forward_ring<T, true, 32, 2, 20>(p, wdtype, dev, given_up, stream);
     if (pieces <= 128) return forward_ring<T, true, 64, 2, 12>(p, wdtype, dev, given_up, stream);
     if (pieces <= 256) return forward_ring<T, true, 128, 2, 6>(p, wdtype, dev, given_up, stream);
-    if (pieces <= 512) return forward_ring<T, true, 256, 2, 3>(p, wdtype, dev, given_up, stream);
+    if (pieces <= 512) return forward_ring<T, true, 256, 2, T::kBytes == 2 ? 3 : 2>(p, wdtype, dev, given_up, stream);
     if (pieces <= 768) return forward_ring<T, true, 256, 3, 2>(p, wdtype, dev, given_up, stream);
     return forward_ring<T, true, 256, 4, 2>(p, wdtype, dev, given_up, stream);
   }
