@@ -7,13 +7,13 @@
 // the tokens its NT = 16 .. 128 columns, and 1 to 8 CTAs share a tile, each with its part
 // of k.  Their partial sums stay in shared memory, laid out as lines of the output; after a cluster
 // barrier each CTA adds its share of the lines over the cluster in rank order and writes it.  No
-// workspace, no atomics: the result depends on the shape alone.
+// workspace, no atomics: the result depends on the shape and the alignment alone.
 //
-// Measured (launches that follow one another, weights larger than L2 in turn): 1 x 4096 x 4096 5.7 us,
-// 64 x 4096 x 4096 8.2, 1 x 8192 x 8192 14.4 (4.7 TB/s of weight), 64 x 8192 x 8192 16.7.  Streaming the weight
-// takes 10.3 us of the last two; the rest is the start (barriers, tensor memory, first bytes from HBM)
+// Measured, launches that follow one another with three weights in turn: 1 x 4096 x 4096 5.6 us and 64 x
+// 4096 x 4096 6.9 (from L2), 1 x 8192 x 8192 14.4 (from HBM, 4.7 TB/s of weight), 64 x 8192 x 8192 16.7.
+// Streaming the weight takes 10.3 us of the last two; the rest is the start (barriers, tensor memory, first bytes from HBM)
 // and the join.  Reading the sums four at a time, with every rank's reads under way at once, took 1.6 us
-// from the last and 1.2 us from the second: a rank's read costs about 0.4 us when the ranks take turns.
+// from the last: a rank's read costs about 0.4 us when the ranks take turns.
 #include <type_traits>
 
 #include <cuda.h>
@@ -383,10 +383,15 @@ cudaError_t launch_gemm_split(const GemmParams& p, unsigned* given_up, const Dev
   }
   const int nt = g.n <= 16 ? 16 : (g.n <= 32 ? 32 : (g.n <= 64 ? 64 : 128));
   const int64_t tiles = ((g.m + 127) / 128) * ((g.n + nt - 1) / nt), nk = (g.k + kBlockK - 1) / kBlockK;
-  // CTAs for two per SM, each with two stages or more: 64 x 8192 x 8192 takes 21.4 us with one CTA
-  // per SM and 18.2 us with two (with four, half of them in a second round, 24.5 us)
+  // CTAs that share a tile, each with two stages or more.  Two CTAs per SM where the copies of one do not
+  // fill the SM's share of HBM or the realigning warps bound it, else one: 64 x 8192 x 8192 18.1 us with
+  // one, 16.7 with two (23 with four, half of them in a second round), 1024 x 1024 x 8192 14.0 and 15.5.
+  // Eight to a tile join slower than four; they pay on half of the SMs (64 x 1024 x 4096 6.0 and 6.5 us,
+  // 64 x 2048 x 4096 7.4 and 6.5), or with little to join (1 x 4096 x 4096 5.5 and 5.7).
+  const int64_t two = nt <= 64 || !(g.a.aligned && g.b.aligned) ? 2 * dev.sms : dev.sms;
+  const int64_t eight = nt == 16 ? 2 * dev.sms : dev.sms / 2;
   int split = 1;
-  while (split < kMaxSplit && tiles * split * 2 <= 2 * dev.sms && nk >= split * 4) split *= 2;
+  while (split < kMaxSplit && tiles * split * 2 <= (split == 4 ? eight : two) && nk >= split * 4) split *= 2;
   switch (nt) {
     case 16: return launch<16>(g, swapped, split, given_up, stream, what);
     case 32: return launch<32>(g, swapped, split, given_up, stream, what);
