@@ -18,10 +18,9 @@
 // leaves one row of partial sums, and a second kernel adds the partial rows in their order, so the
 // sums do not depend on the run.
 //
-// Measured at 16384 x 6144: forward BF16 67.5 us (6.0 TB/s, bound by HBM), backward BF16 92 us, from an
-// 8-bit checkpoint 113 us for 504 MB: there decoding and two passes of arithmetic over the row take 55 %
-// of the issue slots, and two blocks per SM leave waits for statistics and barriers open.  1 x 4096
-// forward: 4.5 us, the time of a call.
+// Measured at 16384 x 6144: forward BF16 61 us (6.6 TB/s, bound by HBM), backward BF16 99 us (6.1 TB/s), from
+// an 8-bit checkpoint 94 us for 504 MB: there decoding and two passes of arithmetic over the row take 56 %
+// of the issue slots at 16 warps per SM.  1 x 4096 forward: 4.6 us, the time of a call.
 #include <type_traits>
 
 #include "common.cuh"
