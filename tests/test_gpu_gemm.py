@@ -224,3 +224,36 @@ def test_refusals():
     assert status(q, s, q, s, out.bfloat16(), out, 64, 64, 128) == 3
     big = torch.zeros(64 * 64 + 16, device="cuda")
     assert status(q, s, q, s, big[16:].view(64, 64), big[:4096].view(64, 64), 64, 64, 128) == 1
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 256), (300, 1, 512), (16, 1000, 1024), (13, 130, 4096), (1030, 29, 2048),
+                                   (50, 516, 640), (516, 64, 1100), (64, 2052, 4096), (96, 130, 2304), (515, 500, 4096)])
+def test_few_tiles(m, n, k, pad, dtype):
+    """One to eight CTAs per tile, either operand on the tile's lanes; output rows on 16 bytes, whole or
+    with a ragged end, and off them; lines of the tile past the output."""
+    rng = np.random.default_rng(m + n + k)
+    a, qa, sa = operand(rng, m, k, False, 128, -(-k // 16) * 16)
+    b, qb, sb = operand(rng, n, k, False, 32, -(-k // 16) * 16)
+    pitch = -(-n // 8) * 8 + 8 + pad
+    buf = torch.full((m, pitch), -3.0, dtype=DT[dtype], device="cuda")
+    c = torch.randn(m, pitch, device="cuda") * k
+    for addend in (None, c[:, :n]):
+        api.mxfp8_gemm(qa, sa, qb, sb, addend, buf[:, :n], m, n, k, b_block=32)
+        api.mxfp8_device_status()
+        check(buf[:, :n], a, b, k, None if addend is None else ref.as64(addend))
+        assert bool((buf[:, n:] == -3.0).all())
+
+
+def test_one_row_many_times():
+    """Launches that follow one another, most lines of their tiles empty: equal bits every time."""
+    rng = np.random.default_rng(8)
+    a, qa, sa = operand(rng, 1, 4096, False, 128)
+    b, qb, sb = operand(rng, 2048, 4096, False, 32)
+    outs = torch.empty(64, 1, 2048, device="cuda")
+    for o in outs:
+        api.mxfp8_gemm(qa, sa, qb, sb, None, o, 1, 2048, 4096, b_block=32)
+    api.mxfp8_device_status()
+    check(outs[0], a, b, 4096)
+    assert bool((outs == outs[:1]).all())

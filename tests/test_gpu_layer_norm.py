@@ -258,3 +258,22 @@ def test_many_rows(cols, dtype):
         got = backward(dy, q, s, w, mean, rstd, out=dy)  # in place
         check_backward(dy64, kept, ref.as64(w), ref.as64(mean), ref.as64(rstd), *got)
     api.mxfp8_device_status()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(1217, 256), (2500, 512), (3700, 1024), (1900, 2048), (1400, 4096), (700, 8192)])
+def test_many_rows_of_each_ring(rows, cols, dtype):
+    """Row counts that fill the blocks of a ring unevenly, each number of blocks per SM; statistics and scales
+    that differ from row to row."""
+    x, w, b = data(rows, cols, dtype, "f32", shift=0.5)
+    x *= torch.exp2(torch.arange(rows, device="cuda") % 9 - 4.0)[:, None].to(x.dtype)
+    y, mean, rstd = forward(x, w, b)
+    check_forward(ref.as64(x), ref.as64(w), ref.as64(b), y, mean, rstd)
+    dy = torch.randn(rows, cols, device="cuda").to(x.dtype)
+    check_backward(*map(ref.as64, (dy, x, w, mean, rstd)), *backward(dy, x, None, w, mean, rstd))
+    q = torch.empty(rows, cols, dtype=torch.uint8, device="cuda")
+    s = torch.empty(api.mxfp8_swizzled_scales_size(rows, -(-cols // 128)), dtype=torch.uint8, device="cuda")
+    api.mxfp8_checkpoint_save(x, q, s, None, None, rows, cols)
+    kept = ref.quantise(ref.as64(x))[0]
+    check_backward(ref.as64(dy), kept, ref.as64(w), ref.as64(mean), ref.as64(rstd), *backward(dy, q, s, w, mean, rstd))
+    api.mxfp8_device_status()
