@@ -652,10 +652,12 @@ __device__ __forceinline__ void ring_start(RingFeed& feed, uint32_t* gave_up, co
   __syncthreads();
 }
 
-// Column of element k of piece i: eight neighbours (kVec), or neighbours across the threads.
+// Column of element k of piece i: eight neighbours (kVec), or neighbours across a warp, whose piece spans
+// 256 columns: two blocks of a checkpoint, k < 4 and k >= 4.
 template <bool kVec, int TH>
 __device__ __forceinline__ int ring_col(int i, int k) {
-  return kVec ? (int(threadIdx.x) + i * TH) * 8 + k : (i * 8 + k) * TH + int(threadIdx.x);
+  return kVec ? (int(threadIdx.x) + i * TH) * 8 + k
+              : (int(threadIdx.x >> 5) + i * (TH / 32)) * 256 + k * 32 + int(threadIdx.x & 31);
 }
 // A piece of a row in shared memory; zeros past the row.
 template <class T, bool kVec, int TH>
@@ -877,7 +879,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
       // the piece's dy and xh, as pairs
       auto piece = [&](int i, Two (&dy)[4], Two (&xh)[4]) {
         const Eight e = ring_piece<T, kVec, TH>(dy_row, i, cols);
-        Eight x, f;
+        Eight x;
         if constexpr (kCodes && kVec) {
           x = load_codes(reinterpret_cast<const uint8_t*>(x_row) + ring_col<true, TH>(i, 0), 8, true);
         } else if constexpr (kCodes) {
@@ -889,8 +891,6 @@ __global__ void __launch_bounds__(TH, BLOCKS)
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(two)));
             x.v[k] = f16_lo(h2);
             x.v[k + 1] = f16_hi(h2);
-            f.v[k] = c0 < cols ? scales[c0 / kCkptBlock] * now.rstd : 0.0f;
-            f.v[k + 1] = c1 < cols ? scales[c1 / kCkptBlock] * now.rstd : 0.0f;
           }
         } else {
           x = ring_piece<T, kVec, TH>(x_row, i, cols);
@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           dy[k] = Two(e.v[2 * k], e.v[2 * k + 1]);
-          const Two mul = kCodes && !kVec ? Two(f.v[2 * k], f.v[2 * k + 1]) : Two(one[i]);
+          const Two mul(kCodes && !kVec ? scales[ring_col<false, TH>(i, 0) / kCkptBlock + (k >> 1)] * now.rstd : one[i]);
           xh[k] = normalised<kFused>(Two(x.v[2 * k], x.v[2 * k + 1]), mul, shift);
         }
       };
@@ -1045,8 +1045,10 @@ cudaError_t forward(const NormForwardParams& p, int wdtype, const DeviceInfo& de
       if (pieces <= 64) return forward_ring<T, false, 64, 1, 12>(p, wdtype, dev, given_up, stream);
       if (pieces <= 128) return forward_ring<T, false, 128, 1, 6>(p, wdtype, dev, given_up, stream);
       if (pieces <= 256) return forward_ring<T, false, 256, 1, 4>(p, wdtype, dev, given_up, stream);
+      if (pieces <= 384) return forward_ring<T, false, 192, 2, 4>(p, wdtype, dev, given_up, stream);
       if (pieces <= 512) return forward_ring<T, false, 256, 2, 3>(p, wdtype, dev, given_up, stream);
-      return forward_ring<T, false, 512, 2, 1>(p, wdtype, dev, given_up, stream);
+      if (pieces <= 768) return forward_ring<T, false, 256, 3, 2>(p, wdtype, dev, given_up, stream);
+      return forward_ring<T, false, 256, 4, 2>(p, wdtype, dev, given_up, stream);
     }
     if (pieces <= 32) return forward_ring<T, true, 32, 1, 24>(p, wdtype, dev, given_up, stream);
     if (pieces <= 64) return forward_ring<T, true, 32, 2, 20>(p, wdtype, dev, given_up, stream);
@@ -1100,10 +1102,15 @@ cudaError_t backward(const NormBackwardParams& p, int wdtype, const DeviceInfo& 
     e = given_up_address(dev.device, &given_up);
     if (e != cudaSuccess) return e;
     if (odd) {
+      // by figures: 16384 x 3001 BF16 77 us (256 threads, two blocks 89), F32 93 with two blocks, 103 with
+      // three; 16384 x 6143 from codes 143 us (512 threads, one block 255, most of it scales per element)
       e = pieces <= 64    ? backward_ring<T, kCodes, false, 64, 1, 8>(p, wdtype, dev, given_up, &blocks, stream)
-          : pieces <= 128 ? backward_ring<T, kCodes, false, 128, 1, 5>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 128 ? (kCodes || T::kBytes == 2 ? backward_ring<T, kCodes, false, 64, 2, 8>(p, wdtype, dev, given_up, &blocks, stream)
+                                                      : backward_ring<T, kCodes, false, 128, 1, 5>(p, wdtype, dev, given_up, &blocks, stream))
           : pieces <= 256 ? backward_ring<T, kCodes, false, 256, 1, 3>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 384 ? backward_ring<T, kCodes, false, 192, 2, kCodes || T::kBytes == 2 ? 3 : 2>(p, wdtype, dev, given_up, &blocks, stream)
           : pieces <= 512 ? backward_ring<T, kCodes, false, 256, 2, 2>(p, wdtype, dev, given_up, &blocks, stream)
+          : pieces <= 768 ? backward_ring<T, kCodes, false, 256, 3, 2>(p, wdtype, dev, given_up, &blocks, stream)
                           : backward_ring<T, kCodes, false, 512, 2, 1>(p, wdtype, dev, given_up, &blocks, stream);
     } else {
       // blocks per SM: BF16 rows are bound by arithmetic and its waits, which more warps fill; F32 rows by
