@@ -573,9 +573,8 @@ struct RingFeed {
     char* slot = slots + s * ring.slot_bytes;
     const uint32_t bar = tc::smem_addr(&h->full[s]), dst = tc::smem_addr(slot);
     if constexpr (kVec) {
-      tc::mbar_expect(bar, a_bytes + b_bytes);
+      tc::mbar_expect(bar, a_bytes);  // the forward pass: one operand
       tc::bulk_load(dst, a + row * a_pitch, a_bytes, bar);
-      if (b_bytes != 0) tc::bulk_load(dst + ring.second, b + row * b_pitch, b_bytes, bar);
     } else {
       auto copy = [&](uint32_t to, const char* m, int64_t pitch, const Units& u) {
         const uintptr_t origin = reinterpret_cast<uintptr_t>(m + row * pitch) & ~uintptr_t(15);
