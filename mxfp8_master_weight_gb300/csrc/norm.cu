@@ -19,7 +19,7 @@
 // sums do not depend on the run.
 //
 // Measured at 16384 x 6144: forward BF16 61 us (6.6 TB/s, bound by HBM), backward BF16 99 us (6.1 TB/s), from
-// an 8-bit checkpoint 94 us for 504 MB: there decoding and two passes of arithmetic over the row take 56 %
+// an 8-bit checkpoint 98 us for 504 MB: there decoding and two passes of arithmetic over the row take 56 %
 // of the issue slots at 16 warps per SM.  1 x 4096 forward: 4.6 us, the time of a call.
 #include <type_traits>
 
@@ -778,9 +778,12 @@ __global__ void __launch_bounds__(TH, BLOCKS)
   }
 }
 
-// xh = (x - mean) rstd of two values.  F32 input keeps the difference; BF16 values and codes,
-// whose own grid is coarser than an F32 rounding of the mean by 2^16 and more, take one fused operation
-// x (f rstd) - mean rstd (f: the code's scale, a power of two).
+// xh = (x - mean) rstd of two values.  F32 input takes the difference first.  BF16 values and codes take one
+// fused operation x (f rstd) - m (f: the code's scale, a power of two; m: mean rstd rounded); what m's
+// rounding left out, the same for a whole row and up to |mean| rstd 2^-24, is added where xh enters the
+// gradient of the weight and the row's sum, and for dx to the row's constant.  Without it a constant row
+// of 1000 had xh = 2.7e-3 for 0.  (The difference first in both passes: 16384 x 4096 BF16 70.5 for 69.4 us,
+// from codes 75.4 for 73.4.)
 template <bool kFused>
 __device__ __forceinline__ Two normalised(Two x, Two mul, Two shift) {
   if constexpr (kFused) return fma2(x, mul, shift);
@@ -874,7 +877,9 @@ __global__ void __launch_bounds__(TH, BLOCKS)
         one[i] = now.rstd;
         if constexpr (kCodes && kVec) one[i] *= scale_value(reinterpret_cast<const uint8_t*>(slot + ring.side + 16)[(t + i * TH) / (kCkptBlock / 8)]);
       }
-      const Two shift(kFused ? -now.mean * now.rstd : -now.mean);
+      const float m = __fmul_rn(now.mean, now.rstd);
+      const Two shift(kFused ? -m : -now.mean);
+      const float rest = kFused ? -__fmaf_rn(now.mean, now.rstd, -m) : 0.0f;
       // the piece's dy and xh, as pairs
       auto piece = [&](int i, Two (&dy)[4], Two (&xh)[4]) {
         const Eight e = ring_piece<T, kVec, TH>(dy_row, i, cols);
@@ -910,6 +915,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const Two g = dy[k] * w[i][k];
+          if constexpr (kFused) xh[k] = xh[k] + Two(rest);
           s0 = s0 + g;
           s1 = fma2(g, xh[k], s1);
           dw[i][k] = fma2(dy[k], xh[k], dw[i][k]);
@@ -931,7 +937,8 @@ __global__ void __launch_bounds__(TH, BLOCKS)
         }
       }
       // dx = rstd g - rstd mean(g) - xh rstd mean(g xh)
-      const Two r2(now.rstd), c0(-now.rstd * (sum[0] * inv)), c1(-now.rstd * (sum[1] * inv));
+      const float by_xh = -now.rstd * (sum[1] * inv);
+      const Two r2(now.rstd), c0(__fmaf_rn(rest, by_xh, -now.rstd * (sum[0] * inv))), c1(by_xh);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (ring_col<kVec, TH>(i, 0) >= cols) continue;
