@@ -18,9 +18,10 @@
 // leaves one row of partial sums, and a second kernel adds the partial rows in their order, so the
 // sums do not depend on the run.
 //
-// Measured at 16384 x 6144: forward BF16 61 us (6.6 TB/s, bound by HBM), backward BF16 99 us (6.1 TB/s), from
+// Measured at 16384 x 6144: forward BF16 62 us (6.5 TB/s, bound by HBM), backward BF16 99 us (6.1 TB/s), from
 // an 8-bit checkpoint 98 us for 504 MB: there decoding and two passes of arithmetic over the row take 56 %
 // of the issue slots at 16 warps per SM.  1 x 4096 forward: 4.6 us, the time of a call.
+#include <cfloat>
 #include <type_traits>
 
 #include "common.cuh"
@@ -717,7 +718,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
   const int t = threadIdx.x;
   {
     const int cols = int(p.cols);
-    const float inv = 1.0f / float(cols);
+    const float count = float(cols), inv = 1.0f / count;
     Eight w[NV], b[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -742,7 +743,12 @@ __global__ void __launch_bounds__(TH, BLOCKS)
       }
       ring_sum<TH>(sum, h, half);
       if (t == 0) feed.next<kVec>(ring, s);  // every thread has the row in registers
-      const float mean = sum[0] * inv;
+      // A product with 1 / cols alone rounds twice: the mean of a constant row would be off by a last place and
+      // its deviations not zero.  Adding what is left of the sum, over cols, makes an exact quotient exact
+      // (dividing: 16384 x 6144 BF16 64.8 us for 62.3; neither 62.1).  Of an infinite sum NaN is left: fminf makes it a number,
+      // and the mean stays infinite.
+      const float near = sum[0] * inv;
+      const float mean = __fmaf_rn(fminf(__fmaf_rn(-count, near, sum[0]), FLT_MAX), inv, near);
       sum[0] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {

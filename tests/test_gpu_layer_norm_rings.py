@@ -65,3 +65,19 @@ def test_backward_of_rows_far_from_zero(cols, dtype):
     mean, rstd = statistics(kept)
     check_given(ref.as64(dy), kept, ref.as64(w), ref.as64(mean), ref.as64(rstd), *backward(dy, q, s, w, mean, rstd))
     api.mxfp8_device_status()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [1000, 1024, 3001, 6143, 7168])
+def test_forward_of_constant_rows(cols, dtype):
+    """Small whole numbers add exactly in any order, and their mean is exact: the deviations are zero, and y
+    is the bias to the last bit."""
+    value = (torch.arange(ROWS, device="cuda") % 256 + 1).float()
+    x = value[:, None].expand(-1, cols).to(DT[dtype]).contiguous()
+    w = 1 + 0.2 * torch.randn(cols, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    b = torch.randn(cols, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").to(x.dtype).float()
+    y, mean, rstd = forward(x, w, b)
+    assert torch.equal(mean, value)
+    assert torch.equal(y.float(), b.expand(ROWS, -1))
+    assert torch.allclose(rstd, torch.full_like(rstd, EPS ** -0.5), rtol=1e-6, atol=0.0)
+    api.mxfp8_device_status()
