@@ -69,7 +69,8 @@ HOST_ONLY_UNITS = ("capi.cu", "noalloc.cu", "checks.h", "linear_capi.cu")
 
 # Sources of the training operators: none of the cast's kernels is made from them.
 OPERATOR_UNITS = ("linear.h", "checkpoint.cu", "gemm.cu", "gemm_impl.cuh", "gemm_maps.cu",
-                  "gemm_maps.h", "gemm_pair.cu", "gemm_realign.cuh", "gemm_split.cu", "norm.cu", "tensor_core.cuh")
+                  "gemm_maps.h", "gemm_pair.cu", "gemm_realign.cuh", "gemm_split.cu", "norm.cu", "tensor_core.cuh",
+                  "waits.h")
 
 
 def kernel_digest() -> str:

@@ -180,7 +180,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kRealign>, 
       const uint32_t lead_full = tc::in_cta(full, 0);
       int s = 0;
       uint32_t phase = 1;
-      int64_t issued = 0;
+      uint32_t issued = 0;
       for (int64_t unit = first; unit < q.units && *gave_up == 0; unit += step) {
         const Tile t = tile_of(q, unit, tiles_m, tiles_n);
         const int am = int(t.tm * 256 + rank * 128), bn = int(t.col + rank * (t.half ? 64 : 128));
@@ -203,15 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kRealign>, 
           }
         }
       }
-      // a wait was given up: let the copies in flight land (or a bounded time pass) before leaving
-      if (*gave_up != 0 && rank == 0) {
-        const long long t0 = clock64();
-        for (int i = 0; i < q.stages && i < issued; ++i) {
-          const int64_t c = issued - 1 - i;
-          while (!tc::mbar_try(full + 8 * int(c % q.stages), uint32_t(c / q.stages) & 1) && clock64() - t0 < tc::kWaitCycles) {
-          }
-        }
-      }
+      if (*gave_up != 0 && rank == 0) tc::settle_copies(full, uint32_t(q.stages), issued);
     }
   } else if (warp == 1) {
     if (rank == 0 && tc::elect_one()) {

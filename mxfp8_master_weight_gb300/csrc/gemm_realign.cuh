@@ -113,14 +113,7 @@ __device__ __forceinline__ void realign_fetch(const RealignRing& ring, const CUt
     ++issued;
     raw.on(1, ring.depth);
   }
-  if (*gave_up != 0) {  // let the copies in flight land (or a bounded time pass) before leaving
-    const long long t0 = clock64();
-    for (uint32_t i = 0; i < uint32_t(ring.depth) && i < issued; ++i) {
-      const uint32_t c = issued - 1 - i, d = uint32_t(ring.depth);
-      while (!tc::mbar_try(ring.full + 8 * (c % d), (c / d) & 1) && clock64() - t0 < tc::kWaitCycles) {
-      }
-    }
-  }
+  if (*gave_up != 0) tc::settle_copies(ring.full, uint32_t(ring.depth), issued);
 }
 
 // Lane l of warp w (0 .. 3) of a group writes word l % 4 of the units of rows 16 (l / 4) + s, s = 4 w .. 4 w + 3.

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads + (kRealign ? 32 * kRealignWarps : 0)
     if (tc::elect_one()) {
       int s = 0;
       uint32_t phase = 1;
-      int64_t issued = 0;
+      uint32_t issued = 0;
       const int am = int(tm * 128), bn = int(tn * NT);
       const bool tma_a = !kRealign || p.a.aligned, tma_b = !kRealign || p.b.aligned;
       for (int64_t kb = k_lo; kb < k_hi; ++kb) {
@@ -233,14 +233,7 @@ __global__ void __launch_bounds__(kThreads + (kRealign ? 32 * kRealignWarps : 0)
           phase ^= 1;
         }
       }
-      if (*gave_up != 0) {  // let the copies in flight land (or a bounded time pass) before leaving
-        const long long t0 = clock64();
-        for (int i = 0; i < q.stages && i < issued; ++i) {
-          const int64_t c = issued - 1 - i;
-          while (!tc::mbar_try(full + 8 * int(c % q.stages), uint32_t(c / q.stages) & 1) && clock64() - t0 < tc::kWaitCycles) {
-          }
-        }
-      }
+      if (*gave_up != 0) tc::settle_copies(full, uint32_t(q.stages), issued);
     }
   } else if (warp == 1) {
     if (tc::elect_one()) {

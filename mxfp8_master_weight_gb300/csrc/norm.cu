@@ -616,15 +616,8 @@ struct RingFeed {
     ++issued;
     row += gridDim.x;
   }
-  // After a wait was given up: lets the copies in flight land (or a bounded time pass).
   __device__ __forceinline__ void settle(const Ring& ring) const {
-    const long long t0 = clock64();
-    for (uint32_t i = 0; i < uint32_t(ring.slots) && i < issued; ++i) {
-      const uint32_t c = issued - 1 - i;
-      while (!tc::mbar_try(tc::smem_addr(&h->full[c % uint32_t(ring.slots)]), (c / uint32_t(ring.slots)) & 1) &&
-             clock64() - t0 < tc::kWaitCycles) {
-      }
-    }
+    tc::settle_copies(tc::smem_addr(h->full), uint32_t(ring.slots), issued);
   }
 };
 

@@ -5,6 +5,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "waits.h"
+
 namespace mxfp8 {
 namespace tc {
 
@@ -61,23 +63,31 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
-// Clock cycles after which a wait is given up (about two seconds).
-constexpr long long kWaitCycles = 4000000000ll;
-
 // Waits for the barrier's phase.  False when the wait was given up, here or (through the
 // block's `gave_up` word in shared memory) by another thread of the block.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
   for (int i = 0; i < 64; ++i)
     if (mbar_try(bar, parity)) return true;
-  const long long t0 = clock64();
+  Patience patience{unsigned(clock())};
   while (!mbar_try(bar, parity)) {
     if (*gave_up != 0) return false;
-    if (clock64() - t0 > kWaitCycles) {
+    if (patience.out(unsigned(clock()))) {
       *gave_up = 1;
       return false;
     }
   }
   return true;
+}
+
+// After a wait was given up: lets the last `depth` of `issued` copies into a ring of `depth` barriers land (or a
+// bounded time pass), so that the block does not leave while they are under way.
+__device__ __forceinline__ void settle_copies(uint32_t bars, uint32_t depth, uint32_t issued) {
+  Patience patience{unsigned(clock())};
+  for (uint32_t i = 0; i < depth && i < issued; ++i) {
+    const uint32_t c = issued - 1 - i;
+    while (!mbar_try(bars + 8 * (c % depth), (c / depth) & 1) && !patience.out(unsigned(clock()))) {
+    }
+  }
 }
 
 // Counts a kernel that gave up a wait (see mxfp8_device_status).
