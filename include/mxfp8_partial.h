@@ -535,8 +535,9 @@ MXFP8_API int mxfp8_gemm(const mxfp8_tensor* a, const mxfp8_tensor* a_scale, con
 /*
  * Health of the operators' kernels: waits for `stream`, then returns 0, or MXFP8_ERR_CUDA when
  * a product or a layer norm on the current device gave up a wait on its own copies or
- * tensor-core work since the last call (every wait inside these kernels ends after about two
- * seconds; the outputs of such a call are invalid).  Not for use during stream capture.
+ * tensor-core work (every wait inside these kernels ends after about two seconds; the outputs of such a call
+ * are invalid).  Each such kernel is reported once, by the first call that sees it; those on other streams
+ * than `stream` once they have completed.  Not for use during stream capture.
  */
 MXFP8_API int mxfp8_device_status(void* stream);
 

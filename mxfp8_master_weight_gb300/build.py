@@ -25,7 +25,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 UNITS = ["capi.cu", "amax.cu", "cast_f32.cu", "cast_bf16.cu", "cast_f32_unaligned.cu",
          "cast_bf16_unaligned.cu", "cast_bf16_unaligned_f16.cu", "fused_f32.cu", "fused_bf16.cu",
          "misc.cu", "noalloc.cu", "nvfp4.cu", "linear_capi.cu", "checkpoint.cu", "gemm.cu",
-         "gemm_pair.cu", "gemm_split.cu", "gemm_maps.cu", "norm.cu"]
+         "gemm_pair.cu", "gemm_split.cu", "gemm_maps.cu", "norm.cu", "status.cu"]
 
 
 def _nvcc() -> str:
@@ -70,7 +70,7 @@ HOST_ONLY_UNITS = ("capi.cu", "noalloc.cu", "checks.h", "linear_capi.cu")
 # Sources of the training operators: none of the cast's kernels is made from them.
 OPERATOR_UNITS = ("linear.h", "checkpoint.cu", "gemm.cu", "gemm_impl.cuh", "gemm_maps.cu",
                   "gemm_maps.h", "gemm_pair.cu", "gemm_realign.cuh", "gemm_split.cu", "norm.cu", "tensor_core.cuh",
-                  "waits.h")
+                  "waits.h", "status.cu", "status.h")
 
 
 def kernel_digest() -> str:

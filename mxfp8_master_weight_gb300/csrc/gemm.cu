@@ -17,29 +17,11 @@
 //
 // This file chooses the kernel: tiles of 256 x 256 by pairs of CTAs (gemm_pair.cu), or tiles of 128
 // rows with the contraction split over a cluster (gemm_split.cu).
-#include <atomic>
-
 #include "gemm_impl.cuh"
 #include "gemm_maps.h"
+#include "status.h"
 
 namespace mxfp8 {
-
-// Kernels that gave up a wait on this device (see mxfp8_device_status).
-static __device__ unsigned g_given_up = 0;
-
-// Device address of g_given_up for the current device, looked up once per device.
-cudaError_t given_up_address(int device, unsigned** out) {
-  constexpr int kMaxDevices = 64;
-  static std::atomic<unsigned*> known[kMaxDevices];
-  unsigned* p = device < kMaxDevices ? known[device].load() : nullptr;
-  if (p == nullptr) {
-    const cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void**>(&p), g_given_up);
-    if (e != cudaSuccess) return e;
-    if (device < kMaxDevices) known[device].store(p);
-  }
-  *out = p;
-  return cudaSuccess;
-}
 
 cudaError_t launch_gemm(const GemmParams& p, const DeviceInfo& dev, cudaStream_t stream, const char** what) {
   unsigned* given_up = nullptr;
@@ -58,15 +40,6 @@ cudaError_t launch_gemm(const GemmParams& p, const DeviceInfo& dev, cudaStream_t
   const bool realigned = !(p.a.aligned && p.b.aligned) && 2 * tiles <= dev.sms && stages >= 8;
   const bool split = p.k > 0 && (p.m <= 64 || p.n <= 64 || few || realigned);
   return split ? launch_gemm_split(p, given_up, dev, stream, what) : launch_gemm_pair(p, given_up, dev, stream, what);
-}
-
-cudaError_t waits_given_up(cudaStream_t stream, unsigned* count) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(count, g_given_up, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, stream);
-  if (e != cudaSuccess) return e;
-  e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess || *count == 0) return e;
-  static const unsigned zero = 0;
-  return cudaMemcpyToSymbolAsync(g_given_up, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, stream);
 }
 
 }  // namespace mxfp8

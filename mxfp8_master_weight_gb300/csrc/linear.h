@@ -95,10 +95,6 @@ cudaError_t launch_checkpoint_restore(const CheckpointRestoreParams& p, int dtyp
 // *what names the step that failed when it is not the launch itself.
 cudaError_t launch_gemm(const GemmParams& p, const DeviceInfo& dev, cudaStream_t stream,
                         const char** what);
-// Kernels that gave up a wait count themselves at this address (of the current device).
-cudaError_t given_up_address(int device, unsigned** out);
-// Reads and clears that count (waits for the stream).
-cudaError_t waits_given_up(cudaStream_t stream, unsigned* count);
 // dtype: of x / dy; wdtype: of weight and bias (0 = F32, 1 = BF16).
 cudaError_t launch_norm_forward(const NormForwardParams& p, int dtype, int wdtype,
                                 const DeviceInfo& dev, cudaStream_t stream);

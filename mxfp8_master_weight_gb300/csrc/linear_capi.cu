@@ -10,6 +10,7 @@
 #include "kernels.h"
 #include "linear.h"
 #include "mxfp8_partial.h"
+#include "status.h"
 
 namespace {
 

@@ -26,6 +26,7 @@
 
 #include "common.cuh"
 #include "linear.h"
+#include "status.h"
 #include "tensor_core.cuh"
 
 namespace mxfp8 {
