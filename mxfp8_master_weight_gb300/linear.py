@@ -29,6 +29,13 @@ def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
+def _check_input(x: torch.Tensor, name: str, tokens: int, width: int) -> None:
+    """An input is tokens x width, or as many values in one dimension: the C entry points take larger buffers, of
+    which they read the first rows and columns, and a larger input would be cut without a word."""
+    if tuple(x.shape) not in ((tokens, width), (tokens * width,)):
+        raise api.MXFP8Error(2, f"{name}: shape {list(x.shape)}, expected [{tokens}, {width}]")
+
+
 class Checkpoint:
     """Buffers of an activation's 8-bit checkpoint, tokens x width, in one or both directions."""
 
@@ -41,6 +48,7 @@ class Checkpoint:
         self.scale_c = u8(api.mxfp8_swizzled_scales_size(width, _blocks(tokens))) if colwise else None
 
     def save(self, x: torch.Tensor) -> None:
+        _check_input(x, "input", self.tokens, self.width)
         api.mxfp8_checkpoint_save(x, self.codes_r, self.scale_r, self.codes_c, self.scale_c, self.tokens, self.width)
 
     def restore(self, out: torch.Tensor, colwise: bool = False) -> None:
@@ -88,6 +96,9 @@ class NormLinear:
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         """y of this step's input (tokens x ins); valid until the next call."""
         t, i, o = self.tokens, self.ins, self.outs
+        _check_input(x, "x", t, i)
+        if x.dtype != self.h.dtype:
+            raise api.MXFP8Error(3, f"x: dtype {x.dtype}, the layer's is {self.h.dtype}")
         self.x8.save(x)
         api.mxfp8_layer_norm_forward(x, self.norm_weight, self.norm_bias, self.h, self.mean, self.rstd, t, i, self.eps)
         self.h8.save(self.h)
@@ -98,6 +109,7 @@ class NormLinear:
     def backward(self, dy: torch.Tensor) -> torch.Tensor:
         """dx of this step's output gradient; adds to grad_weight, sets the norm's gradients."""
         t, i, o = self.tokens, self.ins, self.outs
+        _check_input(dy, "dy", t, o)
         self.dy8.save(dy)
         api.mxfp8_gemm(self.dy8.codes_r, self.dy8.scale_r, self.cast.outputs[0][1], self.w_scale_c, None, self.dh, t, i, o,
                        b_colwise=True, b_block=32)
