@@ -11,7 +11,9 @@ checkpoint (layer norm's gradients read it) and the normalised input as a column
     forward    save(x), layer norm, save(h), y = h W^T
     backward   save(dy), dh = dy W, dW += dy^T h, layer norm's gradients
 
-All buffers are allocated once; every call goes to the current stream.
+All buffers are allocated once; every call goes to the current stream.  A kernel that gives up a wait
+leaves invalid output and its call has already returned: ``check`` raises for it, at the end of a step or
+wherever the program waits for the GPU anyway.
 """
 from __future__ import annotations
 
@@ -63,7 +65,7 @@ class NormLinear:
     def __init__(self, tokens: int, ins: int, outs: int, device="cuda", dtype=torch.bfloat16, bounds=None,
                  eps: float = 1e-5):
         self.tokens, self.ins, self.outs, self.eps = tokens, ins, outs, eps
-        dev = torch.device(device)
+        self.device = dev = torch.device(device)
         self.cast = driver.ShardedCast([driver.WeightSpec(outs, ins, True)], bounds or [0, outs * ins], dev)
         (rr, rc), (cr, cc) = api.block_shapes(outs, ins)
         self._grids = (rr, rc, cr, cc)
@@ -92,6 +94,11 @@ class NormLinear:
         sr, sc = self.cast.scales[0]
         api.mxfp8_swizzle_scales(sr, self.w_scale_r, rr, rc)
         api.mxfp8_swizzle_scales(sc, self.w_scale_c, cr, cc, transpose=True)
+
+    def check(self) -> None:
+        """Waits for the current stream; raises when a kernel of a layer on this device gave up a wait, so that
+        what it wrote is invalid."""
+        api.mxfp8_device_status(self.device)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         """y of this step's input (tokens x ins); valid until the next call."""

@@ -116,6 +116,7 @@ def case_linear(dev, scale):
         layer.refresh([master])
         layer.forward(x)
         layer.backward(dy)
+    run.check = layer.check
     return run
 
 
@@ -141,6 +142,7 @@ def main(argv=None):
         run()
     b.record()
     torch.cuda.synchronize()
+    getattr(run, "check", lambda: None)()  # before the figure: it may be one of invalid steps
     print(f"{args.case}: {args.calls} calls, {a.elapsed_time(b) * 1e3 / max(1, args.calls):.2f} us per call")
 
 
