@@ -88,15 +88,22 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int dtype_index(int32_t dtype) { return dtype == MXFP8_DTYPE_F32 ? 0 : 1; }
 
-// Byte range [lo, hi) of a matrix.
+// Where a matrix lies: bytes [lo, hi), in rows of `width` bytes `pitch` bytes apart.
 struct Span {
-  uintptr_t lo, hi;
+  uintptr_t lo, hi, width, pitch;
 };
 Span span_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t eb) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, lo + uintptr_t(((rows - 1) * ld + cols) * eb)};
+  return {lo, lo + uintptr_t(((rows - 1) * ld + cols) * eb), uintptr_t(cols * eb), uintptr_t(ld * eb)};
 }
-bool overlap(const Span& x, const Span& y) { return x.lo < y.hi && y.lo < x.hi; }
+// Column ranges of one buffer interleave without sharing a byte: with one pitch, a row of y starts `off` bytes
+// after a row of x, behind its end and ending before the next one.
+bool overlap(const Span& x, const Span& y) {
+  if (x.lo >= y.hi || y.lo >= x.hi) return false;
+  if (x.pitch != y.pitch) return true;
+  const uintptr_t p = x.pitch, off = y.lo >= x.lo ? (y.lo - x.lo) % p : (p - (x.lo - y.lo) % p) % p;
+  return off < x.width || off + y.width > p;
+}
 
 }  // namespace
 
@@ -204,7 +211,7 @@ int mxfp8_gemm(const mxfp8_tensor* a, const mxfp8_tensor* a_scale, const mxfp8_t
     if (int rc = want_dtype(addend, "addend", MXFP8_DTYPE_F32)) return rc;
     p.addend = static_cast<const float*>(addend->data);
     p.vec_out = p.vec_out && aligned(p.addend, p.ld_c, 4, 16);
-    const bool same = p.out_f32 && addend->data == out->data && p.ld_c == p.ld_o;
+    const bool same = p.out_f32 && addend->data == out->data && (p.ld_c == p.ld_o || m == 1);
     if (!same && overlap(span_of(p.addend, m, n, p.ld_c, 4), span_of(p.out, m, n, p.ld_o, elem_bytes(out->dtype))))
       return fail(MXFP8_ERR_INVALID, "addend overlaps out without being the same matrix");
   }
