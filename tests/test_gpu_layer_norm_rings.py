@@ -81,3 +81,54 @@ def test_forward_of_constant_rows(cols, dtype):
     assert torch.equal(y.float(), b.expand(ROWS, -1))
     assert torch.allclose(rstd, torch.full_like(rstd, EPS ** -0.5), rtol=1e-6, atol=0.0)
     api.mxfp8_device_status()
+
+
+@pytest.mark.parametrize("dtype,wdtype", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("cols", COLS)
+def test_forward_without_bias_and_of_both_weight_types(cols, dtype, wdtype):
+    x = torch.randn(ROWS, cols, generator=torch.Generator(device="cuda").manual_seed(cols), device="cuda").to(DT[dtype])
+    w = (1 + 0.2 * torch.randn(cols, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")).to(DT[wdtype])
+    b = torch.randn(cols, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").to(DT[wdtype])
+    x64, w64 = ref.as64(x), ref.as64(w)
+    check_forward(x64, w64, None, *forward(x, w, None))
+    check_forward(x64, w64, ref.as64(b), *forward(x, w, b))
+    api.mxfp8_device_status()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", COLS)
+def test_nan_and_infinity_stay_where_they_belong(cols, dtype):
+    """Forward: in their rows.  Backward: in their rows of dx and their columns of the sums over rows; from a
+    checkpoint in the whole block that the NaN scale makes."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.randn(ROWS, cols, generator=g, device="cuda").to(DT[dtype])
+    dy = torch.randn(ROWS, cols, generator=g, device="cuda").to(x.dtype)
+    w = 1 + 0.2 * torch.randn(cols, generator=g, device="cuda")
+    mean, rstd = statistics(ref.as64(x))
+    nan, inf = float("nan"), float("inf")
+    bad_x = {(3, 0): nan, (611, cols - 1): inf, (1899, cols // 2): -inf}
+    bad_dy = {(4, 5): nan, (1500, cols - 2): inf}
+    for (r, c), v in bad_x.items():
+        x[r, c] = v
+    y, m, s = forward(x, w, None)
+    rows = torch.zeros(ROWS, dtype=torch.bool, device="cuda")
+    rows[[r for r, _ in bad_x]] = True
+    assert torch.equal(torch.isnan(y).all(1), rows) and torch.equal((~torch.isfinite(y)).any(1), rows)
+    assert m[3].isnan() and m[611] == inf and m[1899] == -inf and torch.equal(~torch.isfinite(s), rows)
+    for (r, c), v in bad_dy.items():
+        dy[r, c] = v
+    rows[[r for r, _ in bad_dy]] = True
+    q = torch.empty(ROWS, cols, dtype=torch.uint8, device="cuda")
+    sc = torch.empty(api.mxfp8_swizzled_scales_size(ROWS, -(-cols // 128)), dtype=torch.uint8, device="cuda")
+    api.mxfp8_checkpoint_save(x, q, sc, None, None, ROWS, cols)
+    for saved, scale in ((x, None), (q, sc)):
+        dx, dw, db = backward(dy, saved, scale, w, mean, rstd)
+        assert torch.equal((~torch.isfinite(dx)).any(1), rows)
+        in_dw = torch.zeros(cols, dtype=torch.bool, device="cuda")
+        in_db = in_dw.clone()
+        for _, c in bad_dy:
+            in_dw[c] = in_db[c] = True
+        for _, c in bad_x:
+            in_dw[c if scale is None else slice(c // 128 * 128, c // 128 * 128 + 128)] = True
+        assert torch.equal(~torch.isfinite(dw), in_dw) and torch.equal(~torch.isfinite(db), in_db)
+    api.mxfp8_device_status()
