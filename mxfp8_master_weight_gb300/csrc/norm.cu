@@ -722,10 +722,13 @@ __global__ void __launch_bounds__(TH, BLOCKS)
     }
     int s = 0, half = 0;
     uint32_t phase = 0;
+    bool good = true;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-      // a thread whose wait was given up still goes through the row's barriers, so that no other
-      // waits for it; the row is not written
-      const bool good = tc::mbar_wait(tc::smem_addr(&h->full[s]), phase, gave_up);
+      // A thread whose wait was given up still goes through the barriers of this row and the ones after, so
+      // that no other waits for it, but writes no more rows or statistics and fetches nothing: its slot's copy
+      // may yet land, and a barrier takes no second arrival for the same copy.  (What the rest of the block
+      // writes, and the sums over rows, are then invalid: the call is reported.)
+      good &= tc::mbar_wait(tc::smem_addr(&h->full[s]), phase, gave_up);
       const char* src = slots + s * ring.slot_bytes + ring_offset<kVec>(p.x, row * p.ld_x * T::kBytes);
       Eight x[NV];
       float sum[1] = {0.0f};
@@ -736,7 +739,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
         for (int k = 0; k < 8; ++k) sum[0] += x[i].v[k];
       }
       ring_sum<TH>(sum, h, half);
-      if (t == 0) feed.next<kVec>(ring, s);  // every thread has the row in registers
+      if (t == 0 && good) feed.next<kVec>(ring, s);  // every thread has the row in registers
       // A product with 1 / cols alone rounds twice: the mean of a constant row would be off by a last place and
       // its deviations not zero.  Adding what is left of the sum, over cols, makes an exact quotient exact
       // (dividing: 16384 x 6144 BF16 64.8 us for 62.3; neither 62.1).  Of an infinite sum NaN is left: fminf makes it a number,
@@ -754,7 +757,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
       }
       ring_sum<TH>(sum, h, half);
       const float rstd = __frsqrt_rn(sum[0] * inv + p.eps);
-      if (t == 0) {
+      if (t == 0 && good) {
         p.mean[row] = mean;
         p.rstd[row] = rstd;
       }
@@ -851,6 +854,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
     }
     int s = 0, half = 0;
     uint32_t phase = 0;
+    bool good = true;  // as in the forward pass
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
       Stats now = next;
       if constexpr (!kVec) fetch(row + gridDim.x, next);
@@ -862,7 +866,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
         fetch(row + 2 * int64_t(gridDim.x), st);
         later = st.scale;
       }
-      const bool good = tc::mbar_wait(tc::smem_addr(&h->full[s]), phase, gave_up);  // as in the forward pass
+      good &= tc::mbar_wait(tc::smem_addr(&h->full[s]), phase, gave_up);
       const char* slot = slots + s * ring.slot_bytes;
       const char* dy_row = slot + ring_offset<kVec>(p.dy, row * p.ld_dy * T::kBytes);
       const char* x_row = slot + ring.second + ring_offset<kVec>(p.x, row * p.ld_x * kXBytes);
@@ -928,7 +932,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
       s1.get(lo, hi);
       sum[1] = lo + hi;
       ring_sum<TH>(sum, h, half);
-      if (row != blockIdx.x) {  // every thread is past the row before
+      if (row != blockIdx.x && good) {  // every thread is past the row before
         const uint32_t before = s == 0 ? ring.slots - 1 : s - 1;
         if constexpr (kVec) {
           if (t < 32) feed.next(ring, before, side);
