@@ -19,7 +19,7 @@
 // sums do not depend on the run.
 //
 // Measured at 16384 x 6144: forward BF16 62 us (6.5 TB/s, bound by HBM), backward BF16 99 us (6.1 TB/s), from
-// an 8-bit checkpoint 98 us for 504 MB: there decoding and two passes of arithmetic over the row take 56 %
+// an 8-bit checkpoint 95 us for 504 MB: there decoding and two passes of arithmetic over the row take 56 %
 // of the issue slots at 16 warps per SM.  1 x 4096 forward: 4.6 us, the time of a call.
 #include <cfloat>
 #include <type_traits>
@@ -781,18 +781,15 @@ __global__ void __launch_bounds__(TH, BLOCKS)
   }
 }
 
-// xh = (x - mean) rstd of two values.  F32 input takes the difference first.  BF16 values and codes take one
-// fused operation x (f rstd) - m (f: the code's scale, a power of two; m: mean rstd rounded); what m's
-// rounding left out, the same for a whole row and up to |mean| rstd 2^-24, is added where xh enters the
-// gradient of the weight and the row's sum, and for dx to the row's constant.  Without it a constant row
-// of 1000 had xh = 2.7e-3 for 0.  (The difference first in both passes: 16384 x 4096 BF16 70.5 for 69.4 us,
-// from codes 75.4 for 73.4.)
-template <bool kFused>
-__device__ __forceinline__ Two normalised(Two x, Two mul, Two shift) {
-  if constexpr (kFused) return fma2(x, mul, shift);
-  else return (x + shift) * mul;
-}
-
+// The two passes over a row take xh = (x - mean) rstd in two forms, neither of which costs an instruction more
+// than a product would:
+//   sums   d = x - mean, one rounding of a difference that may cancel.  With t = dy d the sums are t w (times
+//          rstd once per row) and t rstd, both fused.
+//   dx     BF16 and codes: x rstd - m with m = mean rstd rounded.  What m's rounding left out, the same for the whole
+//          row and up to |mean| rstd 2^-24, goes into the row's constant.  F32: d rstd.
+// (x rstd - m alone in both had xh = 2.7e-3 for 0 in a constant row of 1000.  d rstd in both: 16384 x 6144 BF16
+// from codes 97.9 us for 94.7, 16384 x 4096 BF16 70.5 for 68.5.)  Codes come with their scale f, a power of two:
+// x stands for x f.
 template <class T, bool kCodes, bool kVec, int TH, int NV, int BLOCKS>
 __global__ void __launch_bounds__(TH, BLOCKS)
     k_norm_backward_ring(const __grid_constant__ NormBackwardParams p, int wbf16, Ring ring, unsigned* given_up) {
@@ -870,7 +867,7 @@ __global__ void __launch_bounds__(TH, BLOCKS)
       const char* slot = slots + s * ring.slot_bytes;
       const char* dy_row = slot + ring_offset<kVec>(p.dy, row * p.ld_dy * T::kBytes);
       const char* x_row = slot + ring.second + ring_offset<kVec>(p.x, row * p.ld_x * kXBytes);
-      float one[NV];  // what a piece's values are multiplied by
+      float scale[NV];  // of a piece's codes
       if constexpr (kVec) {
         const float2 st = *reinterpret_cast<const float2*>(slot + ring.side);
         now.mean = st.x;
@@ -878,14 +875,14 @@ __global__ void __launch_bounds__(TH, BLOCKS)
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        one[i] = now.rstd;
-        if constexpr (kCodes && kVec) one[i] *= scale_value(reinterpret_cast<const uint8_t*>(slot + ring.side + 16)[(t + i * TH) / (kCkptBlock / 8)]);
+        scale[i] = 1.0f;
+        if constexpr (kCodes && kVec) scale[i] = scale_value(reinterpret_cast<const uint8_t*>(slot + ring.side + 16)[(t + i * TH) / (kCkptBlock / 8)]);
       }
       const float m = __fmul_rn(now.mean, now.rstd);
-      const Two shift(kFused ? -m : -now.mean);
       const float rest = kFused ? -__fmaf_rn(now.mean, now.rstd, -m) : 0.0f;
-      // the piece's dy and xh, as pairs
-      auto piece = [&](int i, Two (&dy)[4], Two (&xh)[4]) {
+      const Two r2(now.rstd), minus_mean(-now.mean), shift(-m);
+      // the piece's dy and x, as pairs, and the scales of x
+      auto piece = [&](int i, Two (&dy)[4], Two (&xs)[4], float (&f)[2]) {
         const Eight e = ring_piece<T, kVec, TH>(dy_row, i, cols);
         Eight x;
         if constexpr (kCodes && kVec) {
@@ -906,23 +903,25 @@ __global__ void __launch_bounds__(TH, BLOCKS)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           dy[k] = Two(e.v[2 * k], e.v[2 * k + 1]);
-          const Two mul(kCodes && !kVec ? scales[ring_col<false, TH>(i, 0) / kCkptBlock + (k >> 1)] * now.rstd : one[i]);
-          xh[k] = normalised<kFused>(Two(x.v[2 * k], x.v[2 * k + 1]), mul, shift);
+          xs[k] = Two(x.v[2 * k], x.v[2 * k + 1]);
         }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) f[b] = kCodes && !kVec ? scales[ring_col<false, TH>(i, 0) / kCkptBlock + b] : scale[i];
       };
       Two s0(0.0f), s1(0.0f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (ring_col<kVec, TH>(i, 0) >= cols) continue;
-        Two dy[4], xh[4];  // past the row dy is 0, and adds nothing
-        piece(i, dy, xh);
+        Two dy[4], x[4];  // past the row dy is 0, and adds nothing
+        float f[2];
+        piece(i, dy, x, f);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const Two g = dy[k] * w[i][k];
-          if constexpr (kFused) xh[k] = xh[k] + Two(rest);
-          s0 = s0 + g;
-          s1 = fma2(g, xh[k], s1);
-          dw[i][k] = fma2(dy[k], xh[k], dw[i][k]);
+          const Two d = kCodes ? fma2(x[k], Two(f[k >> 1]), minus_mean) : x[k] + minus_mean;
+          const Two t = dy[k] * d;
+          s0 = fma2(dy[k], w[i][k], s0);
+          s1 = fma2(t, w[i][k], s1);
+          dw[i][k] = fma2(t, r2, dw[i][k]);
           db[i][k] = db[i][k] + dy[k];
         }
       }
@@ -941,16 +940,20 @@ __global__ void __launch_bounds__(TH, BLOCKS)
         }
       }
       // dx = rstd g - rstd mean(g) - xh rstd mean(g xh)
-      const float by_xh = -now.rstd * (sum[1] * inv);
-      const Two r2(now.rstd), c0(__fmaf_rn(rest, by_xh, -now.rstd * (sum[0] * inv))), c1(by_xh);
+      const float by_xh = -now.rstd * (sum[1] * now.rstd * inv);
+      const Two c0(__fmaf_rn(rest, by_xh, -now.rstd * (sum[0] * inv))), c1(by_xh);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (ring_col<kVec, TH>(i, 0) >= cols) continue;
-        Two dy[4], xh[4];  // past the row dy is 0, and adds nothing
-        piece(i, dy, xh);
+        Two dy[4], x[4];
+        float f[2];
+        piece(i, dy, x, f);
         Eight dx;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) fma2(xh[k], c1, fma2(dy[k] * w[i][k], r2, c0)).get(dx.v[2 * k], dx.v[2 * k + 1]);
+        for (int k = 0; k < 4; ++k) {
+          const Two xh = kFused ? fma2(x[k], Two(f[k >> 1] * now.rstd), shift) : (x[k] + minus_mean) * r2;
+          fma2(xh, c1, fma2(dy[k] * w[i][k], r2, c0)).get(dx.v[2 * k], dx.v[2 * k + 1]);
+        }
         if (good) ring_store<T, kVec, TH>(p.dx, row * p.ld_dx, i, cols, dx);
       }
       if (++s == ring.slots) {
