@@ -504,7 +504,9 @@ MXFP8_API int mxfp8_checkpoint_restore(const mxfp8_tensor* codes, const mxfp8_te
  * Matrix product of two block-scaled 8-bit operands,
  *   out[i][j] = sum_p A(i, p) * B(j, p) (+ addend[i][j]),   i < m, j < n, p < k,
  * A(i, p) = decode(code) * 2^(s - 127), s the scale of the block of p; likewise B.  Products
- * are exact and summed in F32; the addend joins in F32 and the result is rounded once.
+ * are exact and summed in F32 by the matrix instruction, whose additions are coarser than one rounding to
+ * nearest each (k = 8192: a relative error of 5e-7 over the matrix, 1.2e-7 with F32 products of the decoded
+ * values); the addend joins in F32 and the result is rounded once.
  *
  * a, b               [in] U8 E4M3 codes.  Rowwise (colwise flag 0): the matrix m x k (n x k), the
  *                         contraction along its rows.  Columnwise (flag 1): the matrix k x m
@@ -523,7 +525,8 @@ MXFP8_API int mxfp8_checkpoint_restore(const mxfp8_tensor* codes, const mxfp8_te
  * b = x columnwise.  k may be 0 (operands and scales may then be empty): out = addend or 0.
  * Operands whose base and row stride are multiples of 16 bytes are fetched as they lie; others
  * are realigned on the way, which takes longer.
- * Results do not depend on the run: no atomics, one fixed order of sums per shape and alignment.
+ * Results do not depend on the run: no atomics, one fixed order of sums per shape, alignment and number of
+ * the GPU's SMs.
  * Errors: 1 bad sizes (m, n, k <= 2^31 - 1024), flags or blocks, unaligned scales, or an addend
  * that overlaps out without being the same matrix; 2 a buffer too small; 3 dtype; 4 missing.
  */

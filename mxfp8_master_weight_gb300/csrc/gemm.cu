@@ -28,13 +28,13 @@ cudaError_t launch_gemm(const GemmParams& p, const DeviceInfo& dev, cudaStream_t
   const cudaError_t e = given_up_address(dev.device, &given_up);
   if (e != cudaSuccess) return e;
   // Split over k: outputs of at most 64 rows or columns (a tile of the pair kernel would stay mostly
-  // empty: 64 x 4096 x 4096 6.9 us split, 10.3 us by pairs), and tiles so few that four CTAs can share
+  // empty: 64 x 4096 x 4096 6.8 us split, 9.9 us by pairs), and tiles so few that four CTAs can share
   // each with an SM to themselves, with a k that pays for joining the sums, the longer the more tiles
-  // there are (split / pairs: 160 x 96 x 2048 6.2 / 7.4 us, 512 x 512 x 2048 7.4 / 7.0, 512 x 512 x 4096 8.2 /
-  // 10.1, 512 x 1024 x 8192 10.9 / 16.1, 128 x 4096 x 4096 8.9 / 10.5, 256 x 4096 x 8192 18.5 / 17.4).  Operands
-  // that are realigned take longer per stage, so the split pays from fewer stages and to more tiles
-  // (301 x 303 x 1005 11.0 / 17.7, 1000 x 1111 x 999 15.2 / 21.6, 301 x 303 x 305 16.2 / 11.5, 2001 x 1111 x
-  // 1999 28.1 / 27.8).
+  // there are (split / pairs: 160 x 96 x 2048 6.2 / 7.2 us, 512 x 512 x 2048 7.4 / 7.0, 512 x 512 x 4096 8.2 /
+  // 9.7, 512 x 1024 x 8192 10.7 / 15.4, 128 x 4096 x 4096 8.8 / 9.9, 256 x 4096 x 8192 17.7 / 16.3).  Operands
+  // that are realigned take longer per stage, so the split pays from fewer stages and to more tiles (both
+  // operands off 16 bytes: 301 x 303 x 1005 10.8 / 16.8, 1000 x 1111 x 999 15.0 / 18.2, 301 x 303 x 305 15.9 / 10.4;
+  // beyond the rule's tiles too with three weights in turn: 2001 x 1111 x 1999 27.7 / 33.9).
   const int64_t tiles = ((p.m + 127) / 128) * ((p.n + 127) / 128), stages = (p.k + kBlockK - 1) / kBlockK;
   const bool few = 4 * tiles <= dev.sms && stages >= 15 + tiles / 2;
   const bool realigned = !(p.a.aligned && p.b.aligned) && 2 * tiles <= dev.sms && stages >= 8;

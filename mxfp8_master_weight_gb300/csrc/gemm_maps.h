@@ -20,7 +20,7 @@ cudaError_t residue_maps(const GemmOperand& o, int64_t k, CUtensorMap* maps, con
 // 128-row block).
 cudaError_t scale_map(const GemmOperand& o, int64_t k, int row_tiles, CUtensorMap* map, const char** what);
 
-// The kernels for aligned operands.
+// The kernels, for operands of any alignment.
 cudaError_t launch_gemm_pair(const GemmParams& g, unsigned* given_up, const DeviceInfo& dev, cudaStream_t stream,
                              const char** what);
 cudaError_t launch_gemm_split(const GemmParams& g, unsigned* given_up, const DeviceInfo& dev, cudaStream_t stream,

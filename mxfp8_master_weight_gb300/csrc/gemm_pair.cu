@@ -19,10 +19,13 @@
 // scales 480..511.  The writers drain the shared columns of a tile first; then the next
 // tile's instructions start in the other buffer while they write the rest.
 //
-// What bounds it: the matrix instructions and what feeds them.  8192^3 takes 315 us (3.49 PFLOP/s, 0.92 of
-// twice the measured BF16 rate; with both operands across k and F32 output 332 us), 4096^3 44 us (3.13),
-// 2048 x 8192 x 8192 with both across k and F32 output 97 us (2.82): the first and last stages of a
-// launch, about 4 us, and the share of the last round that stays empty are what the smaller ones lose.
+// What bounds it: the matrix instructions and what feeds them, and over more than some milliseconds the board's
+// power, which sets the clock.  8192^3 takes 302 us in a burst (3.64 PFLOP/s, 0.96 of twice the measured BF16
+// rate) and 337 in a loop of half a second (1470 MHz).  4096^3 takes 43 us in a burst on unchanged operands, 46.6
+// in a loop (2070 MHz), 48.8 with three sets of operands in turn (1880 MHz), 50-51 with new inputs in every
+// pass; the first and last stages of a launch, about 4 us, and the share of the last round that stays empty are
+// what it loses of 36.  2048 x 8192 x 8192 with both operands across k and F32 output: 94 us in a loop, 100 with
+// the addend (1665 MHz both), 102-105 with the addend and new inputs.
 #include <type_traits>
 
 #include <cuda.h>

@@ -9,13 +9,15 @@
 // 16-byte units in turns, so that with 160 bytes per raw row neither reads nor writes ask a bank twice
 // (16-byte reads and writes of whole units: 248 instead of 228 us in the case below).
 // Box corners are multiples of 64 rows and 64 bytes, so a lane's rows keep their place in a 16-byte
-// unit over the whole matrix.  (The first unit may start up to 15 bytes before the matrix: inside
+// unit over the whole matrix.  (A box cannot start at a row's first byte instead: its innermost coordinate
+// times the element size has to be a multiple of 16 bytes.)  (The first unit may start up to 15 bytes before the matrix: inside
 // its allocation, which starts at a multiple of 16.)
 //
 // What bounds it: the raw boxes' way through shared memory, about as much again as the stages' own
 // (1.0 us per 128 values of k of a 256 x 256 tile, 0.3 aligned).  Tried first: a bulk copy per row (128
 // per box, about 30 cycles each) and cp.async of the units (an SM keeps too few of them under way; in
-// the writing warps, the proxy fence waits for them): 8192 x 5001 x 3001 490 and 264 us, with maps 232 us.
+// the writing warps, the proxy fence waits for them): 8192 x 5001 x 3001 with one operand off 16 bytes 490 and 264 us,
+// with maps 232-235 us; with both off 16 bytes 320.
 #pragma once
 
 #include <type_traits>

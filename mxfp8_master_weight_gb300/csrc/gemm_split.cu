@@ -7,12 +7,14 @@
 // the tokens its NT = 16 .. 128 columns, and 1 to 8 CTAs share a tile, each with its part
 // of k.  Their partial sums stay in shared memory, laid out as lines of the output; after a cluster
 // barrier each CTA adds its share of the lines over the cluster in rank order and writes it.  No
-// workspace, no atomics: the result depends on the shape and the alignment alone.
+// workspace, no atomics: the result depends on the shape, the alignment and the number of SMs (which sets the
+// split) alone.
 //
-// Measured, launches that follow one another with three weights in turn: 1 x 4096 x 4096 5.6 us and 64 x
-// 4096 x 4096 6.9 (from L2), 1 x 8192 x 8192 14.4 (from HBM, 4.7 TB/s of weight), 64 x 8192 x 8192 16.7.
-// Streaming the weight takes 10.3 us of the last two; the rest is the start (barriers, tensor memory, first bytes from HBM)
-// and the join.  Reading the sums four at a time, with every rank's reads under way at once, took 1.6 us
+// Measured, launches of a graph that follow one another with three weights in turn: 1 x 4096 x 4096 5.6 us and 64 x
+// 4096 x 4096 6.8 (from L2), 1 x 8192 x 8192 14.0 (from HBM, 4.8 TB/s of weight), 64 x 8192 x 8192 16.0; called
+// one by one with new inputs, the first 6.2 and the last 17.2-17.5.  Streaming the weight takes 10.3 us of the last two;
+// about 4 us are a launch that starts, allocates tensor memory and joins; the others are the stream's: 256
+// CTAs on 152 SMs leave 48 SMs with half of the weight that the others have.  Reading the sums four at a time, with every rank's reads under way at once, took 1.6 us
 // from the last: a rank's read costs about 0.4 us when the ranks take turns.
 #include <type_traits>
 

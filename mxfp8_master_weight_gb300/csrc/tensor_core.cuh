@@ -32,8 +32,8 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar, uint32_t cta) 
       : "memory");
 }
 // The same for tensor memory alone, which the tcgen05 fences on both sides order: as a release it
-// would wait for the thread's own stores to global memory first. In the pair kernel 4096x4096x4096 takes
-// 44 us so and 46 us with a release, 8192x8192x8192 315.5 and 318.
+// would wait for the thread's own stores to global memory first. In the pair kernel, in bursts on unchanged
+// operands, 4096x4096x4096 took 44 us so and 46 us with a release, 8192x8192x8192 315.5 and 318.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar, uint32_t cta) {
   asm volatile(
       "{ .reg .b32 r; mapa.shared::cluster.u32 r, %0, %1;\n"

@@ -6,7 +6,9 @@ The FP32 master weight lives in shards and reaches its MXFP8 copies (rowwise and
 through ``driver.ShardedCast``; ``refresh`` lays their scales out for the products.  What the
 backward pass needs of the activations is kept in 8 bits: the layer's input as a rowwise
 checkpoint (layer norm's gradients read it) and the normalised input as a columnwise one
-(the weight's gradient contracts over tokens).  A step's calls:
+(the weight's gradient contracts over tokens).  The normalised input's rowwise copy, which
+the forward product reads, is a buffer of the layer too: 3 bytes per value of the input's
+shape in all, and the scales.  A step's calls:
 
     forward    save(x), layer norm, save(h), y = h W^T
     backward   save(dy), dh = dy W, dW += dy^T h, layer norm's gradients
@@ -75,7 +77,8 @@ class NormLinear:
         self.norm_weight, self.norm_bias = torch.ones(ins, device=dev), torch.zeros(ins, device=dev)
         self.grad_weight = torch.zeros(outs, ins, device=dev)
         self.grad_norm_weight, self.grad_norm_bias = torch.empty(ins, device=dev), torch.empty(ins, device=dev)
-        # kept from forward to backward: 1 byte per value of x and of h, and two floats per token
+        # kept from forward to backward: a byte per value of x and the columnwise byte per value of h, and two
+        # floats per token; h8's rowwise copy serves the forward product only
         self.x8 = Checkpoint(tokens, ins, dev, colwise=False)
         self.h8 = Checkpoint(tokens, ins, dev)
         self.mean, self.rstd = torch.empty(tokens, device=dev), torch.empty(tokens, device=dev)
