@@ -587,6 +587,131 @@ MXFP8_API int mxfp8_layer_norm_backward(const mxfp8_tensor* grad_output, const m
 /* Bytes of workspace of mxfp8_layer_norm_backward on any device (-1 for bad sizes). */
 MXFP8_API int64_t mxfp8_layer_norm_workspace_size(int64_t rows, int64_t cols);
 
+/*
+ * RMS norm of each row of a residual stream: s = input + residual, rstd = 1 / sqrt(mean(s^2) + eps) over the row's cols
+ * values, output = s * rstd * weight, in F32; every output is rounded once, from the unrounded s.
+ *
+ * input    [in]  F32 or BF16 matrix rows x cols;  residual [in] OPTIONAL, the same dtype: absent, s = input.
+ * weight   [in]  F32 or BF16 vector of cols.
+ * sum      [out] OPTIONAL matrix of input's dtype: s, the residual stream behind this layer.
+ * output   [out] OPTIONAL matrix of input's dtype.  sum and output may each be the input or the residual (the same
+ *                matrix, row stride included), but not overlap one another.
+ * codes    [out] OPTIONAL U8 matrix rows x cols: E4M3 codes of the output in blocks of 1x128, as
+ *                mxfp8_checkpoint_save writes them rowwise, from the unrounded output; the operand of mxfp8_gemm that a
+ *                layer with 8-bit weights takes.  output or codes is required.
+ * scale    [out] required iff codes: their scales in the GEMM layout, padding entries written as zeros.
+ * amax     [in,out] OPTIONAL F32, at least 1 element: element 0 is max-accumulated with the largest |output| as
+ *                rounded to input's dtype (whether it is stored or not), for nvfp4_quantize; it must hold +0 or a
+ *                previous maximum.  A NaN gives the canonical quiet NaN.
+ * rstd     [out] OPTIONAL F32 vector of rows, for the backward pass.
+ * Errors: 1 bad sizes, eps < 0 or NaN, overlapping matrices or unaligned scales; 2 too small; 3 dtype; 4 missing.
+ */
+MXFP8_API int mxfp8_rms_norm_forward(const mxfp8_tensor* input, const mxfp8_tensor* residual,
+                           const mxfp8_tensor* weight, mxfp8_tensor* sum, mxfp8_tensor* output, mxfp8_tensor* codes,
+                           mxfp8_tensor* scale, mxfp8_tensor* amax, mxfp8_tensor* rstd, int64_t rows, int64_t cols,
+                           float eps, void* stream);
+
+/*
+ * Gradients of RMS norm.  With xh = input * rstd and g = grad_output * weight:
+ *   grad_input  = rstd * (g - xh * mean_cols(g * xh)) + grad_sum
+ *   grad_weight = sum_rows grad_output * xh.
+ *
+ * grad_output [in]  F32 or BF16 matrix rows x cols.
+ * grad_sum    [in]  OPTIONAL, the same dtype: the gradient that reaches s along the residual stream.
+ * input       [in]  the same dtype: the forward pass's s (its sum, or its input where it had no residual).
+ * weight      [in]  F32 or BF16 vector;  rstd [in] F32 vector, as the forward pass left it.
+ * grad_input  [out] the same dtype: the gradient of s, which is that of the forward pass's input and of its residual;
+ *                   may be grad_output, grad_sum or input itself (the same matrix, row stride included).
+ * grad_weight [out] F32 vector of cols.
+ * workspace   [out] at least mxfp8_rms_norm_workspace_size(rows, cols) bytes (U8), 16-byte aligned; its contents
+ *                   before the call do not matter and after it mean nothing.  Calls that overlap on the GPU need
+ *                   workspaces of their own.
+ * The sums have one fixed order for a shape and the alignment of the arguments: results do not depend on the run.
+ * rows == 0: the gradient of the weight is set to zero.
+ * Errors: 1 bad sizes, overlapping matrices or unaligned workspace; 2 too small; 3 dtype; 4 missing.
+ */
+MXFP8_API int mxfp8_rms_norm_backward(const mxfp8_tensor* grad_output, const mxfp8_tensor* grad_sum,
+                            const mxfp8_tensor* input, const mxfp8_tensor* weight, const mxfp8_tensor* rstd,
+                            mxfp8_tensor* grad_input, mxfp8_tensor* grad_weight, mxfp8_tensor* workspace, int64_t rows,
+                            int64_t cols, void* stream);
+
+/* Bytes of workspace of mxfp8_rms_norm_backward on any device (-1 for bad sizes). */
+MXFP8_API int64_t mxfp8_rms_norm_workspace_size(int64_t rows, int64_t cols);
+
+/*
+ * NVFP4 operands.  The product of two 4-bit matrices, the quantisation of an activation (or gradient) to such an
+ * operand, and weights of nvfp4_partial_cast laid out as one.
+ *
+ * An operand of logical size r x c has the contraction along its rows:
+ *   codes  a U8 matrix r x ceil(c/2): E2M1 codes two to a byte, the even column in the low half; the upper half of a
+ *          row's last byte is zero for odd c.  For a product its base and row stride are multiples of 16 bytes.
+ *   scale  one E4M3 byte per 16 values of a row, grid [r][ceil(c/16)] in the GEMM layout, padding entries zero.
+ *   amax   one F32 word: G, the largest magnitude of the tensor.
+ * The convention is the one of nvfp4_partial_amax above, S = 2688 / G and so on, without the rounding through BF16:
+ * code = E2M1(fp32(x * fp32(S / decode(s)))), the multiplier at most the largest float.  G may be smaller than the
+ * tensor's largest magnitude (a maximum of earlier steps): what lies above it saturates.  A block that holds a NaN or an
+ * infinity, and every block where G is not finite, has the scale byte 0x7F (NaN).  A code stands for
+ * fp32(decode(q) * decode(s) * fp32(1 / S)).
+ */
+
+/*
+ * amax_tensor[0] = max |input| over an F32 or BF16 matrix rows x cols; with accumulate 1 the larger of that and what it
+ * holds (+0 or a previous maximum).  A NaN gives the canonical quiet NaN.  rows or cols 0: the maximum is 0.
+ * Errors: 1 bad sizes or accumulate; 2 too small; 3 dtype; 4 missing.
+ */
+MXFP8_API int nvfp4_tensor_amax(const mxfp8_tensor* input, mxfp8_tensor* amax_tensor, int64_t rows, int64_t cols,
+                      int32_t accumulate, void* stream);
+
+/*
+ * One or two operands of an activation from one read.
+ * input          [in]  F32 or BF16 matrix rows x cols;  amax_tensor [in] F32: element 0 is G.
+ * codes_rowwise  [out] OPTIONAL U8 matrix rows x ceil(cols/2);  scale_rowwise [out] required iff codes_rowwise.
+ * codes_colwise  [out] OPTIONAL U8 matrix cols x ceil(rows/2): the operand of the transposed activation (unlike an
+ *                      8-bit checkpoint's columnwise copy, because 4-bit operands are read along the contraction
+ *                      only);  scale_colwise [out] required iff codes_colwise, grid [cols][ceil(rows/16)].
+ * Errors: 1 bad sizes or unaligned scales; 2 too small; 3 dtype; 4 missing, or neither operand present.
+ */
+MXFP8_API int nvfp4_quantize(const mxfp8_tensor* input, const mxfp8_tensor* amax_tensor, mxfp8_tensor* codes_rowwise,
+                   mxfp8_tensor* scale_rowwise, mxfp8_tensor* codes_colwise, mxfp8_tensor* scale_colwise,
+                   int64_t rows, int64_t cols, void* stream);
+
+/*
+ * The values that an operand of size rows x cols stands for (a columnwise copy: cols x rows of its activation).
+ * codes, scale, amax_tensor [in] as nvfp4_quantize wrote them;  output [out] F32 or BF16 matrix rows x cols.
+ * Errors as above.
+ */
+MXFP8_API int nvfp4_restore(const mxfp8_tensor* codes, const mxfp8_tensor* scale, const mxfp8_tensor* amax_tensor,
+                  mxfp8_tensor* output, int64_t rows, int64_t cols, void* stream);
+
+/*
+ * Codes of a weight as an operand's: once per refresh of the weight.  (Its scales: mxfp8_swizzle_scales of the
+ * grid, with the same transpose; its amax: the cast's amax_tensor.)
+ * codes     [in]  the rowwise (transpose 0) or columnwise (transpose 1) output of nvfp4_partial_cast, a U8 matrix
+ *                 rows x cols/2; cols is even.
+ * output    [out] U8 matrix rows x cols/2, or with transpose 1 cols x ceil(rows/2).
+ * Where cols is a multiple of 32 the rowwise output is an operand already.
+ * Errors: 1 bad sizes, an odd cols, another transpose, or buffers that overlap; 2 too small; 3 dtype; 4 missing.
+ */
+MXFP8_API int nvfp4_lay_out(const mxfp8_tensor* codes, mxfp8_tensor* output, int64_t rows, int64_t cols,
+                  int32_t transpose, void* stream);
+
+/*
+ * Matrix product of two NVFP4 operands, A of size m x k and B of size n x k,
+ *   out[i][j] = fp32(1 / Sa) * fp32(1 / Sb) * sum_p A(i, p) * B(j, p) (+ addend[i][j]),
+ * A(i, p) = decode(code) * decode(scale); likewise B.  Products are summed in F32 by the matrix instruction; the tensor
+ * scales and the addend join in F32 and the result is rounded once.
+ * a, a_scale, a_amax, b, b_scale, b_amax [in] the operands.  addend, out as for mxfp8_gemm; k may be 0.
+ * With y = x W^T, W [outs][ins]: output y: a = x, b = W rowwise; input gradient dx = dy W: a = dy, b = W columnwise,
+ * transposed by nvfp4_lay_out; weight gradient dW = dy^T x: a = dy columnwise, b = x columnwise.
+ * Results do not depend on the run: no atomics, one fixed order of sums per shape, alignment of the output and number
+ * of the GPU's SMs.
+ * Errors: 1 bad sizes (m, n, k <= 2^31 - 1024), codes or scales that are not aligned, or an addend that overlaps out
+ * without being the same matrix; 2 a buffer too small; 3 dtype; 4 missing.
+ */
+MXFP8_API int nvfp4_gemm(const mxfp8_tensor* a, const mxfp8_tensor* a_scale, const mxfp8_tensor* a_amax,
+               const mxfp8_tensor* b, const mxfp8_tensor* b_scale, const mxfp8_tensor* b_amax,
+               const mxfp8_tensor* addend, mxfp8_tensor* out, int64_t m, int64_t n, int64_t k, void* stream);
+
 /* Message describing the calling thread's most recent non-zero status ("" if none). */
 MXFP8_API const char* mxfp8_last_error(void);
 

@@ -26,7 +26,9 @@ EXPORTED = ("mxfp8_partial_amax", "mxfp8_amax_max_reduce", "mxfp8_update_scales"
             "mxfp8_sharded_update_noalloc", "nvfp4_partial_amax", "nvfp4_update_scales",
             "nvfp4_partial_cast", "mxfp8_checkpoint_save", "mxfp8_checkpoint_restore", "mxfp8_gemm",
             "mxfp8_device_status", "mxfp8_layer_norm_forward", "mxfp8_layer_norm_backward",
-            "mxfp8_layer_norm_workspace_size", "mxfp8_last_error", "mxfp8_version")
+            "mxfp8_layer_norm_workspace_size", "mxfp8_rms_norm_forward", "mxfp8_rms_norm_backward",
+            "mxfp8_rms_norm_workspace_size", "nvfp4_tensor_amax", "nvfp4_quantize", "nvfp4_restore", "nvfp4_lay_out",
+            "nvfp4_gemm", "mxfp8_last_error", "mxfp8_version")
 
 
 class Tensor(ctypes.Structure):
@@ -126,6 +128,18 @@ def load(path: str | None = None):
         lib.mxfp8_layer_norm_backward.argtypes = [T] * 10 + [i64, i64, vp]
         lib.mxfp8_layer_norm_workspace_size.argtypes = [i64, i64]
         lib.mxfp8_layer_norm_workspace_size.restype = i64
+        lib.mxfp8_rms_norm_forward.argtypes = [T] * 9 + [i64, i64, ctypes.c_float, vp]
+        lib.mxfp8_rms_norm_backward.argtypes = [T] * 8 + [i64, i64, vp]
+        lib.mxfp8_rms_norm_workspace_size.argtypes = [i64, i64]
+        lib.mxfp8_rms_norm_workspace_size.restype = i64
+        lib.nvfp4_tensor_amax.argtypes = [T, T, i64, i64, i32, vp]
+        lib.nvfp4_quantize.argtypes = [T] * 6 + [i64, i64, vp]
+        lib.nvfp4_restore.argtypes = [T] * 4 + [i64, i64, vp]
+        lib.nvfp4_lay_out.argtypes = [T, T, i64, i64, i32, vp]
+        lib.nvfp4_gemm.argtypes = [T] * 8 + [i64, i64, i64, vp]
+        for name in ("mxfp8_rms_norm_forward", "mxfp8_rms_norm_backward", "nvfp4_tensor_amax", "nvfp4_quantize",
+                     "nvfp4_restore", "nvfp4_lay_out", "nvfp4_gemm"):
+            getattr(lib, name).restype = ctypes.c_int
         for name in ("mxfp8_checkpoint_save", "mxfp8_checkpoint_restore", "mxfp8_gemm", "mxfp8_device_status",
                      "mxfp8_layer_norm_forward", "mxfp8_layer_norm_backward"):
             getattr(lib, name).restype = ctypes.c_int

@@ -642,6 +642,143 @@ def prepare_layer_norm_backward(grad_output, input, input_scale, weight, mean, r
                     [t for t in ts if t is not None])
 
 
+def _present(ts):
+    return [t for t in ts if t is not None]
+
+
+def _rms_norm_forward_args(input, residual, weight, sum, output, codes, scale, amax, rstd, rows, cols):
+    return [_matrix(input, "input", rows, cols), _matrix(residual, "residual", rows, cols), handle(weight, "weight"),
+            _matrix(sum, "sum", rows, cols), _matrix(output, "output", rows, cols), _matrix(codes, "codes", rows, cols),
+            handle(scale, "scale"), handle(amax, "amax"), handle(rstd, "rstd")]
+
+
+def mxfp8_rms_norm_forward(input, residual, weight, sum, output, codes, scale, amax, rstd, rows: int, cols: int,
+                           eps: float = 1e-5, stream=None) -> None:
+    """RMS norm of each row of input + residual: the sum, the normed rows as values (``output``) and/or as 8-bit codes
+    with scales, and their largest magnitude (accumulated).  None omits an optional argument."""
+    ts = (input, residual, weight, sum, output, codes, scale, amax, rstd)
+    hs = _rms_norm_forward_args(*ts, rows, cols)
+    _call("mxfp8_rms_norm_forward", _device_of(input, output, codes), *[ctypes.byref(h) for h in hs], int(rows),
+          int(cols), float(eps), _stream(stream, input))
+
+
+def prepare_rms_norm_forward(input, residual, weight, sum, output, codes, scale, amax, rstd, rows, cols,
+                             eps=1e-5) -> Prepared:
+    ts = (input, residual, weight, sum, output, codes, scale, amax, rstd)
+    return Prepared("mxfp8_rms_norm_forward", _rms_norm_forward_args(*ts, rows, cols), (rows, cols, float(eps)),
+                    _present(ts))
+
+
+def mxfp8_rms_norm_workspace_size(rows: int, cols: int) -> int:
+    """Bytes of workspace of mxfp8_rms_norm_backward."""
+    return int(_capi.load().mxfp8_rms_norm_workspace_size(int(rows), int(cols)))
+
+
+def _rms_norm_backward_args(grad_output, grad_sum, input, weight, rstd, grad_input, grad_weight, workspace, rows, cols):
+    return [_matrix(grad_output, "grad_output", rows, cols), _matrix(grad_sum, "grad_sum", rows, cols),
+            _matrix(input, "input", rows, cols), handle(weight, "weight"), handle(rstd, "rstd"),
+            _matrix(grad_input, "grad_input", rows, cols), handle(grad_weight, "grad_weight"),
+            handle(workspace, "workspace")]
+
+
+def mxfp8_rms_norm_backward(grad_output, grad_sum, input, weight, rstd, grad_input, grad_weight, workspace, rows: int,
+                            cols: int, stream=None) -> None:
+    """RMS norm's gradients.  ``input``: the forward pass's sum.  ``grad_sum``: the gradient that reaches the sum along
+    the residual stream, or None."""
+    ts = (grad_output, grad_sum, input, weight, rstd, grad_input, grad_weight, workspace)
+    hs = _rms_norm_backward_args(*ts, rows, cols)
+    _call("mxfp8_rms_norm_backward", _device_of(grad_output, grad_weight), *[ctypes.byref(h) for h in hs], int(rows),
+          int(cols), _stream(stream, grad_weight))
+
+
+def prepare_rms_norm_backward(grad_output, grad_sum, input, weight, rstd, grad_input, grad_weight, workspace, rows,
+                              cols) -> Prepared:
+    ts = (grad_output, grad_sum, input, weight, rstd, grad_input, grad_weight, workspace)
+    return Prepared("mxfp8_rms_norm_backward", _rms_norm_backward_args(*ts, rows, cols), (rows, cols), _present(ts))
+
+
+def nvfp4_tensor_amax(input, amax_tensor, rows: int, cols: int, accumulate: bool = False, stream=None) -> None:
+    """amax_tensor[0] = the largest magnitude of a matrix (``accumulate``: or what it holds, if that is larger)."""
+    hs = [_matrix(input, "input", rows, cols), handle(amax_tensor, "amax_tensor")]
+    _call("nvfp4_tensor_amax", _device_of(input, amax_tensor), *[ctypes.byref(h) for h in hs], int(rows), int(cols),
+          int(bool(accumulate)), _stream(stream, amax_tensor))
+
+
+def prepare_nvfp4_tensor_amax(input, amax_tensor, rows, cols, accumulate=False) -> Prepared:
+    hs = [_matrix(input, "input", rows, cols), handle(amax_tensor, "amax_tensor")]
+    return Prepared("nvfp4_tensor_amax", hs, (rows, cols, bool(accumulate)), [input, amax_tensor])
+
+
+def _packed(n):
+    return (n + 1) // 2
+
+
+def _nvfp4_quantize_args(input, amax_tensor, codes_rowwise, scale_rowwise, codes_colwise, scale_colwise, rows, cols):
+    return [_matrix(input, "input", rows, cols), handle(amax_tensor, "amax_tensor"),
+            _matrix(codes_rowwise, "codes_rowwise", rows, _packed(cols)), handle(scale_rowwise, "scale_rowwise"),
+            _matrix(codes_colwise, "codes_colwise", cols, _packed(rows)), handle(scale_colwise, "scale_colwise")]
+
+
+def nvfp4_quantize(input, amax_tensor, codes_rowwise, scale_rowwise, codes_colwise, scale_colwise, rows: int,
+                   cols: int, stream=None) -> None:
+    """An activation as NVFP4 operands along its rows and/or (transposed) along its columns; None omits one.  Codes two
+    to a byte, one E4M3 scale per 16 values in the GEMM layout."""
+    ts = (input, amax_tensor, codes_rowwise, scale_rowwise, codes_colwise, scale_colwise)
+    hs = _nvfp4_quantize_args(*ts, rows, cols)
+    _call("nvfp4_quantize", _device_of(input, codes_rowwise, codes_colwise), *[ctypes.byref(h) for h in hs], int(rows),
+          int(cols), _stream(stream, input))
+
+
+def prepare_nvfp4_quantize(input, amax_tensor, codes_rowwise, scale_rowwise, codes_colwise, scale_colwise, rows,
+                           cols) -> Prepared:
+    ts = (input, amax_tensor, codes_rowwise, scale_rowwise, codes_colwise, scale_colwise)
+    return Prepared("nvfp4_quantize", _nvfp4_quantize_args(*ts, rows, cols), (rows, cols), _present(ts))
+
+
+def _nvfp4_restore_args(codes, scale, amax_tensor, output, rows, cols):
+    return [_matrix(codes, "codes", rows, _packed(cols)), handle(scale, "scale"), handle(amax_tensor, "amax_tensor"),
+            _matrix(output, "output", rows, cols)]
+
+
+def nvfp4_restore(codes, scale, amax_tensor, output, rows: int, cols: int, stream=None) -> None:
+    """The values that an NVFP4 operand of size rows x cols stands for, in F32 or BF16."""
+    hs = _nvfp4_restore_args(codes, scale, amax_tensor, output, rows, cols)
+    _call("nvfp4_restore", _device_of(codes, output), *[ctypes.byref(h) for h in hs], int(rows), int(cols),
+          _stream(stream, output))
+
+
+def prepare_nvfp4_restore(codes, scale, amax_tensor, output, rows, cols) -> Prepared:
+    return Prepared("nvfp4_restore", _nvfp4_restore_args(codes, scale, amax_tensor, output, rows, cols), (rows, cols),
+                    [codes, scale, amax_tensor, output])
+
+
+def nvfp4_lay_out(codes, output, rows: int, cols: int, transpose: bool = False, stream=None) -> None:
+    """Codes of a weight as nvfp4_partial_cast writes them, as an operand's: a copy with another row stride, or
+    (``transpose``, for the columnwise output) the transposed matrix."""
+    hs = [_matrix(codes, "codes", rows, cols // 2),
+          _matrix(output, "output", *((cols, _packed(rows)) if transpose else (rows, cols // 2)))]
+    _call("nvfp4_lay_out", _device_of(codes, output), *[ctypes.byref(h) for h in hs], int(rows), int(cols),
+          int(bool(transpose)), _stream(stream, output))
+
+
+def _nvfp4_gemm_args(a, a_scale, a_amax, b, b_scale, b_amax, addend, out, m, n, k):
+    return [_matrix(a, "a", m, _packed(k)), handle(a_scale, "a_scale"), handle(a_amax, "a_amax"),
+            _matrix(b, "b", n, _packed(k)), handle(b_scale, "b_scale"), handle(b_amax, "b_amax"),
+            _matrix(addend, "addend", m, n), _matrix(out, "out", m, n)]
+
+
+def nvfp4_gemm(a, a_scale, a_amax, b, b_scale, b_amax, addend, out, m: int, n: int, k: int, stream=None) -> None:
+    """out = A B^T (+ addend) of NVFP4 operands, A m x k and B n x k, with the contraction along their rows."""
+    hs = _nvfp4_gemm_args(a, a_scale, a_amax, b, b_scale, b_amax, addend, out, m, n, k)
+    _call("nvfp4_gemm", _device_of(out, a, b), *[ctypes.byref(h) for h in hs], int(m), int(n), int(k),
+          _stream(stream, out))
+
+
+def prepare_nvfp4_gemm(a, a_scale, a_amax, b, b_scale, b_amax, addend, out, m, n, k) -> Prepared:
+    hs = _nvfp4_gemm_args(a, a_scale, a_amax, b, b_scale, b_amax, addend, out, m, n, k)
+    return Prepared("nvfp4_gemm", hs, (m, n, k), _present((out, a, a_scale, a_amax, b, b_scale, b_amax, addend)))
+
+
 def block_shapes(rows: int, cols: int):
     """Compact (rowwise, columnwise) block-grid shapes: [rows, ceil(cols/32)], [ceil(rows/32), cols]."""
     return (rows, (cols + 31) // 32), ((rows + 31) // 32, cols)

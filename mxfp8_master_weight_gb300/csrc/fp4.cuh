@@ -1,0 +1,58 @@
+// Scale and code arithmetic of NVFP4 operands (see nvfp4_quantize in the header of the library).
+#pragma once
+
+#include <cfloat>
+
+#include "common.cuh"
+
+namespace mxfp8 {
+
+// S of the tensor whose largest magnitude is g: 2688 / g (448 * 6: the largest scale times the largest code),
+// 1 for 0, the largest float if the quotient overflows; NaN where g is not finite, so that every scale is.
+__device__ __forceinline__ float fp4_tensor_scale(float g) {
+  if (g == 0.0f) return 1.0f;
+  const float s = __fdiv_rn(2688.0f, g);
+  return fabsf(g) <= FLT_MAX ? fminf(s, FLT_MAX) : __uint_as_float(0x7fc00000u);
+}
+
+// The scale byte of a block of largest magnitude a (as bits): E4M3(fp32(fp32(a / 6) * S)), NaN (0x7F) where the
+// block or S is not finite.
+__device__ __forceinline__ uint32_t fp4_block_scale(uint32_t a, float tensor_scale) {
+  const float v = __fmul_rn(__fdiv_rn(__uint_as_float(a), 6.0f), tensor_scale);
+  return a >= 0x7f800000u ? 0x7fu : e4m3x2_rn_sat(v, 0.0f) & 0x7fu;
+}
+
+// Value of a non-negative E4M3 byte, exactly, from the format's definition (4 exponent bits with bias 7, 3 mantissa
+// bits; 0x7F is NaN).
+__device__ __forceinline__ float fp4_scale_value(uint32_t b) {
+  if (b == 0x7fu) return __uint_as_float(0x7fc00000u);
+  if (b < 8u) return float(b) * 0x1p-9f;
+  return __uint_as_float(((b >> 3) + 120u) << 23 | (b & 7u) << 20);
+}
+
+// What a block's values are multiplied by: fp32(S / scale), at most the largest float (a zero stays one); 0 where
+// the scale is 0 or NaN.
+__device__ __forceinline__ float fp4_multiplier(uint32_t byte, float tensor_scale) {
+  return byte == 0u || byte == 0x7fu ? 0.0f : fminf(__fdiv_rn(tensor_scale, fp4_scale_value(byte)), FLT_MAX);
+}
+
+// Eight values to E2M1 codes (nearest-even, saturating at 6), the first in the lowest four bits.
+__device__ __forceinline__ uint32_t fp4_codes(const float (&v)[8]) {
+  uint32_t r;
+  asm("{ .reg .b8 a, b, c, d;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      "mov.b32 %0, {a, b, c, d}; }"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// Where entry (r, b) of a scale grid with `tile_cols` tiles of 128 x 4 along a row lies.
+__device__ __forceinline__ int64_t scale_at(int64_t r, int64_t b, int64_t tile_cols) {
+  return ((r >> 7) * tile_cols + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
+}
+
+}  // namespace mxfp8

@@ -74,11 +74,11 @@ cudaError_t residue_maps(const GemmOperand& o, int64_t k, CUtensorMap* maps, con
   return cudaSuccess;
 }
 
-cudaError_t scale_map(const GemmOperand& o, int64_t k, int row_tiles, CUtensorMap* map, const char** what) {
+cudaError_t scale_map(const GemmOperand& o, int64_t k, int row_tiles, CUtensorMap* map, const char** what, int k_tiles) {
   const int64_t along_k = scale_tiles_along_k(k, o.block);
   const cuuint64_t dims[3] = {kScaleTile / 4, cuuint64_t(along_k), cuuint64_t((o.mn + 127) / 128)};
   const cuuint64_t strides[2] = {kScaleTile, cuuint64_t(along_k * kScaleTile)};
-  const cuuint32_t box[3] = {kScaleTile / 4, 1, cuuint32_t(row_tiles)};
+  const cuuint32_t box[3] = {kScaleTile / 4, cuuint32_t(k_tiles), cuuint32_t(row_tiles)};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, o.scale, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE, what);
 }
 

@@ -16,9 +16,9 @@ cudaError_t half_operand_map(const GemmOperand& o, int64_t k, CUtensorMap* map, 
 // 16 maps of an operand that is not aligned: map s has the rows 16 q + s, in boxes of 8 rows by 160
 // bytes from the 16-byte unit that holds a row's first byte.
 cudaError_t residue_maps(const GemmOperand& o, int64_t k, CUtensorMap* maps, const char** what);
-// Boxes of `row_tiles` 512-byte scale tiles, one above the other: coordinates (0, tile along k,
-// 128-row block).
-cudaError_t scale_map(const GemmOperand& o, int64_t k, int row_tiles, CUtensorMap* map, const char** what);
+// Boxes of `row_tiles` 512-byte scale tiles, one above the other, by `k_tiles` along k: coordinates (0, tile along k,
+// 128-row block); zeros past them.
+cudaError_t scale_map(const GemmOperand& o, int64_t k, int row_tiles, CUtensorMap* map, const char** what, int k_tiles = 1);
 
 // The kernels, for operands of any alignment.
 cudaError_t launch_gemm_pair(const GemmParams& g, unsigned* given_up, const DeviceInfo& dev, cudaStream_t stream,

@@ -10,6 +10,7 @@
 namespace mxfp8 {
 
 constexpr int kCkptBlock = 128;  // values per scale of an activation checkpoint
+constexpr int kFp4Values = 16;   // values per scale of an NVFP4 operand
 
 // Bytes of 128x4 scale tiles per 128 logical rows: 512 per 4 blocks.
 inline __host__ __device__ int64_t scale_tile_cols(int64_t nblocks) { return (nblocks + 3) / 4; }
@@ -60,6 +61,88 @@ struct GemmParams {
   int32_t vec_out;      // out (and addend) rows start on 16-byte boundaries
 };
 
+// NVFP4 operands (fp4_quantize.cu, fp4_gemm.cu).
+struct Fp4AmaxParams {
+  const void* in;
+  int64_t rows, cols, ld;  // a dense matrix comes as one row
+  float* amax;             // max-accumulated
+  int32_t vec;             // 16-byte loads of eight (twice four) elements
+};
+
+struct Fp4QuantizeParams {
+  const void* in;
+  int64_t rows, cols, ld;
+  const float* amax;
+  uint8_t* q_r;            // codes [rows][ld_r] or nullptr
+  int64_t ld_r;
+  uint8_t* s_r;
+  uint8_t* q_c;            // codes [cols][ld_c], transposed, or nullptr
+  int64_t ld_c;
+  uint8_t* s_c;
+  int32_t vec_in, vec_r, vec_c;  // 16-byte loads; 4- and 16-byte stores of codes
+};
+
+struct Fp4RestoreParams {
+  const uint8_t* q;
+  int64_t rows, cols, ld_q;
+  const uint8_t* s;
+  const float* amax;
+  void* out;
+  int64_t ld_o;
+  int32_t vec_q, vec_out;  // 8-byte loads, 16-byte stores
+};
+
+struct Fp4LayOutParams {
+  const uint8_t* q;
+  int64_t rows, cols, ld_q;
+  uint8_t* out;
+  int64_t ld_o;
+  int32_t transpose;
+};
+
+// A product's operands are rowwise, `ld` bytes apart and 16-byte aligned, block 16.
+struct Fp4GemmParams {
+  GemmParams g;
+  const float* a_amax;
+  const float* b_amax;
+};
+
+struct RmsForwardParams {
+  const void* x;
+  int64_t rows, cols, ld_x;
+  const void* residual;  // or nullptr
+  int64_t ld_r;
+  const void* weight;
+  void* sum;             // or nullptr
+  int64_t ld_s;
+  void* y;               // or nullptr
+  int64_t ld_y;
+  uint8_t* codes;        // or nullptr
+  int64_t ld_q;
+  uint8_t* scale;
+  float* amax;           // max-accumulated with |y| as stored, or nullptr
+  float* rstd;           // or nullptr
+  float eps;
+  int32_t vec;           // every row and the weight start on 16-byte boundaries
+  int32_t vec_q;         // codes take 8-byte stores
+};
+
+struct RmsBackwardParams {
+  const void* dy;
+  int64_t rows, cols, ld_dy;
+  const void* dsum;      // or nullptr
+  int64_t ld_ds;
+  const void* x;
+  int64_t ld_x;
+  const void* weight;
+  const float* rstd;
+  void* dx;
+  int64_t ld_dx;
+  float* dweight;
+  float* workspace;
+  int32_t vec;
+};
+
 struct NormForwardParams {
   const void* x;
   int64_t rows, cols, ld_x;
@@ -100,6 +183,17 @@ cudaError_t launch_norm_forward(const NormForwardParams& p, int dtype, int wdtyp
                                 const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormBackwardParams& p, int dtype, int wdtype,
                                  const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_tensor_amax(const Fp4AmaxParams& p, int dtype, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_fp4_quantize(const Fp4QuantizeParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_fp4_restore(const Fp4RestoreParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_fp4_lay_out(const Fp4LayOutParams& p, cudaStream_t stream);
+cudaError_t launch_fp4_gemm(const Fp4GemmParams& p, const DeviceInfo& dev, cudaStream_t stream, const char** what);
+cudaError_t launch_rms_forward(const RmsForwardParams& p, int dtype, int wdtype, const DeviceInfo& dev,
+                               cudaStream_t stream);
+cudaError_t launch_rms_backward(const RmsBackwardParams& p, int dtype, int wdtype, const DeviceInfo& dev,
+                                cudaStream_t stream);
+// Rows of partial sums (cols floats each) that the backward pass of RMS norm leaves, at most.
+int64_t rms_partials(int64_t rows, int64_t cols);
 // Rows of partial sums (2 * cols floats each) that the backward pass leaves, at most.
 int64_t norm_partials(int64_t rows, int64_t cols);
 

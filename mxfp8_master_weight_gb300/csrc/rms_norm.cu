@@ -1,0 +1,439 @@
+// RMS norm of the rows of a residual stream, and its gradients.
+//
+//   forward    s = x + residual,  rstd = (sum s^2 / c + eps)^-1/2,  y = s rstd w
+//   backward   xh = s rstd,  g = dy w
+//              ds = rstd (g - xh sum(g xh) / c) + dsum,   dw = sum over rows of dy xh
+//
+// y leaves as values, as E4M3 codes with one E8M0 scale per 128 values of a row, or both, and its largest magnitude may
+// be folded into one word for a 4-bit quantisation that follows.  Everything between load and store is F32; s, y and ds
+// are rounded once, and y and its codes come from the unrounded s.
+//
+// A row belongs to one group of threads, which holds it in registers between the sum and the outputs: a warp for up to
+// 1024 columns, else a block; beyond 32768 columns (16384 backward) the row is read again, mostly from L2.  In the
+// backward pass a thread keeps the running dw of its columns in registers over all rows of its block; a block
+// leaves one row of partial sums, and a second kernel adds the partial rows in their order, so the sums do not depend on
+// the run.
+#include <cfloat>
+#include <type_traits>
+
+#include "fp4.cuh"
+#include "norm_impl.cuh"
+#include "status.h"
+
+namespace mxfp8 {
+namespace {
+
+// The columns of a thread's pieces: eight neighbours where the columns are a multiple of 8, else neighbours across a warp,
+// whose piece spans 256 columns; 128 columns, a block of codes, are 16 lanes or half of a warp's piece (k < 4, k >= 4).
+template <bool kVec>
+struct RowColumns {
+  int64_t cols;
+  int t, width;  // of the row's threads
+  bool aligned;
+  __device__ __forceinline__ int64_t at(int i, int k) const {
+    return kVec ? int64_t(t + i * width) * 8 + k : int64_t((t >> 5) + i * (width >> 5)) * 256 + k * 32 + (t & 31);
+  }
+  __device__ __forceinline__ bool in(int i, int k) const { return at(i, k) < cols; }
+  template <class T>
+  __device__ __forceinline__ Eight load(const void* base, int64_t row, int i) const {
+    if constexpr (kVec) {
+      return load_eight<T>(base, row + at(i, 0), valid(cols, at(i, 0)), aligned);
+    } else {
+      Eight e;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t b = in(i, k) ? load_bits<T>(base, row + at(i, k)) : 0u;
+        e.v[k] = T::kBytes == 4 ? __uint_as_float(b) : __uint_as_float(b << 16);
+      }
+      return e;
+    }
+  }
+  __device__ __forceinline__ Eight param(const void* base, int bf16, int i) const {
+    return bf16 ? load<BF16T>(base, 0, i) : load<F32T>(base, 0, i);
+  }
+  template <class T>
+  __device__ __forceinline__ void store(void* base, int64_t row, int i, const Eight& e) const {
+    if constexpr (kVec) {
+      store_eight<T>(base, row + at(i, 0), e, valid(cols, at(i, 0)), aligned);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (in(i, k)) store_bits<T>(base, row + at(i, k), T::kBytes == 4 ? __float_as_uint(e.v[k]) : bf16x2_rn(e.v[k], 0.0f));
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// |y| as it is stored, as F32 bits.
+template <class T>
+__device__ __forceinline__ uint32_t stored_bits(float v) {
+  return T::kBytes == 4 ? abs_bits(v) : (bf16x2_rn(0.0f, v) & 0x7fff0000u);
+}
+
+__device__ __forceinline__ uint2 encode8(const Eight& y, float f) {
+  float p[8];
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) mul2_rn(y.v[k], y.v[k + 1], f, f, p[k], p[k + 1]);
+  return make_uint2(e4m3x2_rn_sat(p[0], p[1]) | (e4m3x2_rn_sat(p[2], p[3]) << 16),
+                    e4m3x2_rn_sat(p[4], p[5]) | (e4m3x2_rn_sat(p[6], p[7]) << 16));
+}
+
+// The scale byte of block b of a row; behind a row's last block the padding up to a whole group of four.
+__device__ __forceinline__ void store_scale(const RmsForwardParams& p, int64_t row, int64_t b, uint32_t byte) {
+  const int64_t blocks = (p.cols + kCkptBlock - 1) / kCkptBlock;
+  uint8_t* s = p.scale + scale_at(row, b, scale_tile_cols(blocks));
+  *s = uint8_t(byte);
+  if (b == blocks - 1)
+    for (int i = int(b & 3) + 1; i < 4; ++i) *++s = 0;
+}
+
+// Zeros in the scales of the rows behind the last one, up to a whole tile: by the threads of the last row.
+__device__ __forceinline__ void pad_scales(const RmsForwardParams& p, int t, int width) {
+  const int64_t tile_cols = scale_tile_cols((p.cols + kCkptBlock - 1) / kCkptBlock);
+  const int64_t end = (p.rows + 127) / 128 * 128;
+  for (int64_t i = t; i < (end - p.rows) * tile_cols; i += width) {
+    const int64_t row = p.rows + i / tile_cols, tile = i % tile_cols;
+    *reinterpret_cast<uint32_t*>(p.scale + scale_at(row, 4 * tile, tile_cols)) = 0u;
+  }
+}
+
+// Codes of a thread's piece of eight neighbours; the 16 lanes of a block of 128 all take part.
+__device__ __forceinline__ void store_codes(const RmsForwardParams& p, int64_t row, int64_t col, const Eight& y) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = max(m, abs_bits(y.v[k]));
+#pragma unroll
+  for (int off = 1; off < 16; off <<= 1) m = max(m, __shfl_xor_sync(kFullMask, m, off));
+  const int n = valid(p.cols, col);
+  if (n == 0) return;
+  const uint32_t s = e8m0_from_bits<F32T>(m);
+  if ((col & 127) == 0) store_scale(p, row, col >> 7, s);
+  const uint2 q = encode8(y, scale_multiplier(s));
+  uint8_t* dst = p.codes + row * p.ld_q + col;
+  if (p.vec_q && n == 8) {
+    *reinterpret_cast<uint2*>(dst) = q;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) dst[k] = uint8_t((k < 4 ? q.x : q.y) >> (8 * (k & 3)));
+  }
+}
+// The same of a piece that lies across a warp: two blocks.
+__device__ __forceinline__ void store_codes_across(const RmsForwardParams& p, int64_t row, int64_t col0, int lane, const Eight& y) {
+  uint32_t s[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m = max(m, abs_bits(y.v[4 * h + k]));
+    s[h] = e8m0_from_bits<F32T>(__reduce_max_sync(kFullMask, m));
+    if (lane == 0 && col0 + 128 * h < p.cols) store_scale(p, row, (col0 >> 7) + h, s[h]);
+  }
+  uint8_t* dst = p.codes + row * p.ld_q + col0 + lane;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t q = e4m3x2_rn_sat(y.v[k] * scale_multiplier(s[k >> 2]), 0.0f);
+    if (col0 + 32 * k + lane < p.cols) dst[32 * k] = uint8_t(q);
+  }
+}
+
+// Folds a warp's largest |y| into the output word, which most often holds more already.
+__device__ __forceinline__ void fold_amax(float* amax, uint32_t m) {
+  m = canonical_nan<F32T>(__reduce_max_sync(kFullMask, m));
+  if ((threadIdx.x & 31) == 0 && m > __ldcg(reinterpret_cast<const uint32_t*>(amax))) atomicMax(reinterpret_cast<uint32_t*>(amax), m);
+}
+
+// ------------------------------------------------------------------------------ forward
+template <class T, bool kBlock, bool kVec, int NV>
+__global__ void __launch_bounds__(kBlock ? (NV == 1 ? 512 : 1024) : 256)
+    k_rms_forward(const __grid_constant__ RmsForwardParams p, int wbf16) {
+  __shared__ float buf[2][32];
+  grid_dependency_sync();
+  const RowColumns<kVec> c{p.cols, int(kBlock ? threadIdx.x : threadIdx.x & 31), int(kBlock ? blockDim.x : 32), p.vec != 0};
+  const int64_t row = kBlock ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= p.rows) return;  // whole warps only
+  int half = 0;
+  Eight x[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) x[i] = c.template load<T>(p.x, row * p.ld_x, i);
+  if (p.residual != nullptr) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Eight r = c.template load<T>(p.residual, row * p.ld_r, i);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[i].v[k] += r.v[k];
+    }
+  }
+  float s[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[0] += x[i].v[k] * x[i].v[k];
+  group_sum<kBlock>(s, &buf[0][0], half);
+  const float rstd = __frsqrt_rn(s[0] / float(p.cols) + p.eps);
+  if (c.t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (p.sum != nullptr) c.template store<T>(p.sum, row * p.ld_s, i, x[i]);
+    const Eight w = c.param(p.weight, wbf16, i);
+    Eight y;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      y.v[k] = c.in(i, k) ? x[i].v[k] * rstd * w.v[k] : 0.0f;
+      top = max(top, stored_bits<T>(y.v[k]));
+    }
+    if (p.y != nullptr) c.template store<T>(p.y, row * p.ld_y, i, y);
+    if (p.codes != nullptr) {
+      if constexpr (kVec) store_codes(p, row, c.at(i, 0), y);
+      else store_codes_across(p, row, c.at(i, 0) - (c.t & 31), c.t & 31, y);
+    }
+  }
+  if (p.amax != nullptr) fold_amax(p.amax, top);
+  if (p.codes != nullptr && row == p.rows - 1) pad_scales(p, c.t, c.width);
+}
+
+// Rows too long for registers: two passes over the row, the second mostly from L2.
+template <class T>
+__global__ void __launch_bounds__(1024) k_rms_forward_long(const __grid_constant__ RmsForwardParams p, int wbf16) {
+  __shared__ float buf[2][32];
+  grid_dependency_sync();
+  const int64_t row = blockIdx.x, step = int64_t(blockDim.x) * 8;
+  int half = 0;
+  auto load = [&](int64_t col) {
+    const int n = valid(p.cols, col);
+    Eight x = load_eight<T>(p.x, row * p.ld_x + col, n, p.vec);
+    if (p.residual != nullptr) {
+      const Eight r = load_eight<T>(p.residual, row * p.ld_r + col, n, p.vec);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x.v[k] += r.v[k];
+    }
+    return x;
+  };
+  float s[1] = {0.0f};
+  for (int64_t col = int64_t(threadIdx.x) * 8; col < p.cols; col += step) {
+    const Eight x = load(col);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[0] += x.v[k] * x.v[k];
+  }
+  group_sum<true>(s, &buf[0][0], half);
+  const float rstd = __frsqrt_rn(s[0] / float(p.cols) + p.eps);
+  if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+  uint32_t top = 0;
+  for (int64_t base = 0; base < p.cols; base += step) {  // all threads: blocks of codes share their lanes
+    const int64_t col = base + int64_t(threadIdx.x) * 8;
+    const int n = valid(p.cols, col);
+    const Eight x = load(col), w = load_param(p.weight, wbf16, col, n, p.vec);
+    if (p.sum != nullptr) store_eight<T>(p.sum, row * p.ld_s + col, x, n, p.vec);
+    Eight y;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      y.v[k] = k < n ? x.v[k] * rstd * w.v[k] : 0.0f;
+      top = max(top, stored_bits<T>(y.v[k]));
+    }
+    if (p.y != nullptr) store_eight<T>(p.y, row * p.ld_y + col, y, n, p.vec);
+    if (p.codes != nullptr) store_codes(p, row, col, y);
+  }
+  if (p.amax != nullptr) fold_amax(p.amax, top);
+  if (p.codes != nullptr && row == p.rows - 1) pad_scales(p, threadIdx.x, blockDim.x);
+}
+
+// ------------------------------------------------------------------------------ backward
+template <class T, bool kBlock, bool kVec, int NV>
+__global__ void __launch_bounds__(kBlock ? (NV == 1 ? 512 : 1024) : 256)
+    k_rms_backward(const __grid_constant__ RmsBackwardParams p, int wbf16) {
+  __shared__ float buf[2][32];
+  extern __shared__ float s_acc[];  // warp per row: [8 warps][dw of the columns]
+  grid_dependency_sync();
+  const RowColumns<kVec> c{p.cols, int(kBlock ? threadIdx.x : threadIdx.x & 31), int(kBlock ? blockDim.x : 32), p.vec != 0};
+  const int warp = threadIdx.x >> 5;
+  int half = 0;
+  const float inv = 1.0f / float(p.cols);
+  float dw[NV][8];
+  Eight w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    w[i] = c.param(p.weight, wbf16, i);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dw[i][k] = 0.0f;
+  }
+  const int64_t first = kBlock ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 8 + warp;
+  const int64_t step = kBlock ? int64_t(gridDim.x) : int64_t(gridDim.x) * 8;
+  for (int64_t row = first; row < p.rows; row += step) {
+    const float rstd = p.rstd[row];
+    Eight dy[NV], xh[NV];
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      dy[i] = c.template load<T>(p.dy, row * p.ld_dy, i);
+      xh[i] = c.template load<T>(p.x, row * p.ld_x, i);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {  // columns past the last hold zeros
+        xh[i].v[k] *= rstd;
+        const float t = dy[i].v[k] * xh[i].v[k];
+        s[0] += t * w[i].v[k];
+        dw[i][k] += t;
+      }
+    }
+    group_sum<kBlock>(s, &buf[0][0], half);
+    const float along = s[0] * inv;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!c.in(i, 0)) continue;
+      Eight dx, ds = {};
+      if (p.dsum != nullptr) ds = c.template load<T>(p.dsum, row * p.ld_ds, i);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dx.v[k] = rstd * (dy[i].v[k] * w[i].v[k] - xh[i].v[k] * along) + ds.v[k];
+      c.template store<T>(p.dx, row * p.ld_dx, i, dx);
+    }
+  }
+  // one row of partial sums per block: [blocks][cols]
+  float* out = p.workspace + int64_t(blockIdx.x) * p.cols;
+  const int cols = int(p.cols);
+  float* mine = kBlock ? out : s_acc + warp * cols;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c.in(i, k)) mine[c.at(i, k)] = dw[i][k];
+  }
+  if constexpr (!kBlock) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < cols; e += blockDim.x) {
+      float v = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v += s_acc[k * cols + e];
+      out[e] = v;
+    }
+  }
+}
+
+// Rows too long for registers: two passes over the row; the block's partial sums live in its workspace row (each
+// entry touched by one thread only).
+template <class T>
+__global__ void __launch_bounds__(1024) k_rms_backward_long(const __grid_constant__ RmsBackwardParams p, int wbf16) {
+  __shared__ float buf[2][32];
+  grid_dependency_sync();
+  int half = 0;
+  const float inv = 1.0f / float(p.cols);
+  float* out = p.workspace + int64_t(blockIdx.x) * p.cols;
+  const int64_t step = int64_t(blockDim.x) * 8;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const bool first = row == blockIdx.x;
+    const float rstd = p.rstd[row];
+    float s[1] = {0.0f};
+    for (int64_t col = int64_t(threadIdx.x) * 8; col < p.cols; col += step) {
+      const int n = valid(p.cols, col);
+      const Eight dy = load_eight<T>(p.dy, row * p.ld_dy + col, n, p.vec);
+      const Eight x = load_eight<T>(p.x, row * p.ld_x + col, n, p.vec);
+      const Eight w = load_param(p.weight, wbf16, col, n, p.vec);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float t = dy.v[k] * (x.v[k] * rstd);
+        s[0] += t * w.v[k];
+        if (k < n) out[col + k] = t + (first ? 0.0f : out[col + k]);
+      }
+    }
+    group_sum<true>(s, &buf[0][0], half);
+    const float along = s[0] * inv;
+    for (int64_t col = int64_t(threadIdx.x) * 8; col < p.cols; col += step) {
+      const int n = valid(p.cols, col);
+      const Eight dy = load_eight<T>(p.dy, row * p.ld_dy + col, n, p.vec);
+      const Eight x = load_eight<T>(p.x, row * p.ld_x + col, n, p.vec);
+      const Eight w = load_param(p.weight, wbf16, col, n, p.vec);
+      Eight dx, ds = {};
+      if (p.dsum != nullptr) ds = load_eight<T>(p.dsum, row * p.ld_ds + col, n, p.vec);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dx.v[k] = rstd * (dy.v[k] * w.v[k] - x.v[k] * rstd * along) + ds.v[k];
+      store_eight<T>(p.dx, row * p.ld_dx + col, dx, n, p.vec);
+    }
+  }
+}
+
+// Adds the partial rows in their order: a block owns 32 columns, each of its 32 warps a 32nd of the rows, added up
+// through shared memory.
+__global__ void __launch_bounds__(1024) k_rms_partials(const float* __restrict__ part, int nparts, int64_t cols, float* dweight) {
+  __shared__ float s[32][33];
+  grid_dependency_sync();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t e = int64_t(blockIdx.x) * 32 + lane;
+  const int lo = nparts * warp / 32, hi = nparts * (warp + 1) / 32;
+  float v = 0.0f;
+  if (e < cols) {
+#pragma unroll 8
+    for (int r = lo; r < hi; ++r) v += part[int64_t(r) * cols + e];
+  }
+  s[warp][lane] = v;
+  __syncthreads();
+  v = warp_sum(s[lane][warp]);  // this warp: column `warp` of the block
+  const int64_t mine = int64_t(blockIdx.x) * 32 + warp;
+  if (lane == 0 && mine < cols) dweight[mine] = v;
+}
+
+template <class T>
+cudaError_t forward(const RmsForwardParams& p, int wdtype, const DeviceInfo& dev, cudaStream_t stream) {
+  const int64_t pieces = (p.cols + 7) / 8;
+  auto launch = [&](auto kernel, int64_t blocks, int threads) {
+    return launch_kernel(kernel, dim3(unsigned(blocks)), dim3(threads), 0, stream, p, wdtype);
+  };
+  auto direct = [&](auto vec) {
+    constexpr bool kVec = decltype(vec)::value;
+    if (pieces <= 32) return launch(k_rms_forward<T, false, kVec, 1>, (p.rows + 7) / 8, 256);
+    if (pieces <= 64) return launch(k_rms_forward<T, false, kVec, 2>, (p.rows + 7) / 8, 256);
+    if (pieces <= 128) return launch(k_rms_forward<T, false, kVec, 4>, (p.rows + 7) / 8, 256);
+    auto threads = [&](int nv) { return int(((pieces + nv - 1) / nv + 31) / 32 * 32); };
+    if (pieces <= 512) return launch(k_rms_forward<T, true, kVec, 1>, p.rows, threads(1));
+    if (pieces <= 1024) return launch(k_rms_forward<T, true, kVec, 2>, p.rows, threads(2));
+    return launch(k_rms_forward<T, true, kVec, 4>, p.rows, threads(4));
+  };
+  if (pieces <= 4096) return p.cols % 8 == 0 ? direct(std::true_type{}) : direct(std::false_type{});
+  return launch_kernel(k_rms_forward_long<T>, dim3(unsigned(p.rows)), dim3(1024), 0, stream, p, wdtype);
+}
+
+template <class T>
+cudaError_t backward(const RmsBackwardParams& p, int wdtype, const DeviceInfo& dev, cudaStream_t stream) {
+  const int64_t pieces = (p.cols + 7) / 8;
+  const bool block = pieces > 128;
+  const int64_t room = rms_partials(p.rows, p.cols), work = block ? p.rows : (p.rows + 7) / 8;
+  const unsigned blocks = unsigned(work < room ? work : room);
+  auto run = [&](auto kernel, int threads, size_t smem) {
+    return launch_kernel(kernel, dim3(blocks), dim3(threads), smem, stream, p, wdtype);
+  };
+  auto direct = [&](auto vec) {
+    constexpr bool kVec = decltype(vec)::value;
+    auto threads = [&](int nv) { return int(((pieces + nv - 1) / nv + 31) / 32 * 32); };
+    if (block) return pieces <= 512 ? run(k_rms_backward<T, true, kVec, 1>, threads(1), 0) : run(k_rms_backward<T, true, kVec, 2>, threads(2), 0);
+    const size_t smem = size_t(8) * size_t(p.cols) * 4;
+    if (pieces <= 32) return run(k_rms_backward<T, false, kVec, 1>, 256, smem);
+    if (pieces <= 64) return run(k_rms_backward<T, false, kVec, 2>, 256, smem);
+    return run(k_rms_backward<T, false, kVec, 4>, 256, smem);
+  };
+  const cudaError_t e = pieces > 2048         ? run(k_rms_backward_long<T>, 1024, 0)
+                        : p.cols % 8 == 0 ? direct(std::true_type{})
+                                          : direct(std::false_type{});
+  if (e != cudaSuccess) return e;
+  return launch_kernel(k_rms_partials, dim3(unsigned((p.cols + 31) / 32)), dim3(1024), 0, stream,
+                       static_cast<const float*>(p.workspace), int(blocks), p.cols, p.dweight);
+}
+
+}  // namespace
+
+// As many as the blocks of a ring that run at once on 152 SMs.
+int64_t rms_partials(int64_t rows, int64_t cols) {
+  const int64_t most = cols <= 512 ? 3040 : (cols <= 1024 ? 1824 : (cols <= 2048 ? 912 : (cols <= 4096 ? 456 : 304)));
+  return rows < most ? rows : most;
+}
+
+cudaError_t launch_rms_forward(const RmsForwardParams& p, int dtype, int wdtype, const DeviceInfo& dev, cudaStream_t stream) {
+  return dtype == 0 ? forward<F32T>(p, wdtype, dev, stream) : forward<BF16T>(p, wdtype, dev, stream);
+}
+
+cudaError_t launch_rms_backward(const RmsBackwardParams& p, int dtype, int wdtype, const DeviceInfo& dev, cudaStream_t stream) {
+  return dtype == 0 ? backward<F32T>(p, wdtype, dev, stream) : backward<BF16T>(p, wdtype, dev, stream);
+}
+
+}  // namespace mxfp8

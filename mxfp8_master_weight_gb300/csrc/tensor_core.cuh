@@ -210,6 +210,30 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
   }
 }
 
+// Instruction descriptor of the 4-bit kind, E2M1 x E2M1 with E4M3 scales, F32 sums; both operands' rows run along
+// the contraction.
+__host__ __device__ constexpr uint32_t instr_desc4(int m, int n) {
+  return (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 7) << 27);
+}
+// D = (accumulate ? D : 0) + A B^T over 64 4-bit values of k, a scale per 16.
+template <int kCtas>
+__device__ __forceinline__ void mma_scaled4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
+                                            uint32_t sb, uint32_t accumulate) {
+  if constexpr (kCtas == 1) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  }
+}
+
 // The barrier completes a phase's arrival when all tensor-core work issued before is done.
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
