@@ -50,6 +50,25 @@ __device__ __forceinline__ uint32_t fp4_codes(const float (&v)[8]) {
   return r;
 }
 
+// What a product's sums are multiplied by: (1 / Sa) (1 / Sb), in two steps where it is too small to be one number.
+struct Fp4Factor {
+  float first, then;
+  __device__ __forceinline__ Fp4Factor(float a_amax, float b_amax) {
+    const float ra = __frcp_rn(fp4_tensor_scale(a_amax)), rb = __frcp_rn(fp4_tensor_scale(b_amax)), both = __fmul_rn(ra, rb);
+    const bool one = !(both < 0x1p-100f);
+    first = one ? both : ra;
+    then = one ? 1.0f : rb;
+  }
+  template <int N>
+  __device__ __forceinline__ void apply(float (&v)[N]) const {
+#pragma unroll
+    for (int k = 0; k < N; k += 2) mul2_rn(v[k], v[k + 1], first, first, v[k], v[k + 1]);
+    if (then == 1.0f) return;
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] *= then;
+  }
+};
+
 // Where entry (r, b) of a scale grid with `tile_cols` tiles of 128 x 4 along a row lies.
 __device__ __forceinline__ int64_t scale_at(int64_t r, int64_t b, int64_t tile_cols) {
   return ((r >> 7) * tile_cols + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);

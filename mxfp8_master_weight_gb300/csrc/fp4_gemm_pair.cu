@@ -34,7 +34,7 @@ static_assert(kScaleCol + 2 * kScaleSet == 512 && kSecondBuffer + 256 == kScaleC
 
 struct PairParams {
   Fp4GemmParams f;
-  CUtensorMap a, b, b_half, sa, sb;
+  CUtensorMap a, b, b_half, sa, sb, out;
   unsigned* given_up;
   int64_t whole, units;  // whole tiles first, then halves
   int32_t stages, b_bytes;
@@ -53,6 +53,10 @@ __device__ __forceinline__ Tile tile_of(const PairParams& q, int64_t unit, int64
   return t;
 }
 
+// How the sums leave: through TMA as BF16 or F32, or by the writers' own stores (an addend, rows that start anywhere).
+enum Out { kOutBf16, kOutF32, kOutAny };
+
+template <Out kOut>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_fp4_gemm_pair(const __grid_constant__ PairParams q) {
   extern __shared__ char raw[];
   const GemmParams& p = q.f.g;
@@ -165,47 +169,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_fp4_g
   } else {
     const int side = (warp - 2) >> 2;  // the first or second half of the columns
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
-    const float ra = __frcp_rn(fp4_tensor_scale(p.k > 0 ? *q.f.a_amax : 0.0f)), rb = __frcp_rn(fp4_tensor_scale(p.k > 0 ? *q.f.b_amax : 0.0f));
+    const int lane = threadIdx.x & 31;
+    const Fp4Factor factor(p.k > 0 ? *q.f.a_amax : 0.0f, p.k > 0 ? *q.f.b_amax : 0.0f);
     uint32_t nth = 0;
     for (int64_t unit = first; unit < q.units; unit += step, ++nth) {
       const Tile t = tile_of(q, unit, tiles_m, tiles_n);
-      const int cols = (t.half ? 512 : 1024) / kWriters;  // this warp's
       const uint32_t buffer = nth & 1;
       // no two tiles' sums are ready at once that this warp has not drained: the next tile's
       // instructions wait for sums_free
       if (!tc::mbar_wait(sums_full + 8 * buffer, (nth >> 1) & 1, gave_up)) break;
       tc::fence_after_sync();
-      const int64_t row0 = t.tm * 256 + 128 * rank + 32 * (warp & 3), col0 = t.col + cols * side;
-      const uint32_t d = tmem + lanes + (buffer ? kSecondBuffer : 0) + cols * side;
-      // The shared columns, the last of buffer 0 and the first of buffer 1, come first; the arrival after them also says
-      // that the warp is done with the tile before.
-      const int width = p.out_f32 ? 32 : 64, chunks = cols / width;
-      const int from = (buffer ? kSecondBuffer : 0) + cols * side;  // this warp's columns of tensor memory
-      const int shared = buffer ? 256 - from : from + cols - kSecondBuffer;  // of these, shared
-      int left = shared <= 0 ? 0 : (shared + width - 1) / width * (width / 32);  // loads until they are drained
-      if (left > cols / 32) left = cols / 32;
-      auto drained = [&] {
-        tc::fence_before_sync();
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) tc::mbar_arrive_cluster_relaxed(sums_free, 0);
-      };
-      if (left == 0 || nk == 0) drained();
+      const int64_t row0 = t.tm * 256 + 128 * rank + 32 * (warp & 3);
+      const uint32_t d = tmem + lanes + (buffer ? kSecondBuffer : 0);
+      // 64 columns at a time, the two sides in turn.  The shared columns, the last of buffer 0 and the first of buffer 1,
+      // are in registers after the first 64 of both; the arrival then also says that the warp is done with the
+      // tile before.
+      const int parts = t.half ? 1 : 2;
 #pragma unroll 1
-      for (int i = 0; i < chunks; ++i) {
-        const int c = width * (buffer ? i : chunks - 1 - i);
-        write_rows(p, writers + (warp - 2) * kWriterBytes, row0, col0 + c, [&](int e, float(&v)[32]) {
-          if (nk > 0) {
-            tc::tmem_load32(d + c + e, v);
+      for (int i = 0; i < parts; ++i) {
+        const int c = 64 * (2 * (buffer ? i : parts - 1 - i) + side);
+        float v[64];
+        if (nk > 0) {
+          tc::tmem_load64(d + c, v);
+        } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = v[k] * ra * rb;
-          } else {
+          for (int k = 0; k < 64; ++k) v[k] = 0.0f;
+        }
+        if (i == 0) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_cluster_relaxed(sums_free, 0);
+        }
+        factor.apply(v);
+        char* stage = writers + (warp - 2) * kWriterBytes;
+        if constexpr (kOut == kOutAny) {
+          auto part = [&](int e0) {
+            return [&v, e0](int e, float(&o)[32]) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = 0.0f;
+              for (int k = 0; k < 32; ++k) o[k] = v[e0 + e + k];
+            };
+          };
+          write_rows(p, stage, row0, t.col + c, part(0));
+          if (p.out_f32) write_rows(p, stage, row0, t.col + c + 32, part(32));
+        } else {
+          if (row0 >= p.m) continue;
+#pragma unroll
+          for (int h = 0; h < (kOut == kOutF32 ? 2 : 1); ++h) {
+            const int64_t col = t.col + c + 32 * h;
+            if (col >= p.n) break;
+            if (lane == 0) tc::bulk_wait_read();
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              uint4 w;
+              if constexpr (kOut == kOutF32) {
+                const float* e = v + 32 * h + 4 * u;
+                w = make_uint4(__float_as_uint(e[0]), __float_as_uint(e[1]), __float_as_uint(e[2]), __float_as_uint(e[3]));
+              } else {
+                const float* e = v + 8 * u;
+                w = make_uint4(bf16x2_rn(e[0], e[1]), bf16x2_rn(e[2], e[3]), bf16x2_rn(e[4], e[5]), bf16x2_rn(e[6], e[7]));
+              }
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = w;
+            }
+            tc::fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) {
+              tc::tma_store_2d(&q.out, tc::smem_addr(stage), int(col), int(row0));
+              tc::bulk_commit();
+            }
           }
-          if (nk > 0 && left != 0 && --left == 0) drained();
-        });
+        }
       }
     }
+    if (kOut != kOutAny && lane == 0) tc::bulk_wait();
   }
   __syncwarp();
   tc::fence_before_sync();
@@ -242,8 +278,15 @@ cudaError_t launch_fp4_gemm_pair(const Fp4GemmParams& f, unsigned* given_up, con
   const int fit = kStageRoom / (kBoxBytes + q.b_bytes + kScaleBytes);
   q.stages = fit < kMaxStages ? fit : kMaxStages;
   const unsigned grid = 2 * unsigned(q.units < pairs ? q.units : pairs);
-  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_fp4_gemm_pair), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  return e != cudaSuccess ? e : launch_kernel(k_fp4_gemm_pair, dim3(grid), dim3(kThreads), kSmem, stream, q);
+  auto run = [&](auto kernel) {
+    const cudaError_t r = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    return r != cudaSuccess ? r : launch_kernel(kernel, dim3(grid), dim3(kThreads), kSmem, stream, q);
+  };
+  // A store through TMA ends a row on 16 bytes: it would write past one that ends elsewhere.
+  if (g.addend != nullptr || !g.vec_out || g.n % (g.out_f32 ? 4 : 8) != 0) return run(k_fp4_gemm_pair<kOutAny>);
+  e = output_map(g, &q.out, what);
+  if (e != cudaSuccess) return e;
+  return g.out_f32 ? run(k_fp4_gemm_pair<kOutF32>) : run(k_fp4_gemm_pair<kOutBf16>);
 }
 
 }  // namespace mxfp8

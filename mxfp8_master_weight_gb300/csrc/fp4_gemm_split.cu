@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp4_gemm_split(const __grid_con
   float* part = reinterpret_cast<float*>(smem);
   const bool writer = warp >= 2;
   if (writer) {
-    const float ra = __frcp_rn(fp4_tensor_scale(*q.f.a_amax)), rb = __frcp_rn(fp4_tensor_scale(*q.f.b_amax));
+    const Fp4Factor factor(*q.f.a_amax, *q.f.b_amax);
     const int row = 32 * (warp & 3) + (threadIdx.x & 31);
     tc::mbar_wait(done, 0, gave_up);
     tc::fence_after_sync();
@@ -133,8 +133,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp4_gemm_split(const __grid_con
     for (int c = 0; c < NT; c += 16) {
       float v[16];
       tc::tmem_load16(tmem + (uint32_t(32 * (warp & 3)) << 16) + c, v);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = v[e] * ra * rb;
+      factor.apply(v);
       if (q.swapped) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) part[(c + e) * 128 + row] = v[e];

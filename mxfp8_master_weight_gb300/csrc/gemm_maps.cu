@@ -82,4 +82,14 @@ cudaError_t scale_map(const GemmOperand& o, int64_t k, int row_tiles, CUtensorMa
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, o.scale, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE, what);
 }
 
+cudaError_t output_map(const GemmParams& g, CUtensorMap* map, const char** what) {
+  const int size = g.out_f32 ? 4 : 2;
+  const cuuint64_t dims[2] = {cuuint64_t(g.n), cuuint64_t(g.m)};
+  // of a single row any stride will do
+  const cuuint64_t strides[1] = {cuuint64_t(g.m == 1 ? (g.n * size + 15) / 16 * 16 : g.ld_o * size)};
+  const cuuint32_t box[2] = {cuuint32_t(128 / size), 32};
+  return encode(map, g.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.out, dims, strides,
+                box, CU_TENSOR_MAP_SWIZZLE_128B, what);
+}
+
 }  // namespace mxfp8

@@ -20,6 +20,9 @@ cudaError_t residue_maps(const GemmOperand& o, int64_t k, CUtensorMap* maps, con
 // 128-row block); zeros past them.
 cudaError_t scale_map(const GemmOperand& o, int64_t k, int row_tiles, CUtensorMap* map, const char** what, int k_tiles = 1);
 
+// Boxes of 32 rows by 128 bytes of the output under the 128-byte swizzle, for stores; its rows start and end on 16 bytes.
+cudaError_t output_map(const GemmParams& g, CUtensorMap* map, const char** what);
+
 // The kernels, for operands of any alignment.
 cudaError_t launch_gemm_pair(const GemmParams& g, unsigned* given_up, const DeviceInfo& dev, cudaStream_t stream,
                              const char** what);
