@@ -15,25 +15,42 @@ __device__ __forceinline__ float fp4_tensor_scale(float g) {
   return fabsf(g) <= FLT_MAX ? fminf(s, FLT_MAX) : __uint_as_float(0x7fc00000u);
 }
 
-// The scale byte of a block of largest magnitude a (as bits): E4M3(fp32(fp32(a / 6) * S)), NaN (0x7F) where the
-// block or S is not finite.
-__device__ __forceinline__ uint32_t fp4_block_scale(uint32_t a, float tensor_scale) {
-  const float v = __fmul_rn(__fdiv_rn(__uint_as_float(a), 6.0f), tensor_scale);
-  return a >= 0x7f800000u ? 0x7fu : e4m3x2_rn_sat(v, 0.0f) & 0x7fu;
+// fp32(a / 6) for a >= 0, correctly rounded: a product with the rounded reciprocal, the exact remainder, one
+// correction (P. Markstein, IBM J. Res. Dev. 34(1), 1990); equal to the quotient for 0 and from 2^-124 up to the largest
+// float (tests/test_div6_identity.py).  Below, where a remainder may be subnormal, the division itself.
+__device__ __forceinline__ float fp4_div6(float a) {
+  constexpr float kInv6 = 0x1.555556p-3f;
+  const float q = __fmul_rn(a, kInv6);
+  float r = __fmaf_rn(__fmaf_rn(-6.0f, q, a), kInv6, q);
+  if (a < 0x1p-124f && a > 0.0f) r = __fdiv_rn(a, 6.0f);
+  return r;
 }
 
-// Value of a non-negative E4M3 byte, exactly, from the format's definition (4 exponent bits with bias 7, 3 mantissa
-// bits; 0x7F is NaN).
+// The scale bytes of two blocks of largest magnitudes a and b (as bits), b's in the second byte: E4M3(fp32(fp32(a / 6) * S)),
+// NaN (0x7F) where the block or S is not finite.
+__device__ __forceinline__ uint32_t fp4_block_scales(uint32_t a, uint32_t b, float tensor_scale) {
+  const float va = __fmul_rn(fp4_div6(__uint_as_float(a)), tensor_scale), vb = __fmul_rn(fp4_div6(__uint_as_float(b)), tensor_scale);
+  uint32_t s = e4m3x2_rn_sat(va, vb) & 0x7f7fu;
+  if (a >= 0x7f800000u) s |= 0x7fu;
+  if (b >= 0x7f800000u) s |= 0x7f00u;
+  return s;
+}
+
+// Value of a non-negative E4M3 byte, exactly; 0x7F is NaN.
 __device__ __forceinline__ float fp4_scale_value(uint32_t b) {
-  if (b == 0x7fu) return __uint_as_float(0x7fc00000u);
-  if (b < 8u) return float(b) * 0x1p-9f;
-  return __uint_as_float(((b >> 3) + 120u) << 23 | (b & 7u) << 20);
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(b)));
+  return f16_lo(h);
 }
 
 // What a block's values are multiplied by: fp32(S / scale), at most the largest float (a zero stays one); 0 where
-// the scale is 0 or NaN.
-__device__ __forceinline__ float fp4_multiplier(uint32_t byte, float tensor_scale) {
-  return byte == 0u || byte == 0x7fu ? 0.0f : fminf(__fdiv_rn(tensor_scale, fp4_scale_value(byte)), FLT_MAX);
+// the scale is 0 or NaN.  A scale is one of eight significands times a power of two, so the quotients by the significands,
+// fp32(S / (1 + i / 8)) in `by`, are all that is divided: scaling them is exact (2688 / FLT_MAX / 448 is a normal float).
+__device__ __forceinline__ float fp4_quotient(int i, float tensor_scale) { return __fdiv_rn(tensor_scale, 1.0f + 0.125f * float(i)); }
+__device__ __forceinline__ float fp4_multiplier(uint32_t byte, const float* by) {
+  const uint32_t scale = __float_as_uint(fp4_scale_value(byte));
+  const float f = by[(scale >> 20) & 7u] * __uint_as_float((254u << 23) - (scale & 0x7f800000u));
+  return byte == 0u || byte == 0x7fu ? 0.0f : fminf(f, FLT_MAX);
 }
 
 // Eight values to E2M1 codes (nearest-even, saturating at 6), the first in the lowest four bits.

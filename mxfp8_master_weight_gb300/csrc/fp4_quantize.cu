@@ -20,134 +20,209 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 128;
 
-// Eight elements at p as F32 values; zeros past n.
+// Eight elements as they lie: BF16 pairs, or F32 values.
 template <class T>
-__device__ __forceinline__ void load8(const char* p, int n, bool vec, float (&v)[8]) {
+struct Eight {
+  static constexpr int W = T::kBytes * 2;
+  uint32_t w[W];
+  __device__ __forceinline__ float get(int k) const {
+    if constexpr (T::kBytes == 4) return __uint_as_float(w[k]);
+    else return (k & 1) ? bf16_hi(w[k >> 1]) : bf16_lo(w[k >> 1]);
+  }
+};
+
+// Elements [0, n) of p, zeros past them.
+template <class T>
+__device__ __forceinline__ Eight<T> load8(const char* p, int n, bool vec) {
+  Eight<T> v;
   if (vec && n >= 8) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-    if constexpr (T::kBytes == 4) {
-      const uint4 b = *reinterpret_cast<const uint4*>(p + 16);
-      const uint32_t u[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[k] = __uint_as_float(w[k]);
-        v[4 + k] = __uint_as_float(u[k]);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] = bf16_lo(w[k]);
-        v[2 * k + 1] = bf16_hi(w[k]);
-      }
+    for (int k = 0; k < Eight<T>::W; k += 4) {
+      const uint4 a = ld_stream16(p + 4 * k);
+      v.w[k] = a.x; v.w[k + 1] = a.y; v.w[k + 2] = a.z; v.w[k + 3] = a.w;
     }
   } else {
 #pragma unroll
+    for (int k = 0; k < Eight<T>::W; ++k) v.w[k] = 0;
+#pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const uint32_t b = k < n ? load_bits<T>(p, k) : 0u;
-      v[k] = T::kBytes == 4 ? __uint_as_float(b) : __uint_as_float(b << 16);
+      if (k < n) {
+        const uint32_t b = load_bits<T>(p, k);
+        if constexpr (T::kBytes == 4) v.w[k] = b; else v.w[k >> 1] |= b << (16 * (k & 1));
+      }
     }
   }
+  return v;
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// Maxima of |x| as bit patterns, which order as the values do, NaN above infinity; BF16 keeps two to a word.
+template <class T>
+__device__ __forceinline__ uint32_t max_bits(uint32_t a, uint32_t b) {
+  if constexpr (T::kBytes == 4) return max(a, b); else return __vmaxu2(a, b);
+}
 
 // ------------------------------------------------------------------------------ largest magnitude
-// Items of a row's 2048 values (a dense matrix is one row); a block folds its items into one atomic maximum of
-// non-negative bit patterns, which order as their values, NaN above infinity.
+// Items of a row's 8192 values (a dense matrix is one row), four loads under way per thread; a block folds its items into
+// one atomic maximum.  A matrix that one block reads in a few rounds is read by one block, which stores its maximum:
+// no word has to be cleared before.
+constexpr int kAmaxLoads = 4, kAmaxItem = 8 * kThreads * kAmaxLoads;
 template <class T>
 __global__ void __launch_bounds__(kThreads) k_tensor_amax(const __grid_constant__ Fp4AmaxParams p) {
   __shared__ uint32_t s_max[kThreads / 32];
   grid_dependency_sync();
-  const int64_t per_row = (p.cols + 8 * kThreads - 1) / (8 * kThreads), items = per_row * p.rows;
+  const int64_t per_row = (p.cols + kAmaxItem - 1) / kAmaxItem, items = per_row * p.rows;
+  int64_t row = blockIdx.x / per_row, part = blockIdx.x - row * per_row;
+  const int64_t step_row = gridDim.x / per_row, step_part = gridDim.x - step_row * per_row;
   uint32_t m = 0;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t row = item / per_row, col = (item - row * per_row) * (8 * kThreads) + 8 * threadIdx.x;
-    if (col >= p.cols) continue;
-    float v[8];
-    load8<T>(static_cast<const char*>(p.in) + (row * p.ld + col) * T::kBytes, p.cols - col < 8 ? int(p.cols - col) : 8, p.vec, v);
+    const int64_t col = part * kAmaxItem + 8 * threadIdx.x;
+    const char* src = static_cast<const char*>(p.in) + (row * p.ld + col) * T::kBytes;
+    Eight<T> v[kAmaxLoads];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, abs_bits(v[k]));
+    for (int l = 0; l < kAmaxLoads; ++l) {
+      const int64_t left = p.cols - col - l * 8 * kThreads;
+      v[l] = load8<T>(src + l * 8 * kThreads * T::kBytes, left >= 8 ? 8 : (left > 0 ? int(left) : 0), p.vec);
+    }
+#pragma unroll
+    for (int l = 0; l < kAmaxLoads; ++l)
+#pragma unroll
+      for (int k = 0; k < Eight<T>::W; ++k) m = max_bits<T>(m, v[l].w[k] & T::kAbsMask);
+    row += step_row;
+    part += step_part;
+    if (part >= per_row) {
+      part -= per_row;
+      ++row;
+    }
   }
+  if constexpr (T::kBytes == 2) m = max(m << 16, m & 0xffff0000u);
   m = __reduce_max_sync(kFullMask, m);
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) m = max(m, s_max[w]);
-    atomicMax(reinterpret_cast<uint32_t*>(p.amax), canonical_nan<F32T>(m));
+    m = canonical_nan<F32T>(m);
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.amax);
+    if (p.store) *out = m;
+    else atomicMax(out, m);
   }
 }
 
 // ------------------------------------------------------------------------------ quantisation
+// The largest magnitudes of eight blocks as F32 bits: own[i], or those of two threads' halves.  BF16 sends two to a word.
+template <class T>
+__device__ __forceinline__ void join8(const uint32_t (&own)[8], int lane_mask, uint32_t (&m)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    if constexpr (T::kBytes == 4) {
+      m[i] = max(own[i], __shfl_xor_sync(kFullMask, own[i], lane_mask));
+      m[i + 1] = max(own[i + 1], __shfl_xor_sync(kFullMask, own[i + 1], lane_mask));
+    } else {
+      uint32_t two = own[i] | own[i + 1] << 16;
+      two = __vmaxu2(two, __shfl_xor_sync(kFullMask, two, lane_mask));
+      m[i] = two << 16;
+      m[i + 1] = two & 0xffff0000u;
+    }
+  }
+}
+
 template <class T, bool kRow, bool kCol>
-__global__ void __launch_bounds__(kThreads) k_fp4_quantize(const __grid_constant__ Fp4QuantizeParams p) {
-  __shared__ float s_mult[128];
+__global__ void __launch_bounds__(kThreads, T::kBytes == 2 ? 3 : 2) k_fp4_quantize(const __grid_constant__ Fp4QuantizeParams p) {
+  constexpr int W = Eight<T>::W;
+  __shared__ float s_by[8];
   __shared__ __align__(16) uint8_t s_scale[2][1024];
   __shared__ __align__(16) uint32_t s_col[kTile][17];
   grid_dependency_sync();
   const float S = fp4_tensor_scale(*p.amax);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (t < 128) s_mult[t] = fp4_multiplier(uint32_t(t), S);
-  const int64_t tiles_c = (p.cols + kTile - 1) / kTile;
-  const int64_t rb = blockIdx.x / tiles_c, cb = blockIdx.x - rb * tiles_c;
+  if (t < 8) s_by[t] = fp4_quotient(t, S);
+  const uint32_t tiles_c = uint32_t((p.cols + kTile - 1) / kTile);
+  const uint32_t rb = blockIdx.x / tiles_c, cb = blockIdx.x - rb * tiles_c;
   const int r8 = warp * 16 + (lane >> 4) * 8, c8 = (lane & 15) * 8;
-  const int64_t row = rb * kTile + r8, col = cb * kTile + c8;
+  const int64_t row = int64_t(rb) * kTile + r8, col = int64_t(cb) * kTile + c8;
   const int n = p.cols - col >= 8 ? 8 : (p.cols > col ? int(p.cols - col) : 0);
   const int left = p.rows - row >= 8 ? 8 : (p.rows > row ? int(p.rows - row) : 0);
-  float v[8][8];
+  Eight<T> v[8];
   const char* src = static_cast<const char*>(p.in) + (row * p.ld + col) * T::kBytes;
+  if (left == 8) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) load8<T>(src + i * p.ld * T::kBytes, i < left ? n : 0, p.vec_in, v[i]);
+    for (int i = 0; i < 8; ++i) v[i] = load8<T>(src + i * p.ld * T::kBytes, n, p.vec_in);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = load8<T>(src + i * p.ld * T::kBytes, i < left ? n : 0, p.vec_in);
+  }
+  uint32_t rm[8], cm[W];
+#pragma unroll
+  for (int k = 0; k < W; ++k) cm[k] = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const uint32_t a = v[i].w[k] & T::kAbsMask;
+      m = max_bits<T>(m, a);
+      cm[k] = max_bits<T>(cm[k], a);
+    }
+    rm[i] = T::kBytes == 4 ? m : max(m & 0xffffu, m >> 16);
+  }
   __syncthreads();
   if constexpr (kRow) {
+    uint32_t m[8];
+    join8<T>(rm, 1, m);
+    // blocks of columns past the last hold zeros, and so do rows: their scales are zero too, unless S is NaN
+    const bool some = (col & ~int64_t(15)) < p.cols;
     uint8_t* q = p.q_r + row * p.ld_r + (col >> 1);
+    uint8_t* at = &s_scale[0][(c8 >> 6) * 512 + (r8 & 31) * 16 + (r8 >> 5) * 4 + ((c8 >> 4) & 3)];  // block c8 / 16 of row r8
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t m = 0;
+    for (int i = 0; i < 8; i += 2) {
+      uint32_t s2 = fp4_block_scales(m[i], m[i + 1], S);
+      if (!some || i >= left) s2 = 0;
+      else if (i + 1 >= left) s2 &= 0xffu;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) m = max(m, abs_bits(v[i][k]));
-      m = max(m, __shfl_xor_sync(kFullMask, m, 1));
-      const bool inside = i < left && (col & ~int64_t(15)) < p.cols;
-      const uint32_t s = inside ? fp4_block_scale(m, S) : 0u;
-      const float f = s_mult[s];
-      float y[8];
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t s = s2 >> (8 * h) & 0xffu;
+        const float f = fp4_multiplier(s, s_by);
+        float y[8];
 #pragma unroll
-      for (int k = 0; k < 8; k += 2) mul2_rn(v[i][k], v[i][k + 1], f, f, y[k], y[k + 1]);
-      const uint32_t codes = fp4_codes(y);
-      if ((lane & 1) == 0) {  // block c8 / 16 of row r8 + i
-        const int r = r8 + i, b = c8 >> 4;
-        s_scale[0][(b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3)] = uint8_t(s);
-      }
-      if (i < left) {
-        if (p.vec_r && n == 8) {
-          *reinterpret_cast<uint32_t*>(q + i * p.ld_r) = codes;
-        } else {
+        for (int k = 0; k < 8; k += 2) mul2_rn(v[i + h].get(k), v[i + h].get(k + 1), f, f, y[k], y[k + 1]);
+        const uint32_t codes = fp4_codes(y);
+        if ((lane & 1) == 0) at[16 * (i + h)] = uint8_t(s);
+        if (i + h < left) {
+          uint8_t* o = q + (i + h) * p.ld_r;
+          if (p.vec_r && n == 8) {
+            *reinterpret_cast<uint32_t*>(o) = codes;
+          } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (2 * k < n) q[i * p.ld_r + k] = uint8_t(codes >> (8 * k));
+            for (int k = 0; k < 4; ++k)
+              if (2 * k < n) o[k] = uint8_t(codes >> (8 * k));
+          }
         }
       }
     }
   }
   if constexpr (kCol) {
+    uint32_t own[8], m[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      uint32_t m = 0;
+    for (int k = 0; k < 8; ++k) own[k] = T::kBytes == 4 ? cm[k % W] : (cm[k >> 1] >> (16 * (k & 1))) & 0xffffu;
+    join8<T>(own, 16, m);
+    const bool some = (row & ~int64_t(15)) < p.rows;
+    uint8_t* at = &s_scale[1][(warp >> 2) * 512 + (c8 & 31) * 16 + (c8 >> 5) * 4 + (warp & 3)];  // block `warp` of transposed row c8
+    uint32_t* turned = &s_col[c8][(r8 >> 3) ^ ((c8 >> 5) << 1)];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i][k]));
-      m = max(m, __shfl_xor_sync(kFullMask, m, 16));
-      const bool inside = k < n && (row & ~int64_t(15)) < p.rows;
-      const uint32_t s = inside ? fp4_block_scale(m, S) : 0u;
-      const float f = s_mult[s];
-      float y[8];
+    for (int k = 0; k < 8; k += 2) {
+      uint32_t s2 = fp4_block_scales(m[k], m[k + 1], S);
+      if (!some || k >= n) s2 = 0;
+      else if (k + 1 >= n) s2 &= 0xffu;
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) mul2_rn(v[i][k], v[i + 1][k], f, f, y[i], y[i + 1]);
-      if (lane < 16) {  // block `warp` of transposed row c8 + k
-        const int r = c8 + k;
-        s_scale[1][(warp >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (warp & 3)] = uint8_t(s);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t s = s2 >> (8 * h) & 0xffu;
+        const float f = fp4_multiplier(s, s_by);
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) mul2_rn(v[i].get(k + h), v[i + 1].get(k + h), f, f, y[i], y[i + 1]);
+        if (lane < 16) at[16 * (k + h)] = uint8_t(s);
+        turned[17 * (k + h)] = fp4_codes(y);
       }
-      s_col[c8 + k][(r8 >> 3) ^ ((c8 >> 5) << 1)] = fp4_codes(y);
     }
   }
   __syncthreads();
@@ -155,21 +230,22 @@ __global__ void __launch_bounds__(kThreads) k_fp4_quantize(const __grid_constant
   const int which = t >> 6, unit = t & 63;
   if (t < 128) {
     const int64_t tile_cols = scale_tile_cols(((which == 0 ? p.cols : p.rows) + 15) / 16);
-    const int64_t r128 = which == 0 ? rb : cb, at = 2 * (which == 0 ? cb : rb) + (unit >> 5);
+    const int64_t r128 = which == 0 ? rb : cb, at = 2 * int64_t(which == 0 ? cb : rb) + (unit >> 5);
     uint8_t* s = which == 0 ? p.s_r : p.s_c;
     if ((which == 0 ? kRow : kCol) && at < tile_cols)
       *reinterpret_cast<uint4*>(s + (r128 * tile_cols + at) * 512 + (unit & 31) * 16) = *reinterpret_cast<const uint4*>(&s_scale[which][unit * 16]);
   }
   if constexpr (kCol) {
-    const int width = p.rows - rb * kTile < kTile ? int(p.rows - rb * kTile + 1) / 2 : kTile / 2;  // bytes of a transposed row
+    const int64_t rows_left = p.rows - int64_t(rb) * kTile;
+    const int width = rows_left < kTile ? int(rows_left + 1) / 2 : kTile / 2;  // bytes of a transposed row
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int j = (t >> 2) + 64 * h, u = t & 3;
-      if (cb * kTile + j >= p.cols) continue;
+      if (int64_t(cb) * kTile + j >= p.cols) continue;
       uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = s_col[j][(4 * u + k) ^ ((j >> 5) << 1)];
-      uint8_t* q = p.q_c + (cb * kTile + j) * p.ld_c + rb * (kTile / 2) + 16 * u;
+      uint8_t* q = p.q_c + (int64_t(cb) * kTile + j) * p.ld_c + int64_t(rb) * (kTile / 2) + 16 * u;
       if (p.vec_c && 16 * u + 16 <= width) {
         *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
       } else {
@@ -182,15 +258,19 @@ __global__ void __launch_bounds__(kThreads) k_fp4_quantize(const __grid_constant
 }
 
 // ------------------------------------------------------------------------------ values
-// A thread restores blocks of 16: 8 bytes of codes and one scale.
+// A thread restores a block of 16: 8 bytes of codes and one scale; a warp 512 columns of a row.  Rows that start anywhere
+// go through the warp's shared memory and out as 32-bit words aligned in the output, neighbours across the lanes (BF16: a lone
+// value at either end where the row starts between words).
 template <class T>
 __global__ void __launch_bounds__(kThreads) k_fp4_restore(const __grid_constant__ Fp4RestoreParams p) {
   grid_dependency_sync();
   const float r = __frcp_rn(fp4_tensor_scale(*p.amax));
-  const int64_t nb = (p.cols + 15) / 16, per_row = (nb + 31) / 32, tile_cols = scale_tile_cols(nb);
-  const int64_t row = (blockIdx.x / per_row) * 8 + (threadIdx.x >> 5), b = (blockIdx.x % per_row) * 32 + (threadIdx.x & 31);
-  if (row >= p.rows || b >= nb) return;
-  const int n = p.cols - 16 * b < 16 ? int(p.cols - 16 * b) : 16;
+  const int64_t nb = (p.cols + 15) / 16;
+  const uint32_t per_row = uint32_t((nb + 31) / 32), lane = threadIdx.x & 31;
+  const uint32_t rows8 = blockIdx.x / per_row, part = blockIdx.x - rows8 * per_row;
+  const int64_t row = int64_t(rows8) * 8 + (threadIdx.x >> 5), b = int64_t(part) * 32 + lane;
+  if (row >= p.rows) return;  // whole warps
+  const int n = p.cols - 16 * b >= 16 ? 16 : (p.cols > 16 * b ? int(p.cols - 16 * b) : 0);
   const uint8_t* q = p.q + row * p.ld_q + 8 * b;
   uint32_t w[2] = {0, 0};
   if (p.vec_q && n == 16) {
@@ -202,29 +282,50 @@ __global__ void __launch_bounds__(kThreads) k_fp4_restore(const __grid_constant_
     for (int k = 0; k < 8; ++k)
       if (2 * k < n) w[k >> 2] |= uint32_t(q[k]) << (8 * (k & 3));
   }
-  const float s = fp4_scale_value(p.s[scale_at(row, b, tile_cols)] & 0x7fu);
+  const float s = n == 0 ? 0.0f : fp4_scale_value(p.s[scale_at(row, b, scale_tile_cols(nb))] & 0x7fu);
   float v[16];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     uint32_t h;
     asm("{ .reg .b8 c; cvt.u8.u32 c, %1; cvt.rn.f16x2.e2m1x2 %0, c; }" : "=r"(h) : "r"(w[k >> 2] >> (8 * (k & 3)) & 0xffu));
-    v[2 * k] = __fmul_rn(__fmul_rn(f16_lo(h), s), r);  // the first product is exact
-    v[2 * k + 1] = __fmul_rn(__fmul_rn(f16_hi(h), s), r);
+    mul2_rn(f16_lo(h), f16_hi(h), s, s, v[2 * k], v[2 * k + 1]);  // exact
+    mul2_rn(v[2 * k], v[2 * k + 1], r, r, v[2 * k], v[2 * k + 1]);
   }
+  uint32_t o[4 * T::kBytes];
+#pragma unroll
+  for (int k = 0; k < 4 * T::kBytes; ++k) o[k] = T::kBytes == 4 ? __float_as_uint(v[k % 16]) : bf16x2_rn(v[2 * k % 16], v[(2 * k + 1) % 16]);
   char* out = static_cast<char*>(p.out) + (row * p.ld_o + 16 * b) * T::kBytes;
-  if (p.vec_out && n == 16) {
+  if (p.vec_out) {
+    if (n == 16) {
 #pragma unroll
-    for (int k = 0; k < 16; k += 16 / T::kBytes) {
-      if constexpr (T::kBytes == 4)
-        *reinterpret_cast<float4*>(out + 4 * k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-      else
-        *reinterpret_cast<uint4*>(out + 2 * k) = make_uint4(bf16x2_rn(v[k], v[k + 1]), bf16x2_rn(v[k + 2], v[k + 3]),
-                                                            bf16x2_rn(v[k + 4], v[k + 5]), bf16x2_rn(v[k + 6], v[k + 7]));
+      for (int k = 0; k < 4 * T::kBytes; k += 4) *reinterpret_cast<uint4*>(out + 4 * k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (k < n) store_bits<T>(out, k, T::kBytes == 4 ? o[k % (4 * T::kBytes)] : o[k >> 1] >> (16 * (k & 1)));
     }
-  } else {
+    return;
+  }
+  __shared__ __align__(16) uint32_t s_line[kThreads / 32][32 * (4 * T::kBytes + 1)];  // a word apart, against bank conflicts
+  uint32_t* line = s_line[threadIdx.x >> 5];
+  constexpr int kWords = 4 * T::kBytes;
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (k < n) store_bits<T>(out, k, T::kBytes == 4 ? __float_as_uint(v[k]) : bf16x2_rn(v[k], 0.0f));
+  for (int k = 0; k < kWords; ++k) line[lane * (kWords + 1) + k] = o[k];
+  __syncwarp();
+  auto word = [&](int i) { return line[(i / kWords) * (kWords + 1) + i % kWords]; };
+  const int64_t first = int64_t(part) * 512;
+  const int width = p.cols - first < 512 ? int(p.cols - first) : 512;
+  char* start = static_cast<char*>(p.out) + (row * p.ld_o + first) * T::kBytes;
+  if constexpr (T::kBytes == 4) {
+    for (int i = int(lane); i < width; i += 32) reinterpret_cast<uint32_t*>(start)[i] = word(i);
+  } else {
+    auto half = [&](int i) { return word(i >> 1) >> (16 * (i & 1)) & 0xffffu; };
+    const int head = int(reinterpret_cast<uintptr_t>(start) >> 1) & 1, pairs = (width - head) / 2;
+    uint32_t* words = reinterpret_cast<uint32_t*>(start + 2 * head);
+    for (int i = int(lane); i < pairs; i += 32) words[i] = half(2 * i + head) | half(2 * i + 1 + head) << 16;
+    uint16_t* ends = reinterpret_cast<uint16_t*>(start);
+    if (lane == 0 && head) ends[0] = uint16_t(half(0));
+    if (lane == 1 && ((width - head) & 1)) ends[width - 1] = uint16_t(half(width - 1));
   }
 }
 
@@ -287,9 +388,14 @@ cudaError_t quantize(const Fp4QuantizeParams& p, cudaStream_t stream) {
 
 }  // namespace
 
+int64_t amax_items(const Fp4AmaxParams& p) { return (p.cols + kAmaxItem - 1) / kAmaxItem * p.rows; }
+
+// One block: rounds of 8192 values, about 0.3 us each, against a cleared word and a second launch.
+bool one_block_amax(const Fp4AmaxParams& p) { return amax_items(p) <= 4; }
+
 cudaError_t launch_tensor_amax(const Fp4AmaxParams& p, int dtype, const DeviceInfo& dev, cudaStream_t stream) {
-  const int64_t items = (p.cols + 8 * kThreads - 1) / (8 * kThreads) * p.rows, most = 8 * int64_t(dev.sms);
-  const dim3 grid(unsigned(items < most ? items : most));
+  const int64_t items = amax_items(p), most = 8 * int64_t(dev.sms);
+  const dim3 grid(p.store ? 1u : unsigned(items < most ? items : most));
   return dtype == 0 ? launch_kernel(k_tensor_amax<F32T>, grid, dim3(kThreads), 0, stream, p)
                     : launch_kernel(k_tensor_amax<BF16T>, grid, dim3(kThreads), 0, stream, p);
 }

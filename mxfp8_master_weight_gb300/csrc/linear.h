@@ -67,6 +67,7 @@ struct Fp4AmaxParams {
   int64_t rows, cols, ld;  // a dense matrix comes as one row
   float* amax;             // max-accumulated
   int32_t vec;             // 16-byte loads of eight (twice four) elements
+  int32_t store;           // one block, which stores its maximum
 };
 
 struct Fp4QuantizeParams {
@@ -183,6 +184,7 @@ cudaError_t launch_norm_forward(const NormForwardParams& p, int dtype, int wdtyp
                                 const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormBackwardParams& p, int dtype, int wdtype,
                                  const DeviceInfo& dev, cudaStream_t stream);
+bool one_block_amax(const Fp4AmaxParams& p);
 cudaError_t launch_tensor_amax(const Fp4AmaxParams& p, int dtype, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_fp4_quantize(const Fp4QuantizeParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_fp4_restore(const Fp4RestoreParams& p, int dtype, cudaStream_t stream);

@@ -499,19 +499,22 @@ int nvfp4_tensor_amax(const mxfp8_tensor* input, mxfp8_tensor* amax_tensor, int6
     if (int rc = check_matrix(input, "input", rows, cols, &p.ld)) return rc;
     if (int rc = want_float(input, "input")) return rc;
   }
-  if (accumulate == 0) {
+  if (some) {
+    p.in = input->data;
+    p.rows = rows;
+    p.cols = cols;
+    if (p.ld == cols || rows == 1) {  // dense: one row
+      p.cols = rows * cols;
+      p.rows = 1;
+    }
+    p.vec = aligned(p.in, p.rows == 1 ? 0 : p.ld, elem_bytes(input->dtype), 16);
+    p.store = accumulate == 0 && mxfp8::one_block_amax(p);
+  }
+  if (accumulate == 0 && !p.store) {
     const cudaError_t e = cudaMemsetAsync(p.amax, 0, 4, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_status(e, "tensor amax");
   }
   if (!some) return ok();
-  p.in = input->data;
-  p.rows = rows;
-  p.cols = cols;
-  if (p.ld == cols || rows == 1) {  // dense: one row
-    p.cols = rows * cols;
-    p.rows = 1;
-  }
-  p.vec = aligned(p.in, p.rows == 1 ? 0 : p.ld, elem_bytes(input->dtype), 16);
   DeviceInfo dev;
   if (int rc = device_info(&dev)) return rc;
   return cuda_status(mxfp8::launch_tensor_amax(p, dtype_index(input->dtype), dev, static_cast<cudaStream_t>(stream)),
