@@ -374,6 +374,288 @@ __global__ void __launch_bounds__(1024) k_rms_partials(const float* __restrict__
   if (lane == 0 && mine < cols) dweight[mine] = v;
 }
 
+// ------------------------------------------------------------------------------ rings
+// Many rows of up to 8192 columns: persistent blocks, each with a ring of rows in shared memory that thread 0 keeps
+// full with bulk copies, whatever the warps wait for.  A thread owns fixed columns, NV pieces of 8, and keeps what belongs to
+// a column (weight, running gradient) in registers over all rows.  A row takes one barrier of its block.
+//
+// What thread 0 fetches: rows blockIdx.x, blockIdx.x + gridDim.x, ... of up to three matrices of one type into the slots
+// in turn, one behind the other.  Rows that do not start on 16 bytes (kVec false) land as many bytes into their place as
+// they start into their first 16-byte unit; the units at a row's ends are copied whole, but for those that reach past the
+// matrix, whose bytes the thread copies.
+struct RowFeed {
+  RingHead* h;
+  char* slots;
+  const char* m[3];
+  int64_t pitch[3];
+  int64_t row, rows;
+  uint32_t bytes, place, count, issued;  // bytes of a row; of its place in a slot; matrices
+  template <bool kVec>
+  __device__ __forceinline__ void next(const Ring& ring, uint32_t s) {
+    if (row >= rows) return;
+    char* slot = slots + s * ring.slot_bytes;
+    const uint32_t bar = tc::smem_addr(&h->full[s]), dst = tc::smem_addr(slot);
+    if constexpr (kVec) {
+      tc::mbar_expect(bar, bytes * count);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < int(count)) tc::bulk_load(dst + i * place, m[i] + row * pitch[i], bytes, bar);
+    } else {
+      RingFeed::Units u[3];
+      uint32_t total = 0;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        if (i >= int(count)) continue;
+        const RingFeed one{nullptr, nullptr, nullptr, nullptr, 0, 0, row, rows, 0, 0, 0};
+        u[i] = one.ends(slot + i * place, m[i], pitch[i], bytes);
+        total += uint32_t(u[i].to - u[i].from);
+      }
+      tc::mbar_expect(bar, total);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        if (i >= int(count)) continue;
+        const uintptr_t origin = reinterpret_cast<uintptr_t>(m[i] + row * pitch[i]) & ~uintptr_t(15);
+        tc::bulk_load(dst + i * place + uint32_t(u[i].from - origin), reinterpret_cast<const void*>(u[i].from),
+                      uint32_t(u[i].to - u[i].from), bar);
+      }
+    }
+    ++issued;
+    row += gridDim.x;
+  }
+  template <bool kVec>
+  __device__ __forceinline__ void start(const Ring& ring, uint32_t* gave_up) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < ring.slots; ++i) tc::mbar_init(tc::smem_addr(&h->full[i]), 1);
+      *gave_up = 0;
+      tc::mbar_init_fence();
+      for (int i = 0; i < ring.slots; ++i) next<kVec>(ring, i);
+    }
+    __syncthreads();
+  }
+  // Where the current row of matrix i lies in its slot.
+  template <bool kVec>
+  __device__ __forceinline__ const char* at(const char* slot, int i, int64_t r) const {
+    return slot + i * place + ring_offset<kVec>(m[i], r * pitch[i]);
+  }
+};
+
+// Ring of `count` rows of `bytes` each per slot.
+Ring rows_ring(int64_t bytes, int count, int blocks) {
+  const int64_t place = (bytes + 127) / 128 * 128;
+  return ring_of(bytes, place * (count - 1), 0, blocks);
+}
+
+__device__ __forceinline__ void as_pairs(const Eight& e, Two (&v)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = Two(e.v[2 * k], e.v[2 * k + 1]);
+}
+__device__ __forceinline__ float sum_of(Two a) {
+  float lo, hi;
+  a.get(lo, hi);
+  return lo + hi;
+}
+
+template <class T, bool kVec, int TH, int NV, int BLOCKS>
+__global__ void __launch_bounds__(TH, BLOCKS)
+    k_rms_forward_ring(const __grid_constant__ RmsForwardParams p, int wbf16, Ring ring, unsigned* given_up) {
+  extern __shared__ __align__(128) char smem[];
+  __shared__ uint32_t s_gave_up;
+  volatile uint32_t* gave_up = &s_gave_up;
+  RingHead* h = reinterpret_cast<RingHead*>(smem);
+  char* slots = smem + kRingHead;
+  grid_dependency_sync();
+  const bool res = p.residual != nullptr;
+  RowFeed feed{h, slots, {static_cast<const char*>(p.x), static_cast<const char*>(p.residual), nullptr},
+               {p.ld_x * T::kBytes, p.ld_r * T::kBytes, 0}, int64_t(blockIdx.x), p.rows, uint32_t(p.cols * T::kBytes),
+               uint32_t(ring.second), res ? 2u : 1u, 0};
+  feed.start<kVec>(ring, &s_gave_up);
+  const int t = threadIdx.x, cols = int(p.cols);
+  const float inv = 1.0f / float(cols);
+  Two w[NV][4];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) as_pairs(ring_param<kVec, TH>(p.weight, wbf16, i, cols), w[i]);
+  int s = 0, half = 0;
+  uint32_t phase = 0, top = 0;
+  bool good = true;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    // A warp whose wait was given up still goes through the barriers, but writes no more rows and fetches nothing: its
+    // slot's copy may yet land, and a barrier takes no second arrival for the same copy.  (A warp as a whole: the lanes of a
+    // block of codes share their maximum.)
+    good = __all_sync(kFullMask, good & tc::mbar_wait(tc::smem_addr(&h->full[s]), phase, gave_up));
+    const char* slot = slots + s * ring.slot_bytes;
+    const char *x_row = feed.at<kVec>(slot, 0, row), *r_row = res ? feed.at<kVec>(slot, 1, row) : nullptr;
+    Two x[NV][4], sq(0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      as_pairs(ring_piece<T, kVec, TH>(x_row, i, cols), x[i]);
+      if (res) {
+        Two r[4];
+        as_pairs(ring_piece<T, kVec, TH>(r_row, i, cols), r);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[i][k] = x[i][k] + r[k];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sq = fma2(x[i][k], x[i][k], sq);
+    }
+    float sum[1] = {sum_of(sq)};
+    ring_sum<TH>(sum, h, half);
+    if (t == 0 && good) feed.next<kVec>(ring, s);  // every thread has the row in registers
+    const float rstd = __frsqrt_rn(sum[0] * inv + p.eps);
+    if (t == 0 && good && p.rstd != nullptr) p.rstd[row] = rstd;
+    const Two r2(rstd);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      Eight e;
+      if (p.sum != nullptr && good) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[i][k].get(e.v[2 * k], e.v[2 * k + 1]);
+        ring_store<T, kVec, TH>(p.sum, row * p.ld_s, i, cols, e);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) ((x[i][k] * r2) * w[i][k]).get(e.v[2 * k], e.v[2 * k + 1]);
+      if (p.y != nullptr && good) ring_store<T, kVec, TH>(p.y, row * p.ld_y, i, cols, e);
+      if (p.amax != nullptr) {  // past the row x and w are 0
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = max(top, stored_bits<T>(e.v[k]));
+      }
+      if (p.codes != nullptr && good) {
+        if constexpr (kVec) store_codes(p, row, ring_col<true, TH>(i, 0), e);
+        else store_codes_across(p, row, ring_col<false, TH>(i, 0) - (t & 31), t & 31, e);
+      }
+    }
+    if (++s == ring.slots) {
+      s = 0;
+      phase ^= 1;
+    }
+    if (row == p.rows - 1 && p.codes != nullptr) pad_scales(p, t, TH);
+  }
+  if (p.amax != nullptr) fold_amax(p.amax, top);
+  __syncthreads();
+  if (t == 0 && *gave_up != 0) {
+    tc::settle_copies(tc::smem_addr(h->full), uint32_t(ring.slots), feed.issued);
+    tc::report_given_up(given_up);
+  }
+}
+
+template <class T, bool kVec, int TH, int NV, int BLOCKS>
+__global__ void __launch_bounds__(TH, BLOCKS)
+    k_rms_backward_ring(const __grid_constant__ RmsBackwardParams p, int wbf16, Ring ring, unsigned* given_up) {
+  extern __shared__ __align__(128) char smem[];
+  __shared__ uint32_t s_gave_up;
+  volatile uint32_t* gave_up = &s_gave_up;
+  RingHead* h = reinterpret_cast<RingHead*>(smem);
+  char* slots = smem + kRingHead;
+  grid_dependency_sync();
+  const bool add = p.dsum != nullptr;
+  RowFeed feed{h, slots, {static_cast<const char*>(p.dy), static_cast<const char*>(p.x), static_cast<const char*>(p.dsum)},
+               {p.ld_dy * T::kBytes, p.ld_x * T::kBytes, p.ld_ds * T::kBytes}, int64_t(blockIdx.x), p.rows,
+               uint32_t(p.cols * T::kBytes), uint32_t(ring.second), add ? 3u : 2u, 0};
+  feed.start<kVec>(ring, &s_gave_up);
+  const int t = threadIdx.x, cols = int(p.cols);
+  const float inv = 1.0f / float(cols);
+  Two dw[NV][4], w[NV][4];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    as_pairs(ring_param<kVec, TH>(p.weight, wbf16, i, cols), w[i]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dw[i][k] = Two(0.0f);
+  }
+  int s = 0, half = 0;
+  uint32_t phase = 0;
+  bool good = true;  // as in the forward pass
+  float next_rstd = p.rstd[blockIdx.x];  // a row ahead: its latency passes behind the row before
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const float rstd = next_rstd;
+    if (row + gridDim.x < p.rows) next_rstd = p.rstd[row + gridDim.x];
+    good &= tc::mbar_wait(tc::smem_addr(&h->full[s]), phase, gave_up);
+    const char* slot = slots + s * ring.slot_bytes;
+    const char *dy_row = feed.at<kVec>(slot, 0, row), *x_row = feed.at<kVec>(slot, 1, row);
+    const char* ds_row = add ? feed.at<kVec>(slot, 2, row) : nullptr;
+    const Two r2(rstd);
+    Two along(0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (ring_col<kVec, TH>(i, 0) >= cols) continue;
+      Two dy[4], x[4];  // past the row zeros, which add nothing
+      as_pairs(ring_piece<T, kVec, TH>(dy_row, i, cols), dy);
+      as_pairs(ring_piece<T, kVec, TH>(x_row, i, cols), x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const Two d = dy[k] * (x[k] * r2);
+        along = fma2(d, w[i][k], along);
+        dw[i][k] = dw[i][k] + d;
+      }
+    }
+    float sum[1] = {sum_of(along)};
+    ring_sum<TH>(sum, h, half);
+    if (row != blockIdx.x && good && t == 0) feed.next<kVec>(ring, s == 0 ? ring.slots - 1 : s - 1);  // every thread is past the row before
+    // dx = rstd (dy w) + xh (-rstd mean(g xh)) + dsum
+    const Two c(-rstd * (sum[0] * inv));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (ring_col<kVec, TH>(i, 0) >= cols) continue;
+      Two dy[4], x[4], ds[4];
+      as_pairs(ring_piece<T, kVec, TH>(dy_row, i, cols), dy);
+      as_pairs(ring_piece<T, kVec, TH>(x_row, i, cols), x);
+      if (add) {
+        as_pairs(ring_piece<T, kVec, TH>(ds_row, i, cols), ds);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ds[k] = Two(0.0f);
+      }
+      Eight dx;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) fma2(x[k] * r2, c, fma2(dy[k] * w[i][k], r2, ds[k])).get(dx.v[2 * k], dx.v[2 * k + 1]);
+      if (good) ring_store<T, kVec, TH>(p.dx, row * p.ld_dx, i, cols, dx);
+    }
+    if (++s == ring.slots) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+  float* out = p.workspace + int64_t(blockIdx.x) * cols;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    Eight e;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dw[i][k].get(e.v[2 * k], e.v[2 * k + 1]);
+    ring_store<F32T, kVec, TH>(out, 0, i, cols, e);
+  }
+  __syncthreads();
+  if (t == 0 && *gave_up != 0) {
+    tc::settle_copies(tc::smem_addr(h->full), uint32_t(ring.slots), feed.issued);
+    tc::report_given_up(given_up);
+  }
+}
+
+// Whether rows of `cols` columns go through a ring: enough of them for the prologue of a persistent block to pay, and rows
+// of 64 bytes or more.
+bool ring_rows(int64_t rows, int64_t cols, bool odd, const DeviceInfo& dev) {
+  return cols <= 8192 && (cols % 16 == 0 || cols >= 64) && rows >= (odd ? 12 : 4) * int64_t(dev.sms);
+}
+
+template <class T, bool kVec, int TH, int NV, int BLOCKS>
+cudaError_t forward_ring(const RmsForwardParams& p, int wdtype, const DeviceInfo& dev, unsigned* given_up, cudaStream_t stream) {
+  const Ring ring = rows_ring(p.cols * T::kBytes + (kVec ? 0 : 30), p.residual != nullptr ? 2 : 1, BLOCKS);
+  auto kernel = k_rms_forward_ring<T, kVec, TH, NV, BLOCKS>;
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring.smem));
+  if (e != cudaSuccess) return e;
+  const int64_t most = BLOCKS * dev.sms;
+  return launch_kernel(kernel, dim3(unsigned(p.rows < most ? p.rows : most)), dim3(TH), ring.smem, stream, p, wdtype, ring, given_up);
+}
+
+template <class T, bool kVec, int TH, int NV, int BLOCKS>
+cudaError_t backward_ring(const RmsBackwardParams& p, int wdtype, const DeviceInfo& dev, unsigned* given_up, unsigned* blocks,
+                          cudaStream_t stream) {
+  const Ring ring = rows_ring(p.cols * T::kBytes + (kVec ? 0 : 30), p.dsum != nullptr ? 3 : 2, BLOCKS);
+  auto kernel = k_rms_backward_ring<T, kVec, TH, NV, BLOCKS>;
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring.smem));
+  if (e != cudaSuccess) return e;
+  const int64_t most = BLOCKS * dev.sms, room = rms_partials(p.rows, p.cols);
+  *blocks = unsigned(most < room ? most : room);
+  return launch_kernel(kernel, dim3(*blocks), dim3(TH), ring.smem, stream, p, wdtype, ring, given_up);
+}
+
 template <class T>
 cudaError_t forward(const RmsForwardParams& p, int wdtype, const DeviceInfo& dev, cudaStream_t stream) {
   const int64_t pieces = (p.cols + 7) / 8;
@@ -390,7 +672,23 @@ cudaError_t forward(const RmsForwardParams& p, int wdtype, const DeviceInfo& dev
     if (pieces <= 1024) return launch(k_rms_forward<T, true, kVec, 2>, p.rows, threads(2));
     return launch(k_rms_forward<T, true, kVec, 4>, p.rows, threads(4));
   };
-  if (pieces <= 4096) return p.cols % 8 == 0 ? direct(std::true_type{}) : direct(std::false_type{});
+  const bool odd = p.cols % 8 != 0;
+  if (ring_rows(p.rows, p.cols, odd, dev) && (odd || p.vec)) {
+    unsigned* given_up = nullptr;
+    const cudaError_t e = given_up_address(dev.device, &given_up);
+    if (e != cudaSuccess) return e;
+    auto ring = [&](auto vec) {
+      constexpr bool kVec = decltype(vec)::value, kNarrow = T::kBytes == 2;
+      if (pieces <= 64) return forward_ring<T, kVec, 64, 1, kNarrow ? 12 : 10>(p, wdtype, dev, given_up, stream);
+      if (pieces <= 128) return forward_ring<T, kVec, 128, 1, 6>(p, wdtype, dev, given_up, stream);
+      if (pieces <= 256) return forward_ring<T, kVec, 256, 1, 4>(p, wdtype, dev, given_up, stream);
+      if (pieces <= 512) return forward_ring<T, kVec, 256, 2, kNarrow ? 3 : 2>(p, wdtype, dev, given_up, stream);
+      if (pieces <= 768) return forward_ring<T, kVec, 256, 3, 2>(p, wdtype, dev, given_up, stream);
+      return forward_ring<T, kVec, 512, 2, 1>(p, wdtype, dev, given_up, stream);
+    };
+    return odd ? ring(std::false_type{}) : ring(std::true_type{});
+  }
+  if (pieces <= 4096) return odd ? direct(std::false_type{}) : direct(std::true_type{});
   return launch_kernel(k_rms_forward_long<T>, dim3(unsigned(p.rows)), dim3(1024), 0, stream, p, wdtype);
 }
 
@@ -399,7 +697,7 @@ cudaError_t backward(const RmsBackwardParams& p, int wdtype, const DeviceInfo& d
   const int64_t pieces = (p.cols + 7) / 8;
   const bool block = pieces > 128;
   const int64_t room = rms_partials(p.rows, p.cols), work = block ? p.rows : (p.rows + 7) / 8;
-  const unsigned blocks = unsigned(work < room ? work : room);
+  unsigned blocks = unsigned(work < room ? work : room);
   auto run = [&](auto kernel, int threads, size_t smem) {
     return launch_kernel(kernel, dim3(blocks), dim3(threads), smem, stream, p, wdtype);
   };
@@ -412,9 +710,25 @@ cudaError_t backward(const RmsBackwardParams& p, int wdtype, const DeviceInfo& d
     if (pieces <= 64) return run(k_rms_backward<T, false, kVec, 2>, 256, smem);
     return run(k_rms_backward<T, false, kVec, 4>, 256, smem);
   };
-  const cudaError_t e = pieces > 2048         ? run(k_rms_backward_long<T>, 1024, 0)
-                        : p.cols % 8 == 0 ? direct(std::true_type{})
-                                          : direct(std::false_type{});
+  const bool odd = p.cols % 8 != 0;
+  cudaError_t e;
+  if (ring_rows(p.rows, p.cols, odd, dev) && (odd || p.vec)) {
+    unsigned* given_up = nullptr;
+    e = given_up_address(dev.device, &given_up);
+    if (e != cudaSuccess) return e;
+    auto ring = [&](auto vec) {
+      constexpr bool kVec = decltype(vec)::value, kNarrow = T::kBytes == 2;
+      if (pieces <= 64) return backward_ring<T, kVec, 64, 1, kNarrow ? 12 : 8>(p, wdtype, dev, given_up, &blocks, stream);
+      if (pieces <= 128) return backward_ring<T, kVec, 128, 1, kNarrow ? 6 : 5>(p, wdtype, dev, given_up, &blocks, stream);
+      if (pieces <= 256) return backward_ring<T, kVec, 256, 1, kNarrow ? 4 : 3>(p, wdtype, dev, given_up, &blocks, stream);
+      if (pieces <= 512) return backward_ring<T, kVec, 256, 2, kNarrow ? 3 : 2>(p, wdtype, dev, given_up, &blocks, stream);
+      if (pieces <= 768) return backward_ring<T, kVec, kNarrow ? 256 : 384, kNarrow ? 3 : 2, kNarrow ? 2 : 1>(p, wdtype, dev, given_up, &blocks, stream);
+      return backward_ring<T, kVec, 512, 2, 1>(p, wdtype, dev, given_up, &blocks, stream);
+    };
+    e = odd ? ring(std::false_type{}) : ring(std::true_type{});
+  } else {
+    e = pieces > 2048 ? run(k_rms_backward_long<T>, 1024, 0) : odd ? direct(std::false_type{}) : direct(std::true_type{});
+  }
   if (e != cudaSuccess) return e;
   return launch_kernel(k_rms_partials, dim3(unsigned((p.cols + 31) / 32)), dim3(1024), 0, stream,
                        static_cast<const float*>(p.workspace), int(blocks), p.cols, p.dweight);
