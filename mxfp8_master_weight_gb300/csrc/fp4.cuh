@@ -17,23 +17,25 @@ __device__ __forceinline__ float fp4_tensor_scale(float g) {
 
 // fp32(a / 6) for a >= 0, correctly rounded: a product with the rounded reciprocal, the exact remainder, one
 // correction (P. Markstein, IBM J. Res. Dev. 34(1), 1990); equal to the quotient for 0 and from 2^-124 up to the largest
-// float (tests/test_div6_identity.py).  Below, where a remainder may be subnormal, the division itself.
-__device__ __forceinline__ float fp4_div6(float a) {
+// float (tests/test_div6_identity.py); NaN for an infinity.  Below 2^-124 the remainder may be subnormal and the result off
+// by units in the last place, which only a tensor of largest magnitude under 2^-100 can tell: any other's scales of
+// such blocks round to 0.  For those, `tiny` takes the division itself.
+__device__ __forceinline__ float fp4_div6(float a, bool tiny) {
   constexpr float kInv6 = 0x1.555556p-3f;
+  if (tiny) return __fdiv_rn(a, 6.0f);
   const float q = __fmul_rn(a, kInv6);
-  float r = __fmaf_rn(__fmaf_rn(-6.0f, q, a), kInv6, q);
-  if (a < 0x1p-124f && a > 0.0f) r = __fdiv_rn(a, 6.0f);
-  return r;
+  return __fmaf_rn(__fmaf_rn(-6.0f, q, a), kInv6, q);
 }
+__device__ __forceinline__ bool fp4_tiny(float amax) { return amax < 0x1p-100f; }
 
-// The scale bytes of two blocks of largest magnitudes a and b (as bits), b's in the second byte: E4M3(fp32(fp32(a / 6) * S)),
-// NaN (0x7F) where the block or S is not finite.
-__device__ __forceinline__ uint32_t fp4_block_scales(uint32_t a, uint32_t b, float tensor_scale) {
-  const float va = __fmul_rn(fp4_div6(__uint_as_float(a)), tensor_scale), vb = __fmul_rn(fp4_div6(__uint_as_float(b)), tensor_scale);
-  uint32_t s = e4m3x2_rn_sat(va, vb) & 0x7f7fu;
-  if (a >= 0x7f800000u) s |= 0x7fu;
-  if (b >= 0x7f800000u) s |= 0x7f00u;
-  return s;
+// The scale bytes of two blocks of largest magnitudes a and b, b's in the second byte: E4M3(fp32(fp32(a / 6) * S)), NaN
+// (0x7F) where the block or S is not finite.
+__device__ __forceinline__ uint32_t fp4_block_scales(float a, float b, float tensor_scale, bool tiny) {
+  if (tiny) {  // the division of an infinity is one: made NaN, as it comes out below
+    a = a <= FLT_MAX ? a : __uint_as_float(0x7fc00000u);
+    b = b <= FLT_MAX ? b : __uint_as_float(0x7fc00000u);
+  }
+  return e4m3x2_rn_sat(__fmul_rn(fp4_div6(a, tiny), tensor_scale), __fmul_rn(fp4_div6(b, tiny), tensor_scale)) & 0x7f7fu;
 }
 
 // Value of a non-negative E4M3 byte, exactly; 0x7F is NaN.
@@ -44,13 +46,9 @@ __device__ __forceinline__ float fp4_scale_value(uint32_t b) {
 }
 
 // What a block's values are multiplied by: fp32(S / scale), at most the largest float (a zero stays one); 0 where
-// the scale is 0 or NaN.  A scale is one of eight significands times a power of two, so the quotients by the significands,
-// fp32(S / (1 + i / 8)) in `by`, are all that is divided: scaling them is exact (2688 / FLT_MAX / 448 is a normal float).
-__device__ __forceinline__ float fp4_quotient(int i, float tensor_scale) { return __fdiv_rn(tensor_scale, 1.0f + 0.125f * float(i)); }
-__device__ __forceinline__ float fp4_multiplier(uint32_t byte, const float* by) {
-  const uint32_t scale = __float_as_uint(fp4_scale_value(byte));
-  const float f = by[(scale >> 20) & 7u] * __uint_as_float((254u << 23) - (scale & 0x7f800000u));
-  return byte == 0u || byte == 0x7fu ? 0.0f : fminf(f, FLT_MAX);
+// the scale is 0 or NaN.
+__device__ __forceinline__ float fp4_multiplier(uint32_t byte, float tensor_scale) {
+  return byte == 0u || byte == 0x7fu ? 0.0f : fminf(__fdiv_rn(tensor_scale, fp4_scale_value(byte)), FLT_MAX);
 }
 
 // Eight values to E2M1 codes (nearest-even, saturating at 6), the first in the lowest four bits.
@@ -65,6 +63,18 @@ __device__ __forceinline__ uint32_t fp4_codes(const float (&v)[8]) {
       : "=r"(r)
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
+}
+
+// Eight E2M1 codes as pairs of F16 values, the first in the low half of r[0].
+__device__ __forceinline__ void fp4_values(uint32_t codes, uint32_t (&r)[4]) {
+  asm("{ .reg .b8 a, b, c, d;\n"
+      "mov.b32 {a, b, c, d}, %4;\n"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n"
+      "cvt.rn.f16x2.e2m1x2 %3, d; }"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(codes));
 }
 
 // What a product's sums are multiplied by: (1 / Sa) (1 / Sb), in two steps where it is too small to be one number.

@@ -129,13 +129,14 @@ __device__ __forceinline__ void join8(const uint32_t (&own)[8], int lane_mask, u
 template <class T, bool kRow, bool kCol>
 __global__ void __launch_bounds__(kThreads, T::kBytes == 2 ? 3 : 2) k_fp4_quantize(const __grid_constant__ Fp4QuantizeParams p) {
   constexpr int W = Eight<T>::W;
-  __shared__ float s_by[8];
+  __shared__ float s_mult[128];  // by scale byte: a read of it for eight operations of arithmetic
   __shared__ __align__(16) uint8_t s_scale[2][1024];
   __shared__ __align__(16) uint32_t s_col[kTile][17];
   grid_dependency_sync();
-  const float S = fp4_tensor_scale(*p.amax);
+  const float G = *p.amax, S = fp4_tensor_scale(G);
+  const bool tiny = fp4_tiny(G), bad = isnan(S);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (t < 8) s_by[t] = fp4_quotient(t, S);
+  if (t < 128) s_mult[t] = fp4_multiplier(uint32_t(t), S);
   const uint32_t tiles_c = uint32_t((p.cols + kTile - 1) / kTile);
   const uint32_t rb = blockIdx.x / tiles_c, cb = blockIdx.x - rb * tiles_c;
   const int r8 = warp * 16 + (lane >> 4) * 8, c8 = (lane & 15) * 8;
@@ -169,19 +170,18 @@ __global__ void __launch_bounds__(kThreads, T::kBytes == 2 ? 3 : 2) k_fp4_quanti
   if constexpr (kRow) {
     uint32_t m[8];
     join8<T>(rm, 1, m);
-    // blocks of columns past the last hold zeros, and so do rows: their scales are zero too, unless S is NaN
+    // blocks past the last column or row hold zeros: their scales are zero too, unless S is NaN
     const bool some = (col & ~int64_t(15)) < p.cols;
     uint8_t* q = p.q_r + row * p.ld_r + (col >> 1);
     uint8_t* at = &s_scale[0][(c8 >> 6) * 512 + (r8 & 31) * 16 + (r8 >> 5) * 4 + ((c8 >> 4) & 3)];  // block c8 / 16 of row r8
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      uint32_t s2 = fp4_block_scales(m[i], m[i + 1], S);
-      if (!some || i >= left) s2 = 0;
-      else if (i + 1 >= left) s2 &= 0xffu;
+      uint32_t s2 = fp4_block_scales(__uint_as_float(m[i]), __uint_as_float(m[i + 1]), S, tiny);
+      if (bad) s2 = !some || i >= left ? 0 : (i + 1 >= left ? s2 & 0xffu : s2);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t s = s2 >> (8 * h) & 0xffu;
-        const float f = fp4_multiplier(s, s_by);
+        const float f = s_mult[s];
         float y[8];
 #pragma unroll
         for (int k = 0; k < 8; k += 2) mul2_rn(v[i + h].get(k), v[i + h].get(k + 1), f, f, y[k], y[k + 1]);
@@ -210,13 +210,12 @@ __global__ void __launch_bounds__(kThreads, T::kBytes == 2 ? 3 : 2) k_fp4_quanti
     uint32_t* turned = &s_col[c8][(r8 >> 3) ^ ((c8 >> 5) << 1)];
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
-      uint32_t s2 = fp4_block_scales(m[k], m[k + 1], S);
-      if (!some || k >= n) s2 = 0;
-      else if (k + 1 >= n) s2 &= 0xffu;
+      uint32_t s2 = fp4_block_scales(__uint_as_float(m[k]), __uint_as_float(m[k + 1]), S, tiny);
+      if (bad) s2 = !some || k >= n ? 0 : (k + 1 >= n ? s2 & 0xffu : s2);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t s = s2 >> (8 * h) & 0xffu;
-        const float f = fp4_multiplier(s, s_by);
+        const float f = s_mult[s];
         float y[8];
 #pragma unroll
         for (int i = 0; i < 8; i += 2) mul2_rn(v[i].get(k + h), v[i + 1].get(k + h), f, f, y[i], y[i + 1]);
@@ -282,14 +281,20 @@ __global__ void __launch_bounds__(kThreads) k_fp4_restore(const __grid_constant_
     for (int k = 0; k < 8; ++k)
       if (2 * k < n) w[k >> 2] |= uint32_t(q[k]) << (8 * (k & 3));
   }
-  const float s = n == 0 ? 0.0f : fp4_scale_value(p.s[scale_at(row, b, scale_tile_cols(nb))] & 0x7fu);
+  uint32_t s = 0;  // the scale as two F16
+  if (n != 0) {
+    const uint32_t byte = p.s[scale_at(row, b, scale_tile_cols(nb))] & 0x7fu;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<uint16_t>(byte | byte << 8)));
+  }
+  // code times scale is exact in F16 (six bits, from 2^-10 to 2688)
+  uint32_t h[8];
+  fp4_values(w[0], reinterpret_cast<uint32_t(&)[4]>(h[0]));
+  fp4_values(w[1], reinterpret_cast<uint32_t(&)[4]>(h[4]));
   float v[16];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    uint32_t h;
-    asm("{ .reg .b8 c; cvt.u8.u32 c, %1; cvt.rn.f16x2.e2m1x2 %0, c; }" : "=r"(h) : "r"(w[k >> 2] >> (8 * (k & 3)) & 0xffu));
-    mul2_rn(f16_lo(h), f16_hi(h), s, s, v[2 * k], v[2 * k + 1]);  // exact
-    mul2_rn(v[2 * k], v[2 * k + 1], r, r, v[2 * k], v[2 * k + 1]);
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[k]) : "r"(s));
+    mul2_rn(f16_lo(h[k]), f16_hi(h[k]), r, r, v[2 * k], v[2 * k + 1]);
   }
   uint32_t o[4 * T::kBytes];
 #pragma unroll
