@@ -127,6 +127,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_fp4_g
           }
         }
       }
+      // Neither CTA leaves before the other one's last arrivals have come in.
+      for (int i = 0; i < q.stages && *gave_up == 0; ++i) {
+        tc::mbar_wait(empty + 8 * s, phase, gave_up);
+        if (++s == q.stages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
       if (*gave_up != 0 && rank == 0) tc::settle_copies(full, uint32_t(q.stages), issued);
     }
   } else if (warp == 1) {

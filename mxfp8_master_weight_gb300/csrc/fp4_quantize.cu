@@ -55,10 +55,16 @@ __device__ __forceinline__ Eight<T> load8(const char* p, int n, bool vec) {
   return v;
 }
 
-// Maxima of |x| as bit patterns, which order as the values do, NaN above infinity; BF16 keeps two to a word.
+// Maxima of |x|; BF16 keeps two to a word, whose signs mean nothing.  A NaN stays one.
 template <class T>
-__device__ __forceinline__ uint32_t max_bits(uint32_t a, uint32_t b) {
-  if constexpr (T::kBytes == 4) return max(a, b); else return __vmaxu2(a, b);
+__device__ __forceinline__ uint32_t max_abs(uint32_t m, uint32_t w) {
+  if constexpr (T::kBytes == 4) {
+    return max(m, w & 0x7fffffffu);
+  } else {
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(w));
+    return r;
+  }
 }
 
 // ------------------------------------------------------------------------------ largest magnitude
@@ -86,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) k_tensor_amax(const __grid_constant_
 #pragma unroll
     for (int l = 0; l < kAmaxLoads; ++l)
 #pragma unroll
-      for (int k = 0; k < Eight<T>::W; ++k) m = max_bits<T>(m, v[l].w[k] & T::kAbsMask);
+      for (int k = 0; k < Eight<T>::W; ++k) m = max_abs<T>(m, v[l].w[k]);
     row += step_row;
     part += step_part;
     if (part >= per_row) {
@@ -94,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) k_tensor_amax(const __grid_constant_
       ++row;
     }
   }
-  if constexpr (T::kBytes == 2) m = max(m << 16, m & 0xffff0000u);
+  if constexpr (T::kBytes == 2) m = max(m << 16 & 0x7fff0000u, m & 0x7fff0000u);
   m = __reduce_max_sync(kFullMask, m);
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
@@ -127,7 +133,7 @@ __device__ __forceinline__ void join8(const uint32_t (&own)[8], int lane_mask, u
 }
 
 template <class T, bool kRow, bool kCol>
-__global__ void __launch_bounds__(kThreads, T::kBytes == 2 ? 3 : 2) k_fp4_quantize(const __grid_constant__ Fp4QuantizeParams p) {
+__global__ void __launch_bounds__(kThreads, T::kBytes == 4 ? 2 : (kRow && kCol ? 3 : 4)) k_fp4_quantize(const __grid_constant__ Fp4QuantizeParams p) {
   constexpr int W = Eight<T>::W;
   __shared__ float s_mult[128];  // by scale byte: a read of it for eight operations of arithmetic
   __shared__ __align__(16) uint8_t s_scale[2][1024];
@@ -160,11 +166,10 @@ __global__ void __launch_bounds__(kThreads, T::kBytes == 2 ? 3 : 2) k_fp4_quanti
     uint32_t m = 0;
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-      const uint32_t a = v[i].w[k] & T::kAbsMask;
-      m = max_bits<T>(m, a);
-      cm[k] = max_bits<T>(cm[k], a);
+      m = max_abs<T>(m, v[i].w[k]);
+      cm[k] = max_abs<T>(cm[k], v[i].w[k]);
     }
-    rm[i] = T::kBytes == 4 ? m : max(m & 0xffffu, m >> 16);
+    rm[i] = T::kBytes == 4 ? m : max(m & 0x7fffu, m >> 16 & 0x7fffu);
   }
   __syncthreads();
   if constexpr (kRow) {
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, T::kBytes == 2 ? 3 : 2) k_fp4_quanti
   if constexpr (kCol) {
     uint32_t own[8], m[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) own[k] = T::kBytes == 4 ? cm[k % W] : (cm[k >> 1] >> (16 * (k & 1))) & 0xffffu;
+    for (int k = 0; k < 8; ++k) own[k] = T::kBytes == 4 ? cm[k % W] : (cm[k >> 1] >> (16 * (k & 1))) & 0x7fffu;
     join8<T>(own, 16, m);
     const bool some = (row & ~int64_t(15)) < p.rows;
     uint8_t* at = &s_scale[1][(warp >> 2) * 512 + (c8 & 31) * 16 + (c8 >> 5) * 4 + (warp & 3)];  // block `warp` of transposed row c8
@@ -257,63 +262,55 @@ __global__ void __launch_bounds__(kThreads, T::kBytes == 2 ? 3 : 2) k_fp4_quanti
 }
 
 // ------------------------------------------------------------------------------ values
-// A thread restores a block of 16: 8 bytes of codes and one scale; a warp 512 columns of a row.  Rows that start anywhere
-// go through the warp's shared memory and out as 32-bit words aligned in the output, neighbours across the lanes (BF16: a lone
-// value at either end where the row starts between words).
+// A thread restores blocks of 16, 8 bytes of codes and one scale each, a warp 512 columns of kRestoreRows rows, whose loads
+// are all under way at once.  Rows that start anywhere go through the warp's shared memory and out as 32-bit words aligned in
+// the output, neighbours across the lanes (BF16: a lone value at either end where the row starts between words).
+constexpr int kRestoreRows = 2;
 template <class T>
-__global__ void __launch_bounds__(kThreads) k_fp4_restore(const __grid_constant__ Fp4RestoreParams p) {
-  grid_dependency_sync();
-  const float r = __frcp_rn(fp4_tensor_scale(*p.amax));
-  const int64_t nb = (p.cols + 15) / 16;
-  const uint32_t per_row = uint32_t((nb + 31) / 32), lane = threadIdx.x & 31;
-  const uint32_t rows8 = blockIdx.x / per_row, part = blockIdx.x - rows8 * per_row;
-  const int64_t row = int64_t(rows8) * 8 + (threadIdx.x >> 5), b = int64_t(part) * 32 + lane;
-  if (row >= p.rows) return;  // whole warps
+struct RestoreLine {
+  static constexpr int kWords = 4 * T::kBytes;  // of a block's values
+  uint32_t w[32 * (kWords + 1)];                // a word apart, against bank conflicts
+};
+template <class T>
+__device__ __forceinline__ void restore_row(const Fp4RestoreParams& p, const uint2& codes, uint32_t byte, float r, int64_t row,
+                                            uint32_t part, RestoreLine<T>* s_line) {
+  constexpr int kWords = RestoreLine<T>::kWords;
+  const uint32_t lane = threadIdx.x & 31;
+  const int64_t b = int64_t(part) * 32 + lane;
   const int n = p.cols - 16 * b >= 16 ? 16 : (p.cols > 16 * b ? int(p.cols - 16 * b) : 0);
-  const uint8_t* q = p.q + row * p.ld_q + 8 * b;
-  uint32_t w[2] = {0, 0};
-  if (p.vec_q && n == 16) {
-    const uint2 c = *reinterpret_cast<const uint2*>(q);
-    w[0] = c.x;
-    w[1] = c.y;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (2 * k < n) w[k >> 2] |= uint32_t(q[k]) << (8 * (k & 3));
-  }
-  uint32_t s = 0;  // the scale as two F16
-  if (n != 0) {
-    const uint32_t byte = p.s[scale_at(row, b, scale_tile_cols(nb))] & 0x7fu;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<uint16_t>(byte | byte << 8)));
-  }
-  // code times scale is exact in F16 (six bits, from 2^-10 to 2688)
+  uint32_t s;  // the scale as two F16: code times scale is exact there (six bits, from 2^-10 to 2688)
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<uint16_t>(byte | byte << 8)));
   uint32_t h[8];
-  fp4_values(w[0], reinterpret_cast<uint32_t(&)[4]>(h[0]));
-  fp4_values(w[1], reinterpret_cast<uint32_t(&)[4]>(h[4]));
+  fp4_values(codes.x, reinterpret_cast<uint32_t(&)[4]>(h[0]));
+  fp4_values(codes.y, reinterpret_cast<uint32_t(&)[4]>(h[4]));
   float v[16];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[k]) : "r"(s));
     mul2_rn(f16_lo(h[k]), f16_hi(h[k]), r, r, v[2 * k], v[2 * k + 1]);
   }
-  uint32_t o[4 * T::kBytes];
+  uint32_t o[kWords];
 #pragma unroll
-  for (int k = 0; k < 4 * T::kBytes; ++k) o[k] = T::kBytes == 4 ? __float_as_uint(v[k % 16]) : bf16x2_rn(v[2 * k % 16], v[(2 * k + 1) % 16]);
+  for (int k = 0; k < kWords; ++k) o[k] = T::kBytes == 4 ? __float_as_uint(v[k % 16]) : bf16x2_rn(v[2 * k % 16], v[(2 * k + 1) % 16]);
   char* out = static_cast<char*>(p.out) + (row * p.ld_o + 16 * b) * T::kBytes;
   if (p.vec_out) {
-    if (n == 16) {
+    if (n == 16 && p.vec_out == 2) {
 #pragma unroll
-      for (int k = 0; k < 4 * T::kBytes; k += 4) *reinterpret_cast<uint4*>(out + 4 * k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+      for (int k = 0; k < kWords; k += 8)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + 4 * k), "r"(o[k]), "r"(o[k + 1]),
+                     "r"(o[k + 2]), "r"(o[k + 3]), "r"(o[k + 4]), "r"(o[k + 5]), "r"(o[k + 6]), "r"(o[k + 7])
+                     : "memory");
+    } else if (n == 16) {
+#pragma unroll
+      for (int k = 0; k < kWords; k += 4) *reinterpret_cast<uint4*>(out + 4 * k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
     } else {
 #pragma unroll
       for (int k = 0; k < 16; ++k)
-        if (k < n) store_bits<T>(out, k, T::kBytes == 4 ? o[k % (4 * T::kBytes)] : o[k >> 1] >> (16 * (k & 1)));
+        if (k < n) store_bits<T>(out, k, T::kBytes == 4 ? o[k % kWords] : o[k >> 1] >> (16 * (k & 1)));
     }
     return;
   }
-  __shared__ __align__(16) uint32_t s_line[kThreads / 32][32 * (4 * T::kBytes + 1)];  // a word apart, against bank conflicts
-  uint32_t* line = s_line[threadIdx.x >> 5];
-  constexpr int kWords = 4 * T::kBytes;
+  uint32_t* line = s_line[threadIdx.x >> 5].w;
 #pragma unroll
   for (int k = 0; k < kWords; ++k) line[lane * (kWords + 1) + k] = o[k];
   __syncwarp();
@@ -332,6 +329,42 @@ __global__ void __launch_bounds__(kThreads) k_fp4_restore(const __grid_constant_
     if (lane == 0 && head) ends[0] = uint16_t(half(0));
     if (lane == 1 && ((width - head) & 1)) ends[width - 1] = uint16_t(half(width - 1));
   }
+  __syncwarp();
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_fp4_restore(const __grid_constant__ Fp4RestoreParams p) {
+  __shared__ RestoreLine<T> s_line[kThreads / 32];
+  grid_dependency_sync();
+  const int64_t nb = (p.cols + 15) / 16, tile_cols = scale_tile_cols(nb);
+  const uint32_t per_row = uint32_t((nb + 31) / 32), lane = threadIdx.x & 31;
+  const uint32_t rows = blockIdx.x / per_row, part = blockIdx.x - rows * per_row;
+  const int64_t row = (int64_t(rows) * (kThreads / 32) + (threadIdx.x >> 5)) * kRestoreRows, b = int64_t(part) * 32 + lane;
+  if (row >= p.rows) return;  // whole warps
+  const int n = p.cols - 16 * b >= 16 ? 16 : (p.cols > 16 * b ? int(p.cols - 16 * b) : 0);
+  uint2 codes[kRestoreRows];
+  uint32_t byte[kRestoreRows];
+#pragma unroll
+  for (int i = 0; i < kRestoreRows; ++i) {
+    codes[i] = make_uint2(0, 0);
+    byte[i] = 0;
+    if (row + i >= p.rows || n == 0) continue;
+    const uint8_t* q = p.q + (row + i) * p.ld_q + 8 * b;
+    byte[i] = p.s[scale_at(row + i, b, tile_cols)] & 0x7fu;
+    if (p.vec_q && n == 16) {
+      codes[i] = *reinterpret_cast<const uint2*>(q);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t two = 2 * k < n ? uint32_t(q[k]) << (8 * (k & 3)) : 0u;
+        if (k < 4) codes[i].x |= two; else codes[i].y |= two;
+      }
+    }
+  }
+  const float r = __frcp_rn(fp4_tensor_scale(*p.amax));
+#pragma unroll
+  for (int i = 0; i < kRestoreRows; ++i)
+    if (row + i < p.rows) restore_row<T>(p, codes[i], byte[i], r, row + i, part, s_line);
 }
 
 // ------------------------------------------------------------------------------ weights
@@ -411,7 +444,8 @@ cudaError_t launch_fp4_quantize(const Fp4QuantizeParams& p, int dtype, cudaStrea
 
 cudaError_t launch_fp4_restore(const Fp4RestoreParams& p, int dtype, cudaStream_t stream) {
   const int64_t nb = (p.cols + 15) / 16;
-  const dim3 grid(unsigned((p.rows + 7) / 8 * ((nb + 31) / 32)));
+  constexpr int kRows = kThreads / 32 * kRestoreRows;
+  const dim3 grid(unsigned((p.rows + kRows - 1) / kRows * ((nb + 31) / 32)));
   return dtype == 0 ? launch_kernel(k_fp4_restore<F32T>, grid, dim3(kThreads), 0, stream, p)
                     : launch_kernel(k_fp4_restore<BF16T>, grid, dim3(kThreads), 0, stream, p);
 }

@@ -90,7 +90,7 @@ struct Fp4RestoreParams {
   const float* amax;
   void* out;
   int64_t ld_o;
-  int32_t vec_q, vec_out;  // 8-byte loads, 16-byte stores
+  int32_t vec_q, vec_out;  // 8-byte loads; 16- (1) or 32-byte (2) stores
 };
 
 struct Fp4LayOutParams {

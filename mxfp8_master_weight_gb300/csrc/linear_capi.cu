@@ -578,7 +578,8 @@ int nvfp4_restore(const mxfp8_tensor* codes, const mxfp8_tensor* scale, const mx
   p.cols = cols;
   p.out = output->data;
   p.vec_q = aligned(p.q, p.ld_q, 1, 8);
-  p.vec_out = aligned(p.out, p.ld_o, elem_bytes(output->dtype), 16);
+  const int64_t eb = elem_bytes(output->dtype);
+  p.vec_out = aligned(p.out, p.ld_o, eb, 32) ? 2 : aligned(p.out, p.ld_o, eb, 16);
   return cuda_status(mxfp8::launch_fp4_restore(p, dtype_index(output->dtype), static_cast<cudaStream_t>(stream)),
                      "NVFP4 restore launch");
 }
