@@ -12,6 +12,9 @@ Cases (seeded synthetic inputs of the workloads module):
   linear      a training step of a 4096x4096 linear layer behind a layer norm, 4096 tokens
               (tokens divided by --scale): weight cast, forward and backward pass with 8-bit
               activation checkpoints
+  rms_linear  a training step of a 4096x4096 linear layer behind an RMS norm in a residual stream, 4096
+              tokens (divided by --scale): weight cast, the norm's sum, values and 8-bit codes, products
+  nvfp4_linear  the same on NVFP4 weights: the norm's largest magnitude, 4-bit activations and products
   small       the 160x96 FP32 weight (config 1), one full fragment: amax -> scales -> cast
               (a launch of five tiles: the split kernels)
 
@@ -120,8 +123,34 @@ def case_linear(dev, scale):
     return run
 
 
+def _rms_linear(dev, scale, weights):
+    w = wl.cfg3_square()
+    tokens = 4096 // scale
+    layer = linear.RMSNormLinear(tokens, w.cols, w.rows, dev, weights=weights)
+    master = torch.from_numpy(w.data).to(dev)
+    g = torch.Generator(device=dev).manual_seed(0)
+    x, residual = (torch.randn(tokens, w.cols, generator=g, device=dev).bfloat16() for _ in range(2))
+    dy, ds = ((torch.randn(tokens, n, generator=g, device=dev) * 1e-3).bfloat16() for n in (w.rows, w.cols))
+
+    def run():
+        layer.refresh([master])
+        layer.forward(x, residual)
+        layer.backward(dy, ds)
+    run.check = layer.check
+    return run
+
+
+def case_rms_linear(dev, scale):
+    return _rms_linear(dev, scale, "mxfp8")
+
+
+def case_nvfp4_linear(dev, scale):
+    return _rms_linear(dev, scale, "nvfp4")
+
+
 CASES = {"step": case_step, "one_pass": case_one_pass, "sharded": case_sharded, "nvfp4": case_nvfp4,
-         "small": case_small, "linear": case_linear}
+         "small": case_small, "linear": case_linear, "rms_linear": case_rms_linear,
+         "nvfp4_linear": case_nvfp4_linear}
 
 
 def main(argv=None):
