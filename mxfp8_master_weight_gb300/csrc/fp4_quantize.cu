@@ -132,6 +132,29 @@ __device__ __forceinline__ void join8(const uint32_t (&own)[8], int lane_mask, u
   }
 }
 
+// The tile's transposed rows: word w of row j at w ^ (j / 32 * 2), 64 bytes each.
+__device__ __forceinline__ void store_turned(const uint32_t (&s_col)[kTile][17], uint8_t* out, int64_t ld, bool vec, uint32_t rb,
+                                             uint32_t cb, int64_t rows, int64_t cols) {
+  const int64_t rows_left = rows - int64_t(rb) * kTile;
+  const int width = rows_left < kTile ? int(rows_left + 1) / 2 : kTile / 2;  // bytes of a transposed row
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int j = (int(threadIdx.x) >> 2) + 64 * h, u = threadIdx.x & 3;
+    if (int64_t(cb) * kTile + j >= cols) continue;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = s_col[j][(4 * u + k) ^ ((j >> 5) << 1)];
+    uint8_t* q = out + (int64_t(cb) * kTile + j) * ld + int64_t(rb) * (kTile / 2) + 16 * u;
+    if (vec && 16 * u + 16 <= width) {
+      *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (16 * u + k < width) q[k] = uint8_t(w[k >> 2] >> (8 * (k & 3)));
+    }
+  }
+}
+
 template <class T, bool kRow, bool kCol>
 __global__ void __launch_bounds__(kThreads, T::kBytes == 4 ? 2 : (kRow && kCol ? 3 : 4)) k_fp4_quantize(const __grid_constant__ Fp4QuantizeParams p) {
   constexpr int W = Eight<T>::W;
@@ -151,12 +174,28 @@ __global__ void __launch_bounds__(kThreads, T::kBytes == 4 ? 2 : (kRow && kCol ?
   const int left = p.rows - row >= 8 ? 8 : (p.rows > row ? int(p.rows - row) : 0);
   Eight<T> v[8];
   const char* src = static_cast<const char*>(p.in) + (row * p.ld + col) * T::kBytes;
-  if (left == 8) {
+  const int64_t pitch = p.ld * T::kBytes;
+  // BF16 rows that start anywhere are read by 32-bit words, shifted by half a word where they start inside one; words
+  // that would reach past the matrix are left to the loads by the element.
+  const bool words = T::kBytes == 2 && !p.vec_in && n == 8 && left == 8 && (row > 0 || col > 0) && (row + 8 < p.rows || col + 8 < p.cols);
+  if (words) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = load8<T>(src + i * p.ld * T::kBytes, n, p.vec_in);
+    for (int i = 0; i < 8; ++i) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(src + i * pitch);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(at & ~uintptr_t(3));
+      uint32_t raw[5];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) raw[k] = w[k];
+      raw[4] = w[at & 2 ? 4 : 3];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[i].w[k % W] = __funnelshift_r(raw[k], raw[k + 1], at & 2 ? 16 : 0);
+    }
+  } else if (left == 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = load8<T>(src + i * pitch, n, p.vec_in);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = load8<T>(src + i * p.ld * T::kBytes, i < left ? n : 0, p.vec_in);
+    for (int i = 0; i < 8; ++i) v[i] = load8<T>(src + i * pitch, i < left ? n : 0, p.vec_in);
   }
   uint32_t rm[8], cm[W];
 #pragma unroll
@@ -240,24 +279,7 @@ __global__ void __launch_bounds__(kThreads, T::kBytes == 4 ? 2 : (kRow && kCol ?
       *reinterpret_cast<uint4*>(s + (r128 * tile_cols + at) * 512 + (unit & 31) * 16) = *reinterpret_cast<const uint4*>(&s_scale[which][unit * 16]);
   }
   if constexpr (kCol) {
-    const int64_t rows_left = p.rows - int64_t(rb) * kTile;
-    const int width = rows_left < kTile ? int(rows_left + 1) / 2 : kTile / 2;  // bytes of a transposed row
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = (t >> 2) + 64 * h, u = t & 3;
-      if (int64_t(cb) * kTile + j >= p.cols) continue;
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = s_col[j][(4 * u + k) ^ ((j >> 5) << 1)];
-      uint8_t* q = p.q_c + (int64_t(cb) * kTile + j) * p.ld_c + int64_t(rb) * (kTile / 2) + 16 * u;
-      if (p.vec_c && 16 * u + 16 <= width) {
-        *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (16 * u + k < width) q[k] = uint8_t(w[k >> 2] >> (8 * (k & 3)));
-      }
-    }
+    store_turned(s_col, p.q_c, p.ld_c, p.vec_c, rb, cb, p.rows, p.cols);
   }
 }
 
@@ -368,31 +390,44 @@ __global__ void __launch_bounds__(kThreads) k_fp4_restore(const __grid_constant_
 }
 
 // ------------------------------------------------------------------------------ weights
-// Codes [rows][cols] as they lie densely to rows with the contraction along them: as they are, or (kTurn) transposed.
-// The same tile and threads as the quantisation's; once per refresh of a weight, so loads are by the byte.
+// Codes [rows][cols] as they lie densely to rows with the contraction along them: as they are, or (kTurn) transposed.  The
+// tile and the threads are the quantisation's.  Dense rows of a width that is no multiple of 8 start on any byte: their eight
+// codes are put together from bytes.
+__device__ __forceinline__ uint32_t load_codes4(const uint8_t* q, int bytes, bool vec) {
+  if (vec && bytes == 4) return *reinterpret_cast<const uint32_t*>(q);
+  uint32_t w = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k < bytes) w |= uint32_t(q[k]) << (8 * k);
+  return w;
+}
+
 template <bool kTurn>
 __global__ void __launch_bounds__(kThreads) k_fp4_lay_out(const __grid_constant__ Fp4LayOutParams p) {
   __shared__ __align__(16) uint32_t s_col[kTile][17];
   grid_dependency_sync();
-  const int64_t tiles_c = (p.cols + kTile - 1) / kTile;
-  const int64_t rb = blockIdx.x / tiles_c, cb = blockIdx.x - rb * tiles_c;
+  const uint32_t tiles_c = uint32_t((p.cols + kTile - 1) / kTile);
+  const uint32_t rb = blockIdx.x / tiles_c, cb = blockIdx.x - rb * tiles_c;
   const int t = threadIdx.x, lane = t & 31, r8 = (t >> 5) * 16 + (lane >> 4) * 8, c8 = (lane & 15) * 8;
-  const int64_t row = rb * kTile + r8, col = cb * kTile + c8;
+  const int64_t row = int64_t(rb) * kTile + r8, col = int64_t(cb) * kTile + c8;
+  const int bytes = p.cols - col >= 8 ? 4 : (p.cols > col ? int(p.cols - col) / 2 : 0);
   uint32_t w[8];  // eight codes of eight rows
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    w[i] = 0;
-    if (row + i >= p.rows) continue;
+  for (int i = 0; i < 8; ++i) w[i] = row + i < p.rows ? load_codes4(p.q + (row + i) * p.ld_q + (col >> 1), bytes, p.vec_q) : 0u;
+  if constexpr (!kTurn) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (col + 2 * k < p.cols) w[i] |= uint32_t(p.q[(row + i) * p.ld_q + (col >> 1) + k]) << (8 * k);
-    if constexpr (!kTurn) {
+    for (int i = 0; i < 8; ++i) {
+      uint8_t* o = p.out + (row + i) * p.ld_o + (col >> 1);
+      if (row + i >= p.rows) continue;
+      if (p.vec_out && bytes == 4) {
+        *reinterpret_cast<uint32_t*>(o) = w[i];
+      } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (col + 2 * k < p.cols) p.out[(row + i) * p.ld_o + (col >> 1) + k] = uint8_t(w[i] >> (8 * k));
+        for (int k = 0; k < 4; ++k)
+          if (k < bytes) o[k] = uint8_t(w[i] >> (8 * k));
+      }
     }
-  }
-  if constexpr (kTurn) {
+  } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       uint32_t q = 0;
@@ -401,16 +436,7 @@ __global__ void __launch_bounds__(kThreads) k_fp4_lay_out(const __grid_constant_
       s_col[c8 + k][(r8 >> 3) ^ ((c8 >> 5) << 1)] = q;
     }
     __syncthreads();
-    const int width = p.rows - rb * kTile < kTile ? int(p.rows - rb * kTile + 1) / 2 : kTile / 2;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = (t >> 2) + 64 * h, u = t & 3;
-      if (cb * kTile + j >= p.cols) continue;
-      uint8_t* o = p.out + (cb * kTile + j) * p.ld_o + rb * (kTile / 2) + 16 * u;
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (16 * u + k < width) o[k] = uint8_t(s_col[j][(4 * u + (k >> 2)) ^ ((j >> 5) << 1)] >> (8 * (k & 3)));
-    }
+    store_turned(s_col, p.out, p.ld_o, p.vec_out, rb, cb, p.rows, p.cols);
   }
 }
 

@@ -99,6 +99,7 @@ struct Fp4LayOutParams {
   uint8_t* out;
   int64_t ld_o;
   int32_t transpose;
+  int32_t vec_q, vec_out;  // 4-byte loads; 4-byte (transposed: 16-byte) stores
 };
 
 // A product's operands are rowwise, `ld` bytes apart and 16-byte aligned, block 16.

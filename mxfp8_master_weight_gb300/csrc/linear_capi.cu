@@ -603,6 +603,8 @@ int nvfp4_lay_out(const mxfp8_tensor* codes, mxfp8_tensor* output, int64_t rows,
   p.rows = rows;
   p.cols = cols;
   p.transpose = transpose;
+  p.vec_q = aligned(p.q, p.ld_q, 1, 4);
+  p.vec_out = aligned(p.out, p.ld_o, 1, transpose ? 16 : 4);
   return cuda_status(mxfp8::launch_fp4_lay_out(p, static_cast<cudaStream_t>(stream)), "NVFP4 layout launch");
 }
 
