@@ -403,22 +403,30 @@ class Prepared:
     not move between calls (re-prepare after reallocating).
     """
 
-    __slots__ = ("fn", "args", "handles", "tensors", "device")
+    __slots__ = ("fn", "types", "args", "handles", "tensors", "device")
 
     def __init__(self, fn_name, handles, scalars, tensors, job_array=None):
-        self.fn = getattr(_capi.load(), fn_name)
+        lib = _capi.load()
+        # A function object of its own, without argtypes, called with arguments that have their C types already: ctypes
+        # then converts nothing per call (1.9 us against 0.7 for a call of seven arguments).
+        self.fn, self.types = lib[fn_name], getattr(lib, fn_name).argtypes
         self.handles = handles
         if job_array is not None:  # batched entry: (job array, count)
-            self.args = (job_array, int(scalars[0]))
+            self.bind(job_array, int(scalars[0]))
         else:
-            self.args = tuple(ctypes.byref(h) for h in handles) + tuple(
-                v if isinstance(v, float) else int(v) for v in scalars)
+            self.bind(*(ctypes.byref(h) for h in handles), *(v if isinstance(v, float) else int(v) for v in scalars))
         self.tensors = tensors
         self.device = _device_of(*tensors)
+
+    def bind(self, *args) -> None:
+        """The call's arguments but the stream, numbers in the C types of the entry point."""
+        self.args = tuple(t(a) if isinstance(a, (int, float)) else a for a, t in zip(args, self.types))
 
     def call(self, stream=None) -> None:
         if stream is None or hasattr(stream, "cuda_stream"):
             stream = _stream(stream, self.tensors[0] if self.tensors else None)
+        elif not isinstance(stream, ctypes.c_void_p):
+            stream = ctypes.c_void_p(stream)
         rc = self.fn(*self.args, stream)
         if rc != 0:
             _capi.check(rc)
@@ -472,7 +480,7 @@ def prepare_amax_max_reduce_update_scales(slots, reduced, jobs) -> Prepared:
     arr, keep = _scale_jobs(jobs)
     hs = [handle(slots, "slots"), handle(reduced, "reduced")]
     pr = Prepared("mxfp8_amax_max_reduce_update_scales", hs, (), keep + [slots, reduced])
-    pr.args = (ctypes.byref(hs[0]), ctypes.byref(hs[1]), arr, len(jobs))
+    pr.bind(ctypes.byref(hs[0]), ctypes.byref(hs[1]), arr, len(jobs))
     pr.handles = hs + [arr]
     return pr
 
@@ -482,7 +490,7 @@ def prepare_amax_max_reduce_update_scales_ranged(slots, reduced, jobs, slot_rang
     rng, nr = _ranges_array(slot_ranges)
     hs = [handle(slots, "slots"), handle(reduced, "reduced")]
     pr = Prepared("mxfp8_amax_max_reduce_update_scales_ranged", hs, (), keep + [slots, reduced])
-    pr.args = (ctypes.byref(hs[0]), ctypes.byref(hs[1]), arr, len(jobs), rng, nr)
+    pr.bind(ctypes.byref(hs[0]), ctypes.byref(hs[1]), arr, len(jobs), rng, nr)
     pr.handles = hs + [arr, rng]
     return pr
 

@@ -17,6 +17,7 @@
 #include "fp4_gemm.h"
 #include "gemm_impl.cuh"
 #include "gemm_maps.h"
+#include "status.h"
 
 namespace mxfp8 {
 namespace {
@@ -84,8 +85,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_fp4_g
     tc::mbar_init_fence();
     if (p.k > 0) {
       tc::prefetch_map(&q.a);
-      tc::prefetch_map(&q.b);
-      tc::prefetch_map(&q.b_half);
+      if (q.whole > 0) tc::prefetch_map(&q.b);
+      if (q.whole < q.units) tc::prefetch_map(&q.b_half);
       tc::prefetch_map(&q.sa);
       tc::prefetch_map(&q.sb);
     }
@@ -269,15 +270,6 @@ cudaError_t launch_fp4_gemm_pair(const Fp4GemmParams& f, unsigned* given_up, con
   q.given_up = given_up;
   const GemmParams& g = f.g;
   const int64_t bytes = (g.k + 1) / 2;
-  cudaError_t e = cudaSuccess;
-  if (g.k > 0) {
-    e = operand_map(g.a, bytes, 128, &q.a, what);
-    if (e == cudaSuccess) e = operand_map(g.b, bytes, 128, &q.b, what);
-    if (e == cudaSuccess) e = half_operand_map(g.b, bytes, &q.b_half, what);
-    if (e == cudaSuccess) e = scale_map(g.a, g.k, 1, &q.sa, what, 4);
-    if (e == cudaSuccess) e = scale_map(g.b, g.k, 2, &q.sb, what, 4);
-  }
-  if (e != cudaSuccess) return e;
   const int64_t tiles = ((g.m + 255) / 256) * ((g.n + 255) / 256);
   const int64_t pairs = dev.sms / 2, last = tiles % pairs;
   q.whole = last != 0 && 2 * last <= pairs ? tiles - last : tiles;
@@ -285,16 +277,26 @@ cudaError_t launch_fp4_gemm_pair(const Fp4GemmParams& f, unsigned* given_up, con
   q.b_bytes = q.whole == 0 ? kBoxBytes / 2 : kBoxBytes;
   const int fit = kStageRoom / (kBoxBytes + q.b_bytes + kScaleBytes);
   q.stages = fit < kMaxStages ? fit : kMaxStages;
+  cudaError_t e = cudaSuccess;
+  if (g.k > 0) {
+    e = operand_map(g.a, bytes, 128, &q.a, what);
+    if (e == cudaSuccess && q.whole > 0) e = operand_map(g.b, bytes, 128, &q.b, what);
+    if (e == cudaSuccess && q.whole < q.units) e = operand_map(g.b, bytes, 64, &q.b_half, what);
+    if (e == cudaSuccess) e = scale_map(g.a, g.k, 1, &q.sa, what, 4);
+    if (e == cudaSuccess) e = scale_map(g.b, g.k, 2, &q.sb, what, 4);
+  }
+  if (e != cudaSuccess) return e;
   const unsigned grid = 2 * unsigned(q.units < pairs ? q.units : pairs);
-  auto run = [&](auto kernel) {
-    const cudaError_t r = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<unsigned long long> told[3];
+  auto run = [&](auto kernel, std::atomic<unsigned long long>* done) {
+    const cudaError_t r = allow_smem(reinterpret_cast<const void*>(kernel), kSmem, dev.device, done);
     return r != cudaSuccess ? r : launch_kernel(kernel, dim3(grid), dim3(kThreads), kSmem, stream, q);
   };
   // A store through TMA ends a row on 16 bytes: it would write past one that ends elsewhere.
-  if (g.addend != nullptr || !g.vec_out || g.n % (g.out_f32 ? 4 : 8) != 0) return run(k_fp4_gemm_pair<kOutAny>);
+  if (g.addend != nullptr || !g.vec_out || g.n % (g.out_f32 ? 4 : 8) != 0) return run(k_fp4_gemm_pair<kOutAny>, &told[kOutAny]);
   e = output_map(g, &q.out, what);
   if (e != cudaSuccess) return e;
-  return g.out_f32 ? run(k_fp4_gemm_pair<kOutF32>) : run(k_fp4_gemm_pair<kOutBf16>);
+  return g.out_f32 ? run(k_fp4_gemm_pair<kOutF32>, &told[kOutF32]) : run(k_fp4_gemm_pair<kOutBf16>, &told[kOutBf16]);
 }
 
 }  // namespace mxfp8

@@ -12,6 +12,7 @@
 #include "fp4_gemm.h"
 #include "gemm_lines.cuh"
 #include "gemm_maps.h"
+#include "status.h"
 
 namespace mxfp8 {
 namespace {
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp4_gemm_split(const __grid_con
 }
 
 template <int NT>
-cudaError_t launch(const Fp4GemmParams& f, bool swapped, int split, unsigned* given_up, cudaStream_t stream, const char** what) {
+cudaError_t launch(const Fp4GemmParams& f, bool swapped, int split, unsigned* given_up, int device, cudaStream_t stream, const char** what) {
   SplitParams q{};
   q.f = f;
   q.given_up = given_up;
@@ -173,8 +174,8 @@ cudaError_t launch(const Fp4GemmParams& f, bool swapped, int split, unsigned* gi
   if (e == cudaSuccess) e = operand_map(g.b, (g.k + 1) / 2, NT, &q.b, what);
   if (e == cudaSuccess) e = scale_map(g.a, g.k, 1, &q.sa, what, 4);
   if (e == cudaSuccess) e = scale_map(g.b, g.k, 1, &q.sb, what, 4);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_fp4_gemm_split<NT>), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget);
+  static std::atomic<unsigned long long> done{0};
+  if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(k_fp4_gemm_split<NT>), kSmemBudget, device, &done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(((g.m + 127) / 128) * ((g.n + NT - 1) / NT) * split));
@@ -215,10 +216,10 @@ cudaError_t launch_fp4_gemm_split(const Fp4GemmParams& p, unsigned* given_up, co
   int split = 1;
   while (split < kMaxSplit && tiles * split * 2 <= (split == 4 ? eight : two) && nk >= split * 4) split *= 2;
   switch (nt) {
-    case 16: return launch<16>(f, swapped, split, given_up, stream, what);
-    case 32: return launch<32>(f, swapped, split, given_up, stream, what);
-    case 64: return launch<64>(f, swapped, split, given_up, stream, what);
-    default: return launch<128>(f, swapped, split, given_up, stream, what);
+    case 16: return launch<16>(f, swapped, split, given_up, dev.device, stream, what);
+    case 32: return launch<32>(f, swapped, split, given_up, dev.device, stream, what);
+    case 64: return launch<64>(f, swapped, split, given_up, dev.device, stream, what);
+    default: return launch<128>(f, swapped, split, given_up, dev.device, stream, what);
   }
 }
 

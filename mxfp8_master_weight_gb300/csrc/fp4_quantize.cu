@@ -343,10 +343,14 @@ __device__ __forceinline__ void restore_row(const Fp4RestoreParams& p, const uin
   if constexpr (T::kBytes == 4) {
     for (int i = int(lane); i < width; i += 32) reinterpret_cast<uint32_t*>(start)[i] = word(i);
   } else {
-    auto half = [&](int i) { return word(i >> 1) >> (16 * (i & 1)) & 0xffffu; };
     const int head = int(reinterpret_cast<uintptr_t>(start) >> 1) & 1, pairs = (width - head) / 2;
     uint32_t* words = reinterpret_cast<uint32_t*>(start + 2 * head);
-    for (int i = int(lane); i < pairs; i += 32) words[i] = half(2 * i + head) | half(2 * i + 1 + head) << 16;
+    if (head) {
+      for (int i = int(lane); i < pairs; i += 32) words[i] = __funnelshift_r(word(i), 2 * i + 2 < width ? word(i + 1) : 0u, 16);
+    } else {
+      for (int i = int(lane); i < pairs; i += 32) words[i] = word(i);
+    }
+    auto half = [&](int i) { return word(i >> 1) >> (16 * (i & 1)) & 0xffffu; };
     uint16_t* ends = reinterpret_cast<uint16_t*>(start);
     if (lane == 0 && head) ends[0] = uint16_t(half(0));
     if (lane == 1 && ((width - head) & 1)) ends[width - 1] = uint16_t(half(width - 1));

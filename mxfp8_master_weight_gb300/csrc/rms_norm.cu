@@ -638,7 +638,8 @@ template <class T, bool kVec, int TH, int NV, int BLOCKS>
 cudaError_t forward_ring(const RmsForwardParams& p, int wdtype, const DeviceInfo& dev, unsigned* given_up, cudaStream_t stream) {
   const Ring ring = rows_ring(p.cols * T::kBytes + (kVec ? 0 : 30), p.residual != nullptr ? 2 : 1, BLOCKS);
   auto kernel = k_rms_forward_ring<T, kVec, TH, NV, BLOCKS>;
-  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring.smem));
+  static std::atomic<unsigned long long> done{0};  // ring.smem goes by the template's arguments
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), int(ring.smem), dev.device, &done);
   if (e != cudaSuccess) return e;
   const int64_t most = BLOCKS * dev.sms;
   return launch_kernel(kernel, dim3(unsigned(p.rows < most ? p.rows : most)), dim3(TH), ring.smem, stream, p, wdtype, ring, given_up);
@@ -649,7 +650,8 @@ cudaError_t backward_ring(const RmsBackwardParams& p, int wdtype, const DeviceIn
                           cudaStream_t stream) {
   const Ring ring = rows_ring(p.cols * T::kBytes + (kVec ? 0 : 30), p.dsum != nullptr ? 3 : 2, BLOCKS);
   auto kernel = k_rms_backward_ring<T, kVec, TH, NV, BLOCKS>;
-  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring.smem));
+  static std::atomic<unsigned long long> done{0};  // ring.smem goes by the template's arguments
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), int(ring.smem), dev.device, &done);
   if (e != cudaSuccess) return e;
   const int64_t most = BLOCKS * dev.sms, room = rms_partials(p.rows, p.cols);
   *blocks = unsigned(most < room ? most : room);
