@@ -159,7 +159,8 @@ template <class T, bool kRow, bool kCol>
 __global__ void __launch_bounds__(kThreads, T::kBytes == 4 ? 2 : (kRow && kCol ? 3 : 4)) k_fp4_quantize(const __grid_constant__ Fp4QuantizeParams p) {
   constexpr int W = Eight<T>::W;
   __shared__ float s_mult[128];  // by scale byte: a read of it for eight operations of arithmetic
-  __shared__ __align__(16) uint8_t s_scale[2][1024];
+  // scale bytes [direction][block][row], four rows to a word
+  __shared__ uint32_t s_scale[2][8][kTile / 4 + 4];
   __shared__ __align__(16) uint32_t s_col[kTile][17];
   grid_dependency_sync();
   const float G = *p.amax, S = fp4_tensor_scale(G);
@@ -217,11 +218,12 @@ __global__ void __launch_bounds__(kThreads, T::kBytes == 4 ? 2 : (kRow && kCol ?
     // blocks past the last column or row hold zeros: their scales are zero too, unless S is NaN
     const bool some = (col & ~int64_t(15)) < p.cols;
     uint8_t* q = p.q_r + row * p.ld_r + (col >> 1);
-    uint8_t* at = &s_scale[0][(c8 >> 6) * 512 + (r8 & 31) * 16 + (r8 >> 5) * 4 + ((c8 >> 4) & 3)];  // block c8 / 16 of row r8
+    uint32_t bytes[2] = {0, 0}, codes[8];
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       uint32_t s2 = fp4_block_scales(__uint_as_float(m[i]), __uint_as_float(m[i + 1]), S, tiny);
       if (bad) s2 = !some || i >= left ? 0 : (i + 1 >= left ? s2 & 0xffu : s2);
+      bytes[i >> 2] |= s2 << (16 * (i >> 1 & 1));
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t s = s2 >> (8 * h) & 0xffu;
@@ -229,20 +231,21 @@ __global__ void __launch_bounds__(kThreads, T::kBytes == 4 ? 2 : (kRow && kCol ?
         float y[8];
 #pragma unroll
         for (int k = 0; k < 8; k += 2) mul2_rn(v[i + h].get(k), v[i + h].get(k + 1), f, f, y[k], y[k + 1]);
-        const uint32_t codes = fp4_codes(y);
-        if ((lane & 1) == 0) at[16 * (i + h)] = uint8_t(s);
-        if (i + h < left) {
-          uint8_t* o = q + (i + h) * p.ld_r;
-          if (p.vec_r && n == 8) {
-            *reinterpret_cast<uint32_t*>(o) = codes;
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (2 * k < n) o[k] = uint8_t(codes >> (8 * k));
-          }
-        }
+        codes[i + h] = fp4_codes(y);
       }
     }
+    if (p.vec_r && n == 8 && left == 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t*>(q + i * p.ld_r) = codes[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (i < left && 2 * k < n) q[i * p.ld_r + k] = uint8_t(codes[i] >> (8 * k));
+      }
+    }
+    s_scale[0][c8 >> 4][(r8 >> 2) + (lane & 1)] = lane & 1 ? bytes[1] : bytes[0];  // block c8 / 16, four rows by each of its two threads
   }
   if constexpr (kCol) {
     uint32_t own[8], m[8];
@@ -250,12 +253,13 @@ __global__ void __launch_bounds__(kThreads, T::kBytes == 4 ? 2 : (kRow && kCol ?
     for (int k = 0; k < 8; ++k) own[k] = T::kBytes == 4 ? cm[k % W] : (cm[k >> 1] >> (16 * (k & 1))) & 0x7fffu;
     join8<T>(own, 16, m);
     const bool some = (row & ~int64_t(15)) < p.rows;
-    uint8_t* at = &s_scale[1][(warp >> 2) * 512 + (c8 & 31) * 16 + (c8 >> 5) * 4 + (warp & 3)];  // block `warp` of transposed row c8
+    uint32_t bytes[2] = {0, 0};
     uint32_t* turned = &s_col[c8][(r8 >> 3) ^ ((c8 >> 5) << 1)];
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
       uint32_t s2 = fp4_block_scales(__uint_as_float(m[k]), __uint_as_float(m[k + 1]), S, tiny);
       if (bad) s2 = !some || k >= n ? 0 : (k + 1 >= n ? s2 & 0xffu : s2);
+      bytes[k >> 2] |= s2 << (16 * (k >> 1 & 1));
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t s = s2 >> (8 * h) & 0xffu;
@@ -263,20 +267,32 @@ __global__ void __launch_bounds__(kThreads, T::kBytes == 4 ? 2 : (kRow && kCol ?
         float y[8];
 #pragma unroll
         for (int i = 0; i < 8; i += 2) mul2_rn(v[i].get(k + h), v[i + 1].get(k + h), f, f, y[i], y[i + 1]);
-        if (lane < 16) at[16 * (k + h)] = uint8_t(s);
         turned[17 * (k + h)] = fp4_codes(y);
       }
     }
+    s_scale[1][warp][(c8 >> 2) + (lane >> 4)] = lane & 16 ? bytes[1] : bytes[0];  // block `warp`, likewise
   }
   __syncthreads();
-  // the tile's scales: two tiles of the layout along k for each direction, if both are there
-  const int which = t >> 6, unit = t & 63;
+  // The tile's scales: two tiles of the layout along k for each direction, if both are there.  A thread turns four words, of four
+  // blocks, into the words of four rows.
+  const int which = t >> 6, tile = (t >> 5) & 1, quad = lane;
   if (t < 128) {
     const int64_t tile_cols = scale_tile_cols(((which == 0 ? p.cols : p.rows) + 15) / 16);
-    const int64_t r128 = which == 0 ? rb : cb, at = 2 * int64_t(which == 0 ? cb : rb) + (unit >> 5);
-    uint8_t* s = which == 0 ? p.s_r : p.s_c;
-    if ((which == 0 ? kRow : kCol) && at < tile_cols)
-      *reinterpret_cast<uint4*>(s + (r128 * tile_cols + at) * 512 + (unit & 31) * 16) = *reinterpret_cast<const uint4*>(&s_scale[which][unit * 16]);
+    const int64_t r128 = which == 0 ? rb : cb, at = 2 * int64_t(which == 0 ? cb : rb) + tile;
+    if ((which == 0 ? kRow : kCol) && at < tile_cols) {
+      uint32_t w[4], x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = s_scale[which][4 * tile + j][quad];
+      x[0] = __byte_perm(w[0], w[1], 0x5140);  // of rows 0 and 1, blocks 0 and 1
+      x[1] = __byte_perm(w[2], w[3], 0x5140);
+      x[2] = __byte_perm(w[0], w[1], 0x7362);
+      x[3] = __byte_perm(w[2], w[3], 0x7362);
+      uint8_t* s = (which == 0 ? p.s_r : p.s_c) + (r128 * tile_cols + at) * 512 + (quad & 7) * 64 + (quad >> 3) * 4;
+      *reinterpret_cast<uint32_t*>(s) = __byte_perm(x[0], x[1], 0x5410);
+      *reinterpret_cast<uint32_t*>(s + 16) = __byte_perm(x[0], x[1], 0x7632);
+      *reinterpret_cast<uint32_t*>(s + 32) = __byte_perm(x[2], x[3], 0x5410);
+      *reinterpret_cast<uint32_t*>(s + 48) = __byte_perm(x[2], x[3], 0x7632);
+    }
   }
   if constexpr (kCol) {
     store_turned(s_col, p.q_c, p.ld_c, p.vec_c, rb, cb, p.rows, p.cols);

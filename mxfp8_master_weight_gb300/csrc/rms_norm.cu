@@ -628,10 +628,12 @@ __global__ void __launch_bounds__(TH, BLOCKS)
   }
 }
 
-// Whether rows of `cols` columns go through a ring: enough of them for the prologue of a persistent block to pay, and rows
-// of 64 bytes or more.
+// Whether rows of `cols` columns go through a ring: enough of them for the prologue of a persistent block to pay, and long
+// enough that the rows of a block, one after another, keep memory busy (a warp per row / rings, BF16: forward 12867 x 71 8.4 /
+// 19.9 us, 16384 x 256 8.3 / 15.6, 16384 x 512 16.8 / 16.4, 16384 x 1024 35.8 / 28.3; backward 12.5 / 22.6, 16.6 / 16.8, 39.0 /
+// 19.3, 117 / 28).
 bool ring_rows(int64_t rows, int64_t cols, bool odd, const DeviceInfo& dev) {
-  return cols <= 8192 && (cols % 16 == 0 || cols >= 64) && rows >= (odd ? 12 : 4) * int64_t(dev.sms);
+  return cols > 256 && cols <= 8192 && rows >= (odd ? 12 : 4) * int64_t(dev.sms);
 }
 
 template <class T, bool kVec, int TH, int NV, int BLOCKS>
