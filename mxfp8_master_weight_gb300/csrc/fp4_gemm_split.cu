@@ -4,8 +4,12 @@
 // A few tokens against a weight read the whole weight for little arithmetic, so what counts is that every SM
 // has copies in flight from the start.  The weight's rows take the 128 lanes of the tile (the operands change places
 // when the output has few rows), the tokens its NT = 16 .. 128 columns, and 1 to 8 CTAs share a tile, each with its
-// part of k.  Their partial sums stay in shared memory, laid out as lines of the output; after a cluster barrier each
-// CTA adds its share of the lines over the cluster in rank order and writes it: no workspace, no atomics.
+// part of k.  After a cluster barrier each CTA adds its share of the tile's output lines over the cluster in rank order
+// and writes them: no workspace, no atomics.  Partial sums of up to 32 columns are sent to the CTA that adds them, into a
+// place of their own behind the stages, so that one barrier is between them and the output (1 x 4096 x 4096 4.2 us, with the
+// sums read over the cluster 4.9).  Of more columns they stay where they are made, over the stages, and are read by the CTA
+// that adds them: a place of their own would cost a stage (64 x 8192 x 8192 11.9 us, 12.2 with it, 12.7 sent over the stages
+// behind a barrier more).
 #include <cuda.h>
 
 #include "fp4.cuh"
@@ -22,6 +26,8 @@ constexpr int kMaxSplit = 8;
 constexpr int kMaxStages = 8;
 constexpr int kScales = 4 * kScaleTile;  // of 128 rows and a stage
 constexpr int kSmemBudget = 112 * 1024;  // two CTAs share an SM
+template <int NT>
+constexpr bool kApart = NT <= 32;        // sums are sent to a place of their own
 
 struct SplitParams {
   Fp4GemmParams f;    // a: the 128-row side, b: the NT-column side
@@ -63,6 +69,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp4_gemm_split(const __grid_con
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  if (kApart<NT> && q.split > 1) tc::cluster_started();
   tc::grid_wait_then_release();
   const uint32_t tmem = tmem_slot;
   int64_t tm, tn;
@@ -122,40 +129,127 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp4_gemm_split(const __grid_con
     }
   }
   __syncwarp();
-  // the sums, as lines of the output, over the stages' memory
-  float* part = reinterpret_cast<float*>(smem);
-  const bool writer = warp >= 2;
-  if (writer) {
-    const Fp4Factor factor(*q.f.a_amax, *q.f.b_amax);
-    const int row = 32 * (warp & 3) + (threadIdx.x & 31);
-    tc::mbar_wait(done, 0, gave_up);
-    tc::fence_after_sync();
-#pragma unroll
-    for (int c = 0; c < NT; c += 16) {
-      float v[16];
-      tc::tmem_load16(tmem + (uint32_t(32 * (warp & 3)) << 16) + c, v);
-      factor.apply(v);
+  if constexpr (kApart<NT>) {
+    if (q.split > 1) tc::cluster_all_started();
+    char* received = scales + q.stages * 2 * kScales;  // [rank][line of this CTA's][column]
+    // Lines of the output: 128 of NT sums, or with operands that changed places NT of 128; `per` of them are each CTA's.
+    const int width = q.swapped ? 128 : NT, per = (q.swapped ? NT : 128) / q.split, shift_per = 31 - __clz(per);
+    if (warp >= 2) {
+      const Fp4Factor factor(*q.f.a_amax, *q.f.b_amax);
+      const int row = 32 * (warp & 3) + (threadIdx.x & 31);
+      const uint32_t mine = tc::smem_addr(received) + 4 * per * width * rank;
+      tc::mbar_wait(done, 0, gave_up);
+      tc::fence_after_sync();
       if (q.swapped) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) part[(c + e) * 128 + row] = v[e];
-      } else {
+        for (int c = 0; c < NT; c += 16) {
+          float v[16];
+          tc::tmem_load16(tmem + (uint32_t(32 * (warp & 3)) << 16) + c, v);
+          factor.apply(v);
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<float4*>(part + row * NT + 4 * unit_at<NT>(row, (c + e) >> 2)) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          for (int e = 0; e < 16; ++e) {  // 16 lines, of one owner or several
+            const int owner = (c + e) >> shift_per;
+            tc::store_cluster(tc::in_cta(mine + 4 * ((c + e - owner * per) * 128 + row), owner), v[e]);
+          }
+        }
+      } else {
+        const int owner = row >> shift_per, line = row - owner * per;
+        const uint32_t to = tc::in_cta(mine + 4 * line * NT, owner);
+#pragma unroll
+        for (int c = 0; c < NT; c += 16) {
+          float v[16];
+          tc::tmem_load16(tmem + (uint32_t(32 * (warp & 3)) << 16) + c, v);
+          factor.apply(v);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) tc::store_cluster4(to + 16 * unit_at<NT>(line, (c + e) >> 2), v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
       }
     }
+    tc::fence_before_sync();
+    if (q.split > 1) tc::cluster_sync();
+    else __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_free<1>(tmem, kTmemCols);
+    if (warp >= 2) {
+      const int units = width / 4, shift = 31 - __clz(units);
+      const int64_t row0 = (q.swapped ? tn * NT : tm * 128) + per * int64_t(rank), col0 = q.swapped ? tm * 128 : tn * NT;
+      const int64_t rows = q.swapped ? p.n : p.m, cols = q.swapped ? p.m : p.n;
+      const float* sums = reinterpret_cast<const float*>(received);
+      for (int u = int(threadIdx.x) - 64; u < per * units; u += 128) {
+        const int line = u >> shift, c = (u & (units - 1)) * 4;
+        const int64_t r = row0 + line, j = col0 + c;
+        if (r >= rows || j >= cols) continue;
+        const int at = line * width + (q.swapped ? c : 4 * unit_at<NT>(line, c >> 2));
+        float4 v = *reinterpret_cast<const float4*>(sums + at);
+        for (int s = 1; s < q.split; ++s) {
+          const float4 x = *reinterpret_cast<const float4*>(sums + s * per * width + at);
+          v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+        }
+        float e[4] = {v.x, v.y, v.z, v.w};
+        const int n = cols - j < 4 ? int(cols - j) : 4;
+        if (p.addend != nullptr) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < n) e[k] += p.addend[r * p.ld_c + j + k];
+        }
+        if (p.out_f32) {
+          float* o = static_cast<float*>(p.out) + r * p.ld_o + j;
+          if (p.vec_out && n == 4) {
+            *reinterpret_cast<float4*>(o) = make_float4(e[0], e[1], e[2], e[3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < n) o[k] = e[k];
+          }
+        } else {
+          uint16_t* o = static_cast<uint16_t*>(p.out) + r * p.ld_o + j;
+          const uint2 w = make_uint2(bf16x2_rn(e[0], e[1]), bf16x2_rn(e[2], e[3]));
+          if (p.vec_out && n == 4) {
+            *reinterpret_cast<uint2*>(o) = w;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < n) o[k] = uint16_t((k < 2 ? w.x : w.y) >> (16 * (k & 1)));
+          }
+        }
+      }
+    }
+  } else {
+    // the sums, as lines of the output, over the stages' memory
+    float* part = reinterpret_cast<float*>(smem);
+    const bool writer = warp >= 2;
+    if (writer) {
+      const Fp4Factor factor(*q.f.a_amax, *q.f.b_amax);
+      const int row = 32 * (warp & 3) + (threadIdx.x & 31);
+      tc::mbar_wait(done, 0, gave_up);
+      tc::fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < NT; c += 16) {
+        float v[16];
+        tc::tmem_load16(tmem + (uint32_t(32 * (warp & 3)) << 16) + c, v);
+        factor.apply(v);
+        if (q.swapped) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) part[(c + e) * 128 + row] = v[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(part + row * NT + 4 * unit_at<NT>(row, (c + e) >> 2)) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+      }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_free<1>(tmem, kTmemCols);
+    if (q.split > 1) tc::cluster_sync();
+    if (writer) {
+      if (p.vec_out) write_lines<NT, 4, 16>(p, q.swapped, q.split, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
+      else write_lines<NT, 1, 32>(p, q.swapped, q.split, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
+    }
+    __syncwarp();
+    if (q.split > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums: a release, behind every load
   }
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  if (warp == 1) tc::tmem_free<1>(tmem, kTmemCols);
-  if (q.split > 1) tc::cluster_sync();
-  if (writer) {
-    if (p.vec_out) write_lines<NT, 4, 16>(p, q.swapped, q.split, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
-    else write_lines<NT, 1, 32>(p, q.swapped, q.split, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
-  }
-  __syncwarp();
-  if (q.split > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums: a release, behind every load
   if (threadIdx.x == 0 && s_gave_up != 0) tc::report_given_up(q.given_up);
 }
 
@@ -167,9 +261,11 @@ cudaError_t launch(const Fp4GemmParams& f, bool swapped, int split, unsigned* gi
   q.swapped = swapped;
   q.split = split;
   const GemmParams& g = f.g;
-  constexpr int stage = kBoxBytes + NT * 128 + 2 * kScales, fit = (kSmemBudget - 1024) / stage;
+  constexpr int stage = kBoxBytes + NT * 128 + 2 * kScales, sums = 128 * NT * 4, apart = kApart<NT> ? sums : 0,
+                fit = (kSmemBudget - 1024 - apart) / stage;
+  static_assert(fit >= 2 && fit * stage + apart >= sums, "stages");
   q.stages = fit < kMaxStages ? fit : kMaxStages;
-  const int smem = 1024 + q.stages * stage;
+  const int smem = 1024 + q.stages * stage + apart;
   cudaError_t e = operand_map(g.a, (g.k + 1) / 2, 128, &q.a, what);
   if (e == cudaSuccess) e = operand_map(g.b, (g.k + 1) / 2, NT, &q.b, what);
   if (e == cudaSuccess) e = scale_map(g.a, g.k, 1, &q.sa, what, 4);
