@@ -451,8 +451,9 @@ MXFP8_API int nvfp4_partial_cast(const mxfp8_tensor* input, const mxfp8_tensor* 
                        int64_t cols, int64_t start_offset, int64_t out_offset, void* stream);
 
 /*
- * Training operators around the MXFP8 weights: 8-bit activation checkpoints, the
- * block-scaled matrix product that reads them and the cast's outputs, and layer norm.
+ * Training operators around the MXFP8 and NVFP4 weights: 8-bit activation checkpoints, the
+ * block-scaled matrix product that reads them and the cast's outputs, layer norm, RMS norm in a
+ * residual stream, and 4-bit operands with their product.
  * (No counterpart in the source pages, which end at the weights.)
  *
  * Conventions of these entry points, besides the ones at the top of this file:
@@ -462,7 +463,7 @@ MXFP8_API int nvfp4_partial_cast(const mxfp8_tensor* input, const mxfp8_tensor* 
  *   mxfp8_swizzled_scales_size bytes, 16-byte aligned.
  * - Outputs must not overlap inputs, unless an argument says so.
  * - A call with no elements to write returns 0 and launches nothing.
- * - The first product or layer norm on a device loads its kernels and looks up a device address:
+ * - The first product, layer norm or RMS norm on a device loads its kernels and looks up a device address:
  *   make one such call before a stream capture.
  */
 
@@ -537,7 +538,7 @@ MXFP8_API int mxfp8_gemm(const mxfp8_tensor* a, const mxfp8_tensor* a_scale, con
 
 /*
  * Health of the operators' kernels: waits for `stream`, then returns 0, or MXFP8_ERR_CUDA when
- * a product or a layer norm on the current device gave up a wait on its own copies or
+ * a product, a layer norm or an RMS norm on the current device gave up a wait on its own copies or
  * tensor-core work (every wait inside these kernels ends after about two seconds; the outputs of such a call
  * are invalid).  Each such kernel is reported once, by the first call that sees it; those on other streams
  * than `stream` once they have completed.  Not for use during stream capture.

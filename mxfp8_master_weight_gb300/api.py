@@ -596,7 +596,7 @@ def prepare_gemm(a, a_scale, b, b_scale, addend, out, m, n, k, a_colwise=False, 
 
 
 def mxfp8_device_status(device=None, stream=None) -> None:
-    """Waits for the stream; raises when a product or a layer norm gave up a wait that no call has raised for."""
+    """Waits for the stream; raises when a product, a layer norm or an RMS norm gave up a wait that no call has raised for."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     _call("mxfp8_device_status", dev, _stream(torch.cuda.current_stream(dev) if stream is None else stream, None))
 

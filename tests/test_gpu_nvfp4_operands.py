@@ -108,9 +108,10 @@ def test_given_maximum(top):
     assert np.array_equal(s.cpu().numpy(), ref.tiles(fp4.scale_bytes(sv)))
 
 
-def test_not_finite():
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_not_finite(dtype):
     rows, cols = 48, 80
-    x = values(rows, cols, "f32")
+    x = values(rows, cols, dtype)
     x[3, 20], x[17, 5], x[40, 79] = float("nan"), float("inf"), -float("inf")
     top = torch.full((1,), float(x[torch.isfinite(x)].abs().max()), device="cuda")
     q, s = u8(rows, 48), scales(rows, cols)
