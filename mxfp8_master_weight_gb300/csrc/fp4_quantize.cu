@@ -10,7 +10,13 @@
 // All of them are streaming passes.  A block of the quantisation owns a tile of 128 x 128: thread (warp w, lane l)
 // has rows 16 w + 8 (l / 16) .. + 7 of columns 8 (l % 16) .. + 7, so a row's block of 16 is two lanes, a column's block
 // two halves of a warp, and both maxima are one shuffle away.  Column codes pass through shared memory to
-// leave as whole 64-byte pieces of the transposed rows.
+// leave as whole 64-byte pieces of the transposed rows; scale bytes gather in shared memory, four rows to a word, and are
+// turned into the layout's words there.
+//
+// Measured at 16384 x 6144 BF16 (floor at 6.8 TB/s): largest magnitude 33 us (30, HBM); both operands 69 us (46): bound by
+// instructions, about 1250 per thread of 64 values at 62 % of the issue slots, with three blocks per SM (80 registers); one
+// operand 43-45 us (38) with four; values 44 us (38).  16384 x 6143: both 83, values of rows that start anywhere 66.  160 x 96
+// F32: 2.4, 3.9 and 2.4 us.  A weight of 8192 x 8192 transposed 16 us, copied 11.
 #include "fp4.cuh"
 #include "linear.h"
 
@@ -303,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, T::kBytes == 4 ? 2 : (kRow && kCol ?
 // A thread restores blocks of 16, 8 bytes of codes and one scale each, a warp 512 columns of kRestoreRows rows, whose loads
 // are all under way at once.  Rows that start anywhere go through the warp's shared memory and out as 32-bit words aligned in
 // the output, neighbours across the lanes (BF16: a lone value at either end where the row starts between words).
-constexpr int kRestoreRows = 2;
+constexpr int kRestoreRows = 2;  // 16384 x 6144 BF16 43.9 us; one row 45.6, four 46.3
 template <class T>
 struct RestoreLine {
   static constexpr int kWords = 4 * T::kBytes;  // of a block's values

@@ -8,11 +8,17 @@
 // be folded into one word for a 4-bit quantisation that follows.  Everything between load and store is F32; s, y and ds
 // are rounded once, and y and its codes come from the unrounded s.
 //
-// A row belongs to one group of threads, which holds it in registers between the sum and the outputs: a warp for up to
-// 1024 columns, else a block; beyond 32768 columns (16384 backward) the row is read again, mostly from L2.  In the
-// backward pass a thread keeps the running dw of its columns in registers over all rows of its block; a block
+// Both directions read every value once.  Many rows of 257 to 8192 columns go through rings of bulk copies in persistent
+// blocks (below); others belong to one group of threads each, which holds the row in registers between the sum and the
+// outputs: a warp for up to 256 columns, else a block; beyond 32768 columns (16384 backward) the row is read again,
+// mostly from L2.  In the backward pass a thread keeps the running dw of its columns in registers over all rows of its block; a block
 // leaves one row of partial sums, and a second kernel adds the partial rows in their order, so the sums do not depend on
 // the run.
+//
+// Measured at 16384 x 6144 BF16 with the residual (floor at 6.8 TB/s): forward with codes 117 us (104), with values 137 (119);
+// backward with the stream's gradient 130 (119), without 97 (89): bound by HBM, the forward pass with codes also by
+// instructions (57 % of the issue slots at 16 warps per SM).  F32: 230 (193), 261 (237), 261 (237), 205 (178).  16384 x 6143 BF16,
+// an element per load and store: 229, 172, 146, 119.  1 x 4096: 3.5 with codes, 2.7 with values, 5.2 backward (two launches).
 #include <cfloat>
 #include <type_traits>
 
@@ -90,11 +96,11 @@ __device__ __forceinline__ void store_scale(const RmsForwardParams& p, int64_t r
 
 // Zeros in the scales of the rows behind the last one, up to a whole tile: by the threads of the last row.
 __device__ __forceinline__ void pad_scales(const RmsForwardParams& p, int t, int width) {
-  const int64_t tile_cols = scale_tile_cols((p.cols + kCkptBlock - 1) / kCkptBlock);
-  const int64_t end = (p.rows + 127) / 128 * 128;
-  for (int64_t i = t; i < (end - p.rows) * tile_cols; i += width) {
-    const int64_t row = p.rows + i / tile_cols, tile = i % tile_cols;
-    *reinterpret_cast<uint32_t*>(p.scale + scale_at(row, 4 * tile, tile_cols)) = 0u;
+  const uint32_t tile_cols = uint32_t(scale_tile_cols((p.cols + kCkptBlock - 1) / kCkptBlock));
+  const uint32_t words = uint32_t((p.rows + 127) / 128 * 128 - p.rows) * tile_cols;  // one per row and tile of four blocks
+  for (uint32_t i = uint32_t(t); i < words; i += uint32_t(width)) {
+    const uint32_t row = i / tile_cols, tile = i - row * tile_cols;
+    *reinterpret_cast<uint32_t*>(p.scale + scale_at(p.rows + row, 4 * int64_t(tile), tile_cols)) = 0u;
   }
 }
 
@@ -146,7 +152,7 @@ __device__ __forceinline__ void fold_amax(float* amax, uint32_t m) {
 
 // ------------------------------------------------------------------------------ forward
 template <class T, bool kBlock, bool kVec, int NV>
-__global__ void __launch_bounds__(kBlock ? (NV == 1 ? 512 : 1024) : 256)
+__global__ void __launch_bounds__(kBlock ? 1024 : 256)
     k_rms_forward(const __grid_constant__ RmsForwardParams p, int wbf16) {
   __shared__ float buf[2][32];
   grid_dependency_sync();
@@ -241,7 +247,7 @@ __global__ void __launch_bounds__(1024) k_rms_forward_long(const __grid_constant
 
 // ------------------------------------------------------------------------------ backward
 template <class T, bool kBlock, bool kVec, int NV>
-__global__ void __launch_bounds__(kBlock ? (NV == 1 ? 512 : 1024) : 256)
+__global__ void __launch_bounds__(kBlock ? 1024 : 256)
     k_rms_backward(const __grid_constant__ RmsBackwardParams p, int wbf16) {
   __shared__ float buf[2][32];
   extern __shared__ float s_acc[];  // warp per row: [8 warps][dw of the columns]
@@ -668,12 +674,12 @@ cudaError_t forward(const RmsForwardParams& p, int wdtype, const DeviceInfo& dev
   };
   auto direct = [&](auto vec) {
     constexpr bool kVec = decltype(vec)::value;
+    // a block per row of more than 256 columns: these rows are few (128 x 627 BF16 with a warp each 7.1 us, 64 x 1024 4.9; with a
+    // block 2.7 and 2.5)
     if (pieces <= 32) return launch(k_rms_forward<T, false, kVec, 1>, (p.rows + 7) / 8, 256);
-    if (pieces <= 64) return launch(k_rms_forward<T, false, kVec, 2>, (p.rows + 7) / 8, 256);
-    if (pieces <= 128) return launch(k_rms_forward<T, false, kVec, 4>, (p.rows + 7) / 8, 256);
     auto threads = [&](int nv) { return int(((pieces + nv - 1) / nv + 31) / 32 * 32); };
-    if (pieces <= 512) return launch(k_rms_forward<T, true, kVec, 1>, p.rows, threads(1));
-    if (pieces <= 1024) return launch(k_rms_forward<T, true, kVec, 2>, p.rows, threads(2));
+    if (pieces <= 1024) return launch(k_rms_forward<T, true, kVec, 1>, p.rows, threads(1));
+    if (pieces <= 2048) return launch(k_rms_forward<T, true, kVec, 2>, p.rows, threads(2));
     return launch(k_rms_forward<T, true, kVec, 4>, p.rows, threads(4));
   };
   const bool odd = p.cols % 8 != 0;
@@ -696,23 +702,25 @@ cudaError_t forward(const RmsForwardParams& p, int wdtype, const DeviceInfo& dev
   return launch_kernel(k_rms_forward_long<T>, dim3(unsigned(p.rows)), dim3(1024), 0, stream, p, wdtype);
 }
 
+// Blocks per SM without a ring: more rows of partial sums cost more than they save (600 x 1024 BF16 6.6 us, with four 8.1, with one
+// 7.5; 1800 x 511 8.8, 7.7, 14.0; 12867 x 71 8.7, 9.8, 11.6).
+constexpr int64_t kDirectBlocks = 2;
 template <class T>
-cudaError_t backward(const RmsBackwardParams& p, int wdtype, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t backward(RmsBackwardParams p, int wdtype, const DeviceInfo& dev, cudaStream_t stream) {
   const int64_t pieces = (p.cols + 7) / 8;
-  const bool block = pieces > 128;
+  const bool block = pieces > 32;
   const int64_t room = rms_partials(p.rows, p.cols), work = block ? p.rows : (p.rows + 7) / 8;
-  unsigned blocks = unsigned(work < room ? work : room);
+  const int64_t most = kDirectBlocks * dev.sms < room ? kDirectBlocks * dev.sms : room;
+  unsigned blocks = unsigned(work < most ? work : most);
+  if (blocks == 1) p.workspace = p.dweight;  // one row of partial sums is the sum: 1 x 4096 3.6 us, with a second launch 5.2
   auto run = [&](auto kernel, int threads, size_t smem) {
     return launch_kernel(kernel, dim3(blocks), dim3(threads), smem, stream, p, wdtype);
   };
   auto direct = [&](auto vec) {
     constexpr bool kVec = decltype(vec)::value;
     auto threads = [&](int nv) { return int(((pieces + nv - 1) / nv + 31) / 32 * 32); };
-    if (block) return pieces <= 512 ? run(k_rms_backward<T, true, kVec, 1>, threads(1), 0) : run(k_rms_backward<T, true, kVec, 2>, threads(2), 0);
-    const size_t smem = size_t(8) * size_t(p.cols) * 4;
-    if (pieces <= 32) return run(k_rms_backward<T, false, kVec, 1>, 256, smem);
-    if (pieces <= 64) return run(k_rms_backward<T, false, kVec, 2>, 256, smem);
-    return run(k_rms_backward<T, false, kVec, 4>, 256, smem);
+    if (block) return pieces <= 1024 ? run(k_rms_backward<T, true, kVec, 1>, threads(1), 0) : run(k_rms_backward<T, true, kVec, 2>, threads(2), 0);
+    return run(k_rms_backward<T, false, kVec, 1>, 256, size_t(8) * size_t(p.cols) * 4);
   };
   const bool odd = p.cols % 8 != 0;
   cudaError_t e;
@@ -733,7 +741,7 @@ cudaError_t backward(const RmsBackwardParams& p, int wdtype, const DeviceInfo& d
   } else {
     e = pieces > 2048 ? run(k_rms_backward_long<T>, 1024, 0) : odd ? direct(std::false_type{}) : direct(std::true_type{});
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || blocks == 1) return e;
   return launch_kernel(k_rms_partials, dim3(unsigned((p.cols + 31) / 32)), dim3(1024), 0, stream,
                        static_cast<const float*>(p.workspace), int(blocks), p.cols, p.dweight);
 }
