@@ -158,3 +158,15 @@ def test_concurrent_streams():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.parametrize("weights", KINDS)
+def test_no_tokens(weights):
+    """A step of no tokens leaves the weight's gradient as it is and sets the norm's to zero."""
+    layer, _, x, r, dy, ds = make(weights, 0, 64, 32)
+    layer.grad_weight.fill_(3.0)
+    layer.grad_norm_weight.fill_(3.0)
+    y, s = layer.forward(x, r)
+    assert y.shape == (0, 32) and s.shape == (0, 64) and layer.backward(dy, ds).shape == (0, 64)
+    assert bool((layer.grad_weight == 3.0).all()) and bool((layer.grad_norm_weight == 0).all())
+    layer.check()
