@@ -18,7 +18,7 @@
 // Measured at 16384 x 6144 BF16 with the residual (floor at 6.8 TB/s): forward with codes 117 us (104), with values 137 (119);
 // backward with the stream's gradient 130 (119), without 97 (89): bound by HBM, the forward pass with codes also by
 // instructions (57 % of the issue slots at 16 warps per SM).  F32: 230 (193), 261 (237), 261 (237), 205 (178).  16384 x 6143 BF16,
-// an element per load and store: 229, 172, 146, 119.  1 x 4096: 3.5 with codes, 2.7 with values, 5.2 backward (two launches).
+// an element per load and store: 193, 151, 146, 119.  1 x 4096: 3.5 with codes, 2.7 with values, 5.2 backward (two launches).
 #include <cfloat>
 #include <type_traits>
 
@@ -693,7 +693,8 @@ cudaError_t forward(const RmsForwardParams& p, int wdtype, const DeviceInfo& dev
       if (pieces <= 128) return forward_ring<T, kVec, 128, 1, 6>(p, wdtype, dev, given_up, stream);
       if (pieces <= 256) return forward_ring<T, kVec, 256, 1, 4>(p, wdtype, dev, given_up, stream);
       if (pieces <= 512) return forward_ring<T, kVec, 256, 2, kNarrow ? 3 : 2>(p, wdtype, dev, given_up, stream);
-      if (pieces <= 768) return forward_ring<T, kVec, 256, 3, 2>(p, wdtype, dev, given_up, stream);
+      // an element per load and store waits longer than it computes: 16384 x 6143 BF16 with codes 193 us, with two blocks 224
+      if (pieces <= 768) return forward_ring<T, kVec, 256, 3, kNarrow && !kVec ? 3 : 2>(p, wdtype, dev, given_up, stream);
       return forward_ring<T, kVec, 512, 2, 1>(p, wdtype, dev, given_up, stream);
     };
     return odd ? ring(std::false_type{}) : ring(std::true_type{});
