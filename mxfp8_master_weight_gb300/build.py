@@ -71,7 +71,7 @@ HOST_ONLY_UNITS = ("capi.cu", "noalloc.cu", "checks.h", "linear_capi.cu")
 # Sources of the training operators: none of the cast's kernels is made from them.
 OPERATOR_UNITS = ("linear.h", "checkpoint.cu", "gemm.cu", "gemm_impl.cuh", "gemm_maps.cu",
                   "gemm_maps.h", "gemm_pair.cu", "gemm_realign.cuh", "gemm_split.cu", "norm.cu", "tensor_core.cuh",
-                  "waits.h", "status.cu", "status.h", "gemm_lines.cuh", "norm_impl.cuh", "rms_norm.cu", "fp4.cuh",
+                  "waits.h", "status.cu", "status.h", "launch.h", "gemm_lines.cuh", "norm_impl.cuh", "rms_norm.cu", "fp4.cuh",
                   "fp4_quantize.cu", "fp4_gemm.h", "fp4_gemm.cu", "fp4_gemm_pair.cu", "fp4_gemm_split.cu")
 
 

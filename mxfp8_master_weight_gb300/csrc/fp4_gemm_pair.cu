@@ -25,7 +25,7 @@
 #include "fp4_gemm.h"
 #include "gemm_impl.cuh"
 #include "gemm_maps.h"
-#include "status.h"
+#include "launch.h"
 
 namespace mxfp8 {
 namespace {

@@ -20,7 +20,7 @@
 #include "fp4_gemm.h"
 #include "gemm_lines.cuh"
 #include "gemm_maps.h"
-#include "status.h"
+#include "launch.h"
 
 namespace mxfp8 {
 namespace {

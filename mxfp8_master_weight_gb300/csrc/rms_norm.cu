@@ -23,8 +23,8 @@
 #include <type_traits>
 
 #include "fp4.cuh"
+#include "launch.h"
 #include "norm_impl.cuh"
-#include "status.h"
 
 namespace mxfp8 {
 namespace {

@@ -21,15 +21,6 @@ struct Told {
   }
 };
 
-// Lets a kernel take `bytes` of dynamic shared memory, once per device: `done` has a bit for each that was told.
-inline cudaError_t allow_smem(const void* kernel, int bytes, int device, std::atomic<unsigned long long>* done) {
-  const unsigned long long bit = device < kMaxDevices ? 1ull << device : 0;
-  if (done->load() & bit) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done->fetch_or(bit);
-  return e;
-}
-
 // Where the current device's kernels count the waits that they gave up.
 cudaError_t given_up_address(int device, unsigned** out);
 // Waits for the stream; *count: those of the current device that no call has told before.
