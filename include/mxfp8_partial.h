@@ -700,7 +700,8 @@ MXFP8_API int nvfp4_lay_out(const mxfp8_tensor* codes, mxfp8_tensor* output, int
  * Matrix product of two NVFP4 operands, A of size m x k and B of size n x k,
  *   out[i][j] = fp32(1 / Sa) * fp32(1 / Sb) * sum_p A(i, p) * B(j, p) (+ addend[i][j]),
  * A(i, p) = decode(code) * decode(scale); likewise B.  Products are summed in F32 by the matrix instruction; the tensor
- * scales and the addend join in F32 and the result is rounded once.
+ * scales and the addend join in F32 and the result is rounded once.  Any finite maxima will do: where 1/Sa * 1/Sb is below 2^-100
+ * or past F32's range the sum is multiplied by one after the other, so that a sum of 0 is 0 and what fits F32 comes out finite.
  * a, a_scale, a_amax, b, b_scale, b_amax [in] the operands.  addend, out as for mxfp8_gemm; k may be 0.
  * With y = x W^T, W [outs][ins]: output y: a = x, b = W rowwise; input gradient dx = dy W: a = dy, b = W columnwise,
  * transposed by nvfp4_lay_out; weight gradient dW = dy^T x: a = dy columnwise, b = x columnwise.

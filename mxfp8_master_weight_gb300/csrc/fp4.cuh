@@ -77,14 +77,16 @@ __device__ __forceinline__ void fp4_values(uint32_t codes, uint32_t (&r)[4]) {
       : "r"(codes));
 }
 
-// What a product's sums are multiplied by: (1 / Sa) (1 / Sb), in two steps where it is too small to be one number.
+// What a product's sums are multiplied by: (1 / Sa) (1 / Sb), in two steps where that is too small or too large to be one number:
+// as an infinity it would make a NaN of a sum of 0.  The larger factor comes first: where the product overflows both are above 1,
+// so the first step overflows only where the result does; where it is too small, what the first step loses the second would too.
 struct Fp4Factor {
   float first, then;
   __device__ __forceinline__ Fp4Factor(float a_amax, float b_amax) {
     const float ra = __frcp_rn(fp4_tensor_scale(a_amax)), rb = __frcp_rn(fp4_tensor_scale(b_amax)), both = __fmul_rn(ra, rb);
-    const bool one = !(both < 0x1p-100f);
-    first = one ? both : ra;
-    then = one ? 1.0f : rb;
+    const bool one = !(both < 0x1p-100f) && !(both > FLT_MAX);  // a NaN is one number
+    first = one ? both : fmaxf(ra, rb);
+    then = one ? 1.0f : fminf(ra, rb);
   }
   template <int N>
   __device__ __forceinline__ void apply(float (&v)[N]) const {
