@@ -82,6 +82,7 @@ __device__ __forceinline__ void fp4_values(uint32_t codes, uint32_t (&r)[4]) {
 // so the first step overflows only where the result does; where it is too small, what the first step loses the second would too.
 struct Fp4Factor {
   float first, then;
+  __device__ __forceinline__ Fp4Factor() {}
   __device__ __forceinline__ Fp4Factor(float a_amax, float b_amax) {
     const float ra = __frcp_rn(fp4_tensor_scale(a_amax)), rb = __frcp_rn(fp4_tensor_scale(b_amax)), both = __fmul_rn(ra, rb);
     const bool one = !(both < 0x1p-100f) && !(both > FLT_MAX);  // a NaN is one number
@@ -90,11 +91,15 @@ struct Fp4Factor {
   }
   template <int N>
   __device__ __forceinline__ void apply(float (&v)[N]) const {
+    if constexpr (N == 1) {
+      v[0] = __fmul_rn(v[0], first);
+    } else {
 #pragma unroll
-    for (int k = 0; k < N; k += 2) mul2_rn(v[k], v[k + 1], first, first, v[k], v[k + 1]);
+      for (int k = 0; k < N; k += 2) mul2_rn(v[k], v[k + 1], first, first, v[k], v[k + 1]);
+    }
     if (then == 1.0f) return;
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] *= then;
+    for (int k = 0; k < N; ++k) v[k] = __fmul_rn(v[k], then);
   }
 };
 

@@ -133,13 +133,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp4_gemm_split(const __grid_con
     }
   }
   __syncwarp();
+  // The joined sums are multiplied by it, not each part of k: parts that cancel would leave what their roundings differ by,
+  // or overflow.
+  Fp4Factor factor;
+  if (warp >= 2) factor = Fp4Factor(*q.f.a_amax, *q.f.b_amax);
   if constexpr (kApart<NT>) {
     if (q.split > 1) tc::cluster_all_started();
     char* received = scales + q.stages * 2 * kScales;  // [rank][line of this CTA's][column]
     // Lines of the output: 128 of NT sums, or with operands that changed places NT of 128; `per` of them are each CTA's.
     const int width = q.swapped ? 128 : NT, per = (q.swapped ? NT : 128) / q.split, shift_per = 31 - __clz(per);
     if (warp >= 2) {
-      const Fp4Factor factor(*q.f.a_amax, *q.f.b_amax);
       const int row = 32 * (warp & 3) + (threadIdx.x & 31);
       const uint32_t mine = tc::smem_addr(received) + 4 * per * width * rank;
       tc::mbar_wait(done, 0, gave_up);
@@ -149,7 +152,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp4_gemm_split(const __grid_con
         for (int c = 0; c < NT; c += 16) {
           float v[16];
           tc::tmem_load16(tmem + (uint32_t(32 * (warp & 3)) << 16) + c, v);
-          factor.apply(v);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {  // 16 lines, of one owner or several
             const int owner = (c + e) >> shift_per;
@@ -163,7 +165,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp4_gemm_split(const __grid_con
         for (int c = 0; c < NT; c += 16) {
           float v[16];
           tc::tmem_load16(tmem + (uint32_t(32 * (warp & 3)) << 16) + c, v);
-          factor.apply(v);
 #pragma unroll
           for (int e = 0; e < 16; e += 4) tc::store_cluster4(to + 16 * unit_at<NT>(line, (c + e) >> 2), v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
@@ -190,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp4_gemm_split(const __grid_con
           v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
         }
         float e[4] = {v.x, v.y, v.z, v.w};
+        factor.apply(e);
         const int n = cols - j < 4 ? int(cols - j) : 4;
         if (p.addend != nullptr) {
 #pragma unroll
@@ -223,7 +225,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp4_gemm_split(const __grid_con
     float* part = reinterpret_cast<float*>(smem);
     const bool writer = warp >= 2;
     if (writer) {
-      const Fp4Factor factor(*q.f.a_amax, *q.f.b_amax);
       const int row = 32 * (warp & 3) + (threadIdx.x & 31);
       tc::mbar_wait(done, 0, gave_up);
       tc::fence_after_sync();
@@ -231,7 +232,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp4_gemm_split(const __grid_con
       for (int c = 0; c < NT; c += 16) {
         float v[16];
         tc::tmem_load16(tmem + (uint32_t(32 * (warp & 3)) << 16) + c, v);
-        factor.apply(v);
         if (q.swapped) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) part[(c + e) * 128 + row] = v[e];
@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp4_gemm_split(const __grid_con
     if (warp == 1) tc::tmem_free<1>(tmem, kTmemCols);
     if (q.split > 1) tc::cluster_sync();
     if (writer) {
-      if (p.vec_out) write_lines<NT, 4, 16>(p, q.swapped, q.split, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
-      else write_lines<NT, 1, 32>(p, q.swapped, q.split, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
+      if (p.vec_out) write_lines<NT, 4, 16>(p, factor, q.swapped, q.split, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
+      else write_lines<NT, 1, 32>(p, factor, q.swapped, q.split, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
     }
     __syncwarp();
     if (q.split > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums: a release, behind every load

@@ -10,12 +10,19 @@ namespace mxfp8 {
 template <int NT>
 __device__ __forceinline__ int unit_at(int r, int u) { return u ^ (NT >= 32 ? r & 7 : (r >> 1) & 3); }
 
-// Adds this CTA's share of the tile's output lines over the S CTAs of the cluster, in rank order, and writes
-// them.  The partial sums lie at `part` as lines of the output: 128 lines of NT sums, or with operands
-// that changed places NT lines of 128.  A thread keeps W neighbouring columns, four where the output takes
+// Of sums that are the result as they are.
+struct NoFactor {
+  template <int N>
+  __device__ __forceinline__ void apply(float (&)[N]) const {}
+};
+
+// Adds this CTA's share of the tile's output lines over the S CTAs of the cluster, in rank order, multiplies the joined sums
+// by `factor`, adds the addend and writes them.  The partial sums lie at `part` as lines of the output: 128 lines of NT sums,
+// or with operands that changed places NT lines of 128.  A thread keeps W neighbouring columns, four where the output takes
 // 16-byte stores, else one, and walks down the lines with kLoads loads under way at once.
-template <int NT, int W, int S, int kLoads>
-__device__ __forceinline__ void write_lines(const GemmParams& p, bool swapped, uint32_t part, int64_t i0, int64_t j0, int rank, int thread) {
+template <int NT, int W, int S, int kLoads, class F>
+__device__ __forceinline__ void write_lines(const GemmParams& p, const F& factor, bool swapped, uint32_t part, int64_t i0, int64_t j0,
+                                            int rank, int thread) {
   constexpr int kBatch = kLoads / S;
   const int width = swapped ? 128 : NT, shift = 31 - __clz(width / W), step = 128 >> shift;
   const int64_t row0 = swapped ? j0 : i0, rows = (swapped ? p.n : p.m) - row0;
@@ -64,13 +71,16 @@ __device__ __forceinline__ void write_lines(const GemmParams& p, bool swapped, u
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b, out += step * p.ld_o * size) {
+      float sum[W];
 #pragma unroll
       for (int e = 0; e < W; ++e) {
-        float sum = x[0][b][e];
+        sum[e] = x[0][b][e];
 #pragma unroll
-        for (int r = 1; r < S; ++r) sum += x[r][b][e];
-        v[b][e] += sum;
+        for (int r = 1; r < S; ++r) sum[e] += x[r][b][e];
       }
+      factor.apply(sum);
+#pragma unroll
+      for (int e = 0; e < W; ++e) v[b][e] += sum[e];
       if (line + step * b >= end) continue;
       if (W == 4 && cols >= W) {
         if (p.out_f32) *reinterpret_cast<float4*>(out) = make_float4(v[b][0], v[b][W > 1 ? 1 : 0], v[b][W > 2 ? 2 : 0], v[b][W > 3 ? 3 : 0]);
@@ -87,12 +97,13 @@ __device__ __forceinline__ void write_lines(const GemmParams& p, bool swapped, u
   }
 }
 
-template <int NT, int W, int kLoads>
-__device__ __forceinline__ void write_lines(const GemmParams& p, bool swapped, int split, uint32_t part, int64_t i0, int64_t j0, int rank, int thread) {
-  if (split == 1) write_lines<NT, W, 1, kLoads>(p, swapped, part, i0, j0, rank, thread);
-  else if (split == 2) write_lines<NT, W, 2, kLoads>(p, swapped, part, i0, j0, rank, thread);
-  else if (split == 4) write_lines<NT, W, 4, kLoads>(p, swapped, part, i0, j0, rank, thread);
-  else write_lines<NT, W, 8, kLoads>(p, swapped, part, i0, j0, rank, thread);
+template <int NT, int W, int kLoads, class F>
+__device__ __forceinline__ void write_lines(const GemmParams& p, const F& factor, bool swapped, int split, uint32_t part, int64_t i0,
+                                            int64_t j0, int rank, int thread) {
+  if (split == 1) write_lines<NT, W, 1, kLoads>(p, factor, swapped, part, i0, j0, rank, thread);
+  else if (split == 2) write_lines<NT, W, 2, kLoads>(p, factor, swapped, part, i0, j0, rank, thread);
+  else if (split == 4) write_lines<NT, W, 4, kLoads>(p, factor, swapped, part, i0, j0, rank, thread);
+  else write_lines<NT, W, 8, kLoads>(p, factor, swapped, part, i0, j0, rank, thread);
 }
 
 }  // namespace mxfp8

@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(kThreads + (kRealign ? 32 * kRealignWarps : 0)
   if (warp == 1) tc::tmem_free<1>(tmem, kTmemCols);
   if (q.split > 1) tc::cluster_sync();
   if (writer) {
-    if (p.vec_out) write_lines<NT, 4, kRealign ? 8 : 16>(p, q.swapped, q.split, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
-    else write_lines<NT, 1, kRealign ? 16 : 32>(p, q.swapped, q.split, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
+    if (p.vec_out) write_lines<NT, 4, kRealign ? 8 : 16>(p, NoFactor{}, q.swapped, q.split, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
+    else write_lines<NT, 1, kRealign ? 16 : 32>(p, NoFactor{}, q.swapped, q.split, tc::smem_addr(part), tm * 128, tn * NT, int(rank), threadIdx.x - 64);
   }
   __syncwarp();
   if (q.split > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums: a release, behind every load

@@ -95,3 +95,36 @@ def test_activation_with_a_huge_value():
     finite, past = np.abs(want) + tol < LARGEST, np.abs(want) - tol > LARGEST
     assert np.any(finite & (want != 0)) and np.all(np.abs(got - want)[finite] <= tol[finite])
     assert np.array_equal(got[past], np.copysign(np.inf, want[past]))
+
+
+# several CTAs add parts of k: of few columns, whose sums are sent; of 64 and of 128, whose sums are read
+SPLIT = [(1, 300, 8192), (30, 200, 4096), (200, 60, 8192), (256, 256, 8192)]
+
+
+@pytest.mark.parametrize("ta,tb,power", TOPS)
+@pytest.mark.parametrize("m,n,k", SPLIT)
+def test_product_split_over_k(m, n, k, ta, tb, power):
+    test_product(m, n, k, ta, tb, power)
+
+
+@pytest.mark.parametrize("ta,tb", [(1e24, 1e24), (3e21, 1e24), (1e30, 1e30)])
+@pytest.mark.parametrize("m,n,k", SPLIT + [(300, 300, 4096)])
+def test_parts_that_cancel(m, n, k, ta, tb):
+    """Sums over parts of k that leave F32 once the tensor scales are in them, and whose total does not: 0, or two terms."""
+    q, p = np.full((m, k), 6.0), np.full((n, k), 6.0)
+    q[:, k // 2:] = -6.0
+    q[1::2, 0] = 4.0
+    a, b = q * 2.0 ** -9, p * 2.0 ** -9
+    codes = lambda v: torch.from_numpy(fp4.pack(v, k // 2)).cuda()  # noqa: E731
+    scales = lambda r: torch.from_numpy(ref.tiles(np.full((r, k // 16), 0x01, np.uint8))).cuda()  # noqa: E731
+    ga, gb = (torch.tensor([t], dtype=torch.float32, device="cuda") for t in (ta, tb))
+    ra, rb = (float(np.float32(1) / fp4.tensor_scale(t)) for t in (ta, tb))
+    want = (a @ b.T) * ra * rb
+    out = torch.full((m, n), -3.0, device="cuda")
+    api.nvfp4_gemm(codes(q), scales(m), ga, codes(p), scales(n), gb, None, out, m, n, k)
+    api.mxfp8_device_status()
+    got = ref.as64(out)
+    assert not np.any(np.isnan(got))
+    fits = np.abs(want) < 3.38e38
+    assert np.all(np.abs(got - want)[fits] <= 2 * U * (1 + U) * np.abs(want)[fits])
+    assert np.array_equal(got[~fits], np.copysign(np.inf, want[~fits]))
