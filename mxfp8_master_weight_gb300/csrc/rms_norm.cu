@@ -749,9 +749,11 @@ cudaError_t backward(RmsBackwardParams p, int wdtype, const DeviceInfo& dev, cud
 
 }  // namespace
 
-// As many as the blocks of a ring that run at once on 152 SMs.
+// A row of partial sums per block of the backward pass: kDirectBlocks per SM, or those of its rings (of BF16, which has more),
+// of 152 SMs.  The pass takes no more blocks than that on any device.
 int64_t rms_partials(int64_t rows, int64_t cols) {
-  const int64_t most = cols <= 512 ? 3040 : (cols <= 1024 ? 1824 : (cols <= 2048 ? 912 : (cols <= 4096 ? 456 : 304)));
+  const int64_t per_sm = cols <= 256 ? kDirectBlocks : (cols <= 512 ? 12 : (cols <= 1024 ? 6 : (cols <= 2048 ? 4 : (cols <= 4096 ? 3 : kDirectBlocks))));
+  const int64_t most = 152 * per_sm;
   return rows < most ? rows : most;
 }
 
