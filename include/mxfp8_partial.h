@@ -590,7 +590,9 @@ MXFP8_API int64_t mxfp8_layer_norm_workspace_size(int64_t rows, int64_t cols);
 
 /*
  * RMS norm of each row of a residual stream: s = input + residual, rstd = 1 / sqrt(mean(s^2) + eps) over the row's cols
- * values, output = s * rstd * weight, in F32; every output is rounded once, from the unrounded s.
+ * values, output = s * rstd * weight, in F32; every output is rounded once, from the unrounded s.  The squares are summed in
+ * F32 too: a row whose sum of squares passes 3.4e38 (one value of 1.9e19) has rstd 0 and finite values of it give 0; with eps 0
+ * a row whose mean square rounds to 0 has an infinite rstd, and its zeros give NaN.
  *
  * input    [in]  F32 or BF16 matrix rows x cols;  residual [in] OPTIONAL, the same dtype: absent, s = input.
  * weight   [in]  F32 or BF16 vector of cols.

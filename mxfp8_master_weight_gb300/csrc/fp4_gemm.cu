@@ -20,10 +20,12 @@ cudaError_t launch_fp4_gemm(const Fp4GemmParams& p, const DeviceInfo& dev, cudaS
   const cudaError_t e = given_up_address(dev.device, &given_up);
   if (e != cudaSuccess) return e;
   // Split over k: outputs of at most 64 rows or columns (a tile of the pair kernel would stay mostly empty: split / pairs
-  // 1 x 4096 x 4096 4.2 / 8.8 us, 64 x 1024 x 4096 5.7 / 7.0, 64 x 8192 x 8192 11.9 / 12.5, 64 x 16384 x 4096 11.7 / 11.3), and tiles so
-  // few that four CTAs can share each, with a k that pays for joining the sums, the longer the more tiles there are
-  // (128 x 1024 x 8192 7.7 / 10.7, 256 x 256 x 8192 7.5 / 10.6, 512 x 1024 x 8192 9.1 / 10.8, 512 x 512 x 4096 7.6 / 7.4,
-  // 512 x 512 x 2048 7.1 / 5.6, 300 x 300 x 300 13.1 / 5.3).
+  // 1 x 4096 x 4096 4.2 / 8.8 us, 64 x 1024 x 4096 5.7 / 7.0, 64 x 8192 x 8192 11.9 / 12.5; 64 x 16384 x 4096 11.7 / 11.3 is the
+  // exception), and tiles so few that four CTAs can share each, with a k that pays for joining the sums, the longer the more
+  // tiles there are (128 x 1024 x 8192 7.7 / 10.7, 256 x 256 x 8192 7.0 / 10.6, 512 x 1024 x 8192 8.8 / 10.8, 512 x 512 x 4096
+  // 7.6 / 7.4, 512 x 512 x 2048 7.1 / 5.6, 300 x 300 x 300 13.1 / 5.3).  From 65 to 256 tokens against a large weight pairs take about
+  // the same time, however full their tiles are (of 8192 x 8192: 65 rows 12.6, 128 13.0, 256 13.2, 512 16.1; of 16384 x 4096: 11.5,
+  // 12.1, 12.5, 17.7; floors 5.8 to 9).
   const int64_t tiles = ((p.g.m + 127) / 128) * ((p.g.n + 127) / 128), stages = (p.g.k + kFp4StageK - 1) / kFp4StageK;
   const bool few = 4 * tiles <= dev.sms && stages >= 15 + tiles / 2;
   const bool split = p.g.k > 0 && (p.g.m <= 64 || p.g.n <= 64 || few);

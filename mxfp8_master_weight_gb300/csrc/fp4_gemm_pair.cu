@@ -14,8 +14,9 @@
 // Where the output's rows start and end on 16 bytes and nothing is added, the sums leave through TMA from 4 KB of shared memory
 // of each writer (16384 x 8192 x 256, all output, 44 us; by the writers' own stores 121); else by their own stores.
 //
-// What bounds it: shared memory.  Per stage an SM writes 38 KB to it and its matrix instructions read 38 KB, 596 cycles at 128 bytes
-// a cycle, where they would compute for 512; a stage takes 654 (with all loads but a quarter of the instructions 522, with the
+// What bounds it, with the instruction's form of 64 values of k (sm_103a has one of 96 as well, which is not used here): shared
+// memory.  Per stage an SM writes 38 KB (38912 bytes) to it and its matrix instructions read as much, 608 cycles at 128 bytes a
+// cycle, where they would compute for 512; a stage takes 654 (with all loads but a quarter of the instructions 522, with the
 // instructions alone 564).  Then the board's power: 8192^3 155 us (7.1 PFLOP/s), at 1.83 GHz; 165-172 in loops of a second.  4096^3:
 // 26.5 us on three sets of operands in turn, 27.5 with new inputs in every pass: 3.5 rounds of tiles of 5 us, about 1 us
 // between two tiles of a pair, start and end.  2048 x 8192 x 8192 with F32 output 51.6 us, 58.8 with an addend and new inputs.

@@ -17,8 +17,12 @@
 //
 // Measured at 16384 x 6144 BF16 with the residual (floor at 6.8 TB/s): forward with codes 117 us (104), with values 137 (119);
 // backward with the stream's gradient 130 (119), without 97 (89): bound by HBM, the forward pass with codes also by
-// instructions (57 % of the issue slots at 16 warps per SM).  F32: 230 (193), 261 (237), 261 (237), 205 (178).  16384 x 6143 BF16,
-// an element per load and store: 193, 151, 146, 119.  1 x 4096: 3.5 with codes, 2.7 with values, 5.2 backward (two launches).
+// instructions (57 % of the issue slots at 16 warps per SM).  F32: 230 (193), 261 (237), 261 (237), 205 (178).  16384 x 6143 BF16:
+// 193, 151, 146, 119; this path takes an element per load and store, also of codes, whose rows could take wider ones.
+// 1 x 4096: 3.0 with codes, 2.5 with values, 3.7 backward, each one launch.
+// Without a ring, where a block waits for its row and nothing is fetched behind it, codes / values / backward: 8192 x 12288 BF16 285,
+// 267, 289 (104, 119, 119), 8192 x 16384 318, 294, 315 (138, 158, 158), where the backward pass also spills (136 to 196 bytes at 64
+// registers); 16384 x 6144 in rows that start off 16 bytes 405, 564, 442, eight single elements per thread side by side.
 #include <cfloat>
 #include <type_traits>
 
