@@ -13,11 +13,11 @@
 // leave as whole 64-byte pieces of the transposed rows; scale bytes gather in shared memory, four rows to a word, and are
 // turned into the layout's words there.
 //
-// Measured at 16384 x 6144 BF16 (floor at 6.8 TB/s): largest magnitude 33 us (30, HBM); both operands 69 us (46): about
-// 1250 instructions per thread of 64 values, which three blocks per SM (80 registers, 48 bytes of them spilled) issue in 62 % of
-// the slots: neither the slots nor HBM are full.  One operand 42-45 us (38) with four; values 44 us (38).  16384 x 6143: both 83, values of rows that start anywhere 66.  F32 16384 x 6144: both 95 us (76),
-// one 81 (68); 16384 x 6143, an element per load, 133 and 105; 4096 x 4096 20 and 17.  160 x 96 F32: 2.4, 3.9 and 2.4 us.  A weight
-// of 8192 x 8192 transposed 16 us, copied 11.
+// Measured at 16384 x 6144 BF16 (floor at 6.8 TB/s): largest magnitude 33 us (30, HBM); both operands 69 us (46): about 1250
+// instructions per thread of 64 values, which three blocks per SM (80 registers, 48 bytes of them spilled) issue in 62 % of the
+// slots: neither the slots nor HBM are full.  One operand 42-45 us (38) with four; values 44 us (38).  16384 x 6143: both 83,
+// values of rows that start anywhere 66.  F32 16384 x 6144: both 95 us (76), one 81 (68); 16384 x 6143, an element per load, 133
+// and 105; 4096 x 4096 20 and 17.  160 x 96 F32: 2.4, 3.9 and 2.4 us.  A weight of 8192 x 8192 transposed 16 us, copied 11.
 #include "fp4.cuh"
 #include "linear.h"
 
